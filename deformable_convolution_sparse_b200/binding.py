@@ -22,7 +22,7 @@ STATUS_NAMES = {
     0: "DCNV4_OK", 1: "DCNV4_ERR_NULL", 2: "DCNV4_ERR_SHAPE", 3: "DCNV4_ERR_GROUPS",
     4: "DCNV4_ERR_DTYPE", 5: "DCNV4_ERR_ALIGN", 6: "DCNV4_ERR_ALIAS", 7: "DCNV4_ERR_SCALE",
     8: "DCNV4_ERR_TOO_LARGE", 9: "DCNV4_ERR_LAUNCH", 10: "DCNV4_ERR_CUDA", 11: "DCNV4_ERR_STAGING",
-    12: "DCNV4_ERR_FLAGS",
+    12: "DCNV4_ERR_FLAGS", 13: "DCNV4_ERR_WORKSPACE", 14: "DCNV4_ERR_COEFFICIENTS",
 }
 # variant switches of dcnv4_forward_ex
 FLAG_SOFTMAX, FLAG_REMOVE_CENTER, FLAG_CENTER_SCALE = 1, 2, 4
@@ -32,7 +32,9 @@ TORCH_DTYPE = {torch.float32: DCNV4_F32, torch.float16: DCNV4_F16, torch.bfloat1
 # every symbol include/dcnv4.h declares
 EXPORTS = ("dcnv4_output_shape", "dcnv4_validate", "dcnv4_validate_ex", "dcnv4_forward", "dcnv4_forward_ex",
            "dcnv4_forward_trace",
-           "dcnv4_backward", "dcnv4_backward_ex", "dcnv4_predictor", "dcnv4_sampling_index",
+           "dcnv4_backward", "dcnv4_backward_ex", "dcnv4_predictor", "dcnv4_predictor_backward",
+           "dcnv4_predictor_backward_workspace", "dcnv4_mx_quantize", "dcnv4_mx_dequantize", "dcnv4_predictor_mx",
+           "dcnv4_orthogonalize", "dcnv4_orthogonalize_workspace", "dcnv4_sampling_index",
            "dcnv4_forward_host", "dcnv4_forward_host_noalloc", "dcnv4_device_status", "dcnv4_selftest_wait_timeout",
            "dcnv4_probe_smem_gather", "dcnv4_probe_red_global", "dcnv4_probe_red_shared", "dcnv4_forward_plan", "dcnv4_strerror", "dcnv4_abi_version")
 DEVSTATUS_COPY_TIMEOUT, DEVSTATUS_SELFTEST_TIMEOUT = 1, 2
@@ -72,6 +74,21 @@ def load_library():
     lib.dcnv4_forward_ex.restype = i
     lib.dcnv4_predictor.argtypes = [p] * 4 + [i] * 4 + [ctypes.c_uint, i, p]
     lib.dcnv4_predictor.restype = i
+    z = ctypes.c_size_t
+    lib.dcnv4_predictor_backward.argtypes = [p] * 7 + [z] + [i] * 4 + [ctypes.c_uint, i, p]
+    lib.dcnv4_predictor_backward.restype = i
+    lib.dcnv4_predictor_backward_workspace.argtypes = [i] * 4 + [ctypes.c_uint, i, ctypes.POINTER(z)]
+    lib.dcnv4_predictor_backward_workspace.restype = i
+    lib.dcnv4_mx_quantize.argtypes = [p] * 3 + [i] * 3 + [p]
+    lib.dcnv4_mx_quantize.restype = i
+    lib.dcnv4_mx_dequantize.argtypes = [p] * 3 + [i] * 3 + [p]
+    lib.dcnv4_mx_dequantize.restype = i
+    lib.dcnv4_predictor_mx.argtypes = [p] * 5 + [i] * 4 + [ctypes.c_uint, i, p]
+    lib.dcnv4_predictor_mx.restype = i
+    lib.dcnv4_orthogonalize.argtypes = [p] * 3 + [z] + [i] * 4 + [f] * 4 + [i, p]
+    lib.dcnv4_orthogonalize.restype = i
+    lib.dcnv4_orthogonalize_workspace.argtypes = [i] * 4 + [ctypes.POINTER(z)]
+    lib.dcnv4_orthogonalize_workspace.restype = i
     lib.dcnv4_backward.argtypes = [p] * 5 + [i] * 9 + [f, i, p]
     lib.dcnv4_backward_ex.argtypes = [p] * 7 + [i] * 9 + [f, i, ctypes.c_uint, p]
     lib.dcnv4_backward_ex.restype = i
@@ -362,6 +379,198 @@ def predictor(y: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None, 
                                             _stream_handle(stream))
     if rc != DCNV4_OK:
         raise DCNv4Error(rc, "dcnv4_predictor")
+    return out
+
+
+def _output(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype, device) -> torch.Tensor:
+    """``t`` checked against shape, dtype and device, or a new tensor of them."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t
+
+
+def _launching_on(device, stream):
+    """Makes ``device`` current, and ``stream`` too when one is given: outputs and workspaces then come from
+    the memory pool of the stream whose kernels use them, which is what orders their reuse."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream)
+
+
+def _pixels(lead) -> int:
+    m = 1
+    for d in lead:
+        m *= d
+    return m
+
+
+def predictor_backward(y: torch.Tensor, weight: torch.Tensor, grad_offset_mask: torch.Tensor, G: int, K: int,
+                       remove_center: bool = False, with_bias: bool = True, grad_y: torch.Tensor | None = None,
+                       grad_weight: torch.Tensor | None = None, grad_bias: torch.Tensor | None = None, stream=None):
+    """Gradients of ``predictor`` through ``dcnv4_predictor_backward``.
+
+    y: [..., C]; weight: [3*G*P, C] in y's dtype; grad_offset_mask: fp32
+    [..., G, 3*P], as ``backward`` returns it. Returns (grad_y [..., C],
+    grad_weight [3*G*P, C], grad_bias [3*G*P]), all fp32; grad_bias is None
+    with ``with_bias=False``. The sums' order is fixed: equal calls give equal
+    bits. Asynchronous on ``stream`` (default: the current stream).
+    """
+    for t, name in ((y, "y"), (weight, "weight"), (grad_offset_mask, "grad_offset_mask")):
+        _check_tensor(t, name)
+    P = K * K - (1 if remove_center else 0)
+    C, lead, NO = y.shape[-1], tuple(y.shape[:-1]), 3 * G * P
+    if weight.dtype != y.dtype or weight.device != y.device or tuple(weight.shape) != (NO, C):
+        raise ValueError(f"weight must be [{NO}, {C}] in y's dtype and device")
+    if grad_offset_mask.dtype != torch.float32 or grad_offset_mask.device != y.device or \
+            tuple(grad_offset_mask.shape) != lead + (G, 3 * P):
+        raise ValueError(f"grad_offset_mask must be fp32 {lead + (G, 3 * P)} on y's device")
+    if not with_bias and grad_bias is not None:
+        raise ValueError("grad_bias is given but with_bias is False")
+    M, flags, dt = _pixels(lead), FLAG_REMOVE_CENTER if remove_center else 0, TORCH_DTYPE[y.dtype]
+    lib = load_library()
+    size = ctypes.c_size_t(0)
+    rc = lib.dcnv4_predictor_backward_workspace(M, C, G, K, flags, dt, ctypes.byref(size))
+    if rc != DCNV4_OK:
+        raise DCNv4Error(rc, "dcnv4_predictor_backward_workspace")
+    f32, dev = torch.float32, y.device
+    with _launching_on(dev, stream):
+        gy = _output(grad_y, "grad_y", tuple(y.shape), f32, dev)
+        gw = _output(grad_weight, "grad_weight", (NO, C), f32, dev)
+        gb = _output(grad_bias, "grad_bias", (NO,), f32, dev) if with_bias else None
+        ws = torch.empty(size.value, dtype=torch.uint8, device=dev)
+        rc = lib.dcnv4_predictor_backward(y.data_ptr(), weight.data_ptr(), grad_offset_mask.data_ptr(),
+                                          gy.data_ptr(), gw.data_ptr(), 0 if gb is None else gb.data_ptr(),
+                                          ws.data_ptr(), size.value, M, C, G, K, flags, dt, _stream_handle(stream))
+    if rc != DCNV4_OK:
+        raise DCNv4Error(rc, "dcnv4_predictor_backward")
+    return gy, gw, gb
+
+
+MX_BLOCK = 32  # channels that share a scale
+
+
+def _check_mx(codes: torch.Tensor, scales: torch.Tensor, lead: tuple, C: int, names=("codes", "scales")):
+    nb = (C + MX_BLOCK - 1) // MX_BLOCK
+    for t, name, shape in ((codes, names[0], lead + (nb * 16,)), (scales, names[1], lead + (nb,))):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.device.type != "cuda" or t.dtype != torch.uint8 or not t.is_contiguous() or tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor of shape {shape}")
+    if codes.device != scales.device:
+        raise ValueError(f"{names[0]} and {names[1]} must be on one device")
+
+
+def mx_quantize(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
+    """Microscaled 4-bit (MXFP4) form of x through ``dcnv4_mx_quantize``.
+
+    x: [..., C], fp32/fp16/bf16. Returns (codes uint8 [..., 16*nb], scales
+    uint8 [..., nb]), nb = ceil(C/32): per block of 32 channels two e2m1
+    elements a byte (the even one in the low half) and one power-of-two scale
+    byte (127: 1). Asynchronous on ``stream`` (default: the current stream).
+    """
+    _check_tensor(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must be [..., C]")
+    C, lead = x.shape[-1], tuple(x.shape[:-1])
+    nb = (C + MX_BLOCK - 1) // MX_BLOCK
+    with _launching_on(x.device, stream):
+        codes = _output(codes, "codes", lead + (nb * 16,), torch.uint8, x.device)
+        scales = _output(scales, "scales", lead + (nb,), torch.uint8, x.device)
+        rc = load_library().dcnv4_mx_quantize(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), _pixels(lead), C,
+                                              TORCH_DTYPE[x.dtype], _stream_handle(stream))
+    if rc != DCNV4_OK:
+        raise DCNv4Error(rc, "dcnv4_mx_quantize")
+    return codes, scales
+
+
+def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, C: int, dtype: torch.dtype = torch.float32,
+                  out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values [..., C] that ``mx_quantize``'s codes and scales stand for, in ``dtype``
+    (``dcnv4_mx_dequantize``)."""
+    if dtype not in TORCH_DTYPE:
+        raise TypeError(f"unsupported dtype {dtype}")
+    if C <= 0:
+        raise ValueError("C must be positive")
+    if not isinstance(scales, torch.Tensor) or scales.dim() < 1:
+        raise TypeError("scales must be a torch.Tensor [..., nb]")
+    lead = tuple(scales.shape[:-1])
+    _check_mx(codes, scales, lead, C)
+    with _launching_on(codes.device, stream):
+        out = _output(out, "out", lead + (C,), dtype, codes.device)
+        rc = load_library().dcnv4_mx_dequantize(codes.data_ptr(), scales.data_ptr(), out.data_ptr(), _pixels(lead), C,
+                                                TORCH_DTYPE[dtype], _stream_handle(stream))
+    if rc != DCNV4_OK:
+        raise DCNv4Error(rc, "dcnv4_mx_dequantize")
+    return out
+
+
+def predictor_mx(y: torch.Tensor, weight_codes: torch.Tensor, weight_scales: torch.Tensor, bias: torch.Tensor | None,
+                 G: int, K: int, remove_center: bool = False, out: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """``predictor`` with both operands in microscaled 4-bit form, through ``dcnv4_predictor_mx``.
+
+    y: [..., C], quantised on the way as ``mx_quantize`` would; weight_codes,
+    weight_scales: ``mx_quantize`` of the [3*G*P, C] weight; bias: fp32
+    [3*G*P] or None. Returns offset_mask [..., G, 3*P] in y's dtype.
+    """
+    _check_tensor(y, "y")
+    P = K * K - (1 if remove_center else 0)
+    C, lead, NO = y.shape[-1], tuple(y.shape[:-1]), 3 * G * P
+    _check_mx(weight_codes, weight_scales, (NO,), C, ("weight_codes", "weight_scales"))
+    if weight_codes.device != y.device:
+        raise ValueError("weight_codes must be on y's device")
+    bp = 0
+    if bias is not None:
+        _check_tensor(bias, "bias")
+        if bias.dtype != torch.float32 or tuple(bias.shape) != (NO,) or bias.device != y.device:
+            raise ValueError(f"bias must be fp32 [{NO}] on y's device")
+        bp = bias.data_ptr()
+    with _launching_on(y.device, stream):
+        out = _output(out, "out", lead + (G, 3 * P), y.dtype, y.device)
+        rc = load_library().dcnv4_predictor_mx(y.data_ptr(), weight_codes.data_ptr(), weight_scales.data_ptr(), bp,
+                                               out.data_ptr(), _pixels(lead), C, G, K,
+                                               FLAG_REMOVE_CENTER if remove_center else 0, TORCH_DTYPE[y.dtype],
+                                               _stream_handle(stream))
+    if rc != DCNV4_OK:
+        raise DCNv4Error(rc, "dcnv4_predictor_mx")
+    return out
+
+
+def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients: tuple = (3.4445, -4.7750, 2.0315),
+                  eps: float = 1e-7, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Newton-Schulz orthogonalisation of a stack of matrices through ``dcnv4_orthogonalize``.
+
+    x: [..., R, C]; each matrix X is divided by (its Frobenius norm + eps) and
+    then ``steps`` times replaced by a X + (b A + c A A) X with A = X X^T (on
+    the transpose when R > C): the update the Muon optimiser forms from a
+    weight's momentum. Returns the same shape and dtype; the iterates carry
+    fp32 precision whatever the dtype. Coefficients whose iteration could
+    leave its bounds are refused. Asynchronous on ``stream`` (default: the
+    current stream).
+    """
+    _check_tensor(x, "x")
+    if x.dim() < 2:
+        raise ValueError("x must be [..., R, C]")
+    a, b, c = (float(v) for v in coefficients)
+    R, C = x.shape[-2:]
+    B, dt = _pixels(x.shape[:-2]), TORCH_DTYPE[x.dtype]
+    lib = load_library()
+    size = ctypes.c_size_t(0)
+    rc = lib.dcnv4_orthogonalize_workspace(B, R, C, dt, ctypes.byref(size))
+    if rc != DCNV4_OK:
+        raise DCNv4Error(rc, "dcnv4_orthogonalize_workspace")
+    with _launching_on(x.device, stream):
+        out = _output(out, "out", tuple(x.shape), x.dtype, x.device)
+        ws = torch.empty(size.value, dtype=torch.uint8, device=x.device)
+        rc = lib.dcnv4_orthogonalize(x.data_ptr(), out.data_ptr(), ws.data_ptr(), size.value, B, R, C, int(steps),
+                                     a, b, c, float(eps), dt, _stream_handle(stream))
+    if rc != DCNV4_OK:
+        raise DCNv4Error(rc, "dcnv4_orthogonalize")
     return out
 
 

@@ -17,9 +17,11 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdcnv4.so")
-# the C ABI, and the forward of each storage type in a unit of its own (its kernel
-# specialisations compile in parallel with the others)
-SOURCES = [os.path.join(CSRC, f) for f in ("dcnv4.cu", "dcnv4_fwd_f32.cu", "dcnv4_fwd_f16.cu", "dcnv4_fwd_bf16.cu")]
+# the C ABI, the forward of each storage type in a unit of its own (its kernel
+# specialisations compile in parallel with the others), and the operators around the
+# predictor's weight
+SOURCES = [os.path.join(CSRC, f) for f in ("dcnv4.cu", "dcnv4_fwd_f32.cu", "dcnv4_fwd_f16.cu", "dcnv4_fwd_bf16.cu",
+                                           "dcnv4_mx.cu", "dcnv4_predictor_backward.cu", "dcnv4_orthogonalize.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h", ".inl"))] + \
     [os.path.join(INCLUDE, "dcnv4.h")]
 

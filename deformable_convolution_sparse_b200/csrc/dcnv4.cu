@@ -239,6 +239,10 @@ int points_per_unit(int K, unsigned flags) { return K * K - ((flags & DCNV4_FLAG
 
 }  // namespace
 
+namespace dcnv4_host {
+unsigned* device_status_word() { return status_word(); }
+}  // namespace dcnv4_host
+
 extern "C" {
 
 int dcnv4_abi_version(void) { return DCNV4_ABI_VERSION; }
@@ -258,6 +262,8 @@ const char* dcnv4_strerror(int status) {
         case DCNV4_ERR_CUDA: return "CUDA runtime call failed";
         case DCNV4_ERR_STAGING: return "one image does not fit half of the static staging area";
         case DCNV4_ERR_FLAGS: return "unknown variant flag";
+        case DCNV4_ERR_WORKSPACE: return "the workspace is too small";
+        case DCNV4_ERR_COEFFICIENTS: return "coefficients or eps not finite, eps not positive, or an unbounded iteration";
         default: return "unknown status";
     }
 }

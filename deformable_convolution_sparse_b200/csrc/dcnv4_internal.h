@@ -1,7 +1,10 @@
 // Interface between the translation units of libdcnv4.so (not installed, not
 // part of the C ABI): the forward of each storage type is compiled in its own
 // unit (dcnv4_fwd_f32.cu, dcnv4_fwd_f16.cu, dcnv4_fwd_bf16.cu) so that the
-// kernel specialisations build in parallel; dcnv4.cu holds the C ABI.
+// kernel specialisations build in parallel; dcnv4.cu holds the C ABI, apart
+// from the operators around the predictor's weight, whose entry points are in
+// units of their own (dcnv4_mx.cu, dcnv4_predictor_backward.cu,
+// dcnv4_orthogonalize.cu).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -30,5 +33,8 @@ int forward_bf16(const void* x, const void* om, void* out, const dcnv4::FwdParam
 int plan_f32(const dcnv4::FwdParams& p, int nsm, int* fields);
 int plan_f16(const dcnv4::FwdParams& p, int nsm, int* fields);
 int plan_bf16(const dcnv4::FwdParams& p, int nsm, int* fields);
+
+// Device address of the status word on the current device; NULL on failure.
+unsigned* device_status_word();
 
 }  // namespace dcnv4_host

@@ -101,7 +101,10 @@ typedef enum {
     DCNV4_ERR_CUDA = 10,     /* a CUDA runtime call other than a launch failed          */
     DCNV4_ERR_STAGING = 11,  /* dcnv4_forward_host_noalloc: one image does not fit its  */
                              /* half of the library's static staging area               */
-    DCNV4_ERR_FLAGS = 12     /* dcnv4_forward_ex: a flag bit that is not defined        */
+    DCNV4_ERR_FLAGS = 12,    /* dcnv4_forward_ex: a flag bit that is not defined        */
+    DCNV4_ERR_WORKSPACE = 13, /* the workspace is smaller than its _workspace call says  */
+    DCNV4_ERR_COEFFICIENTS = 14 /* dcnv4_orthogonalize: coefficients or eps not finite,  */
+                             /* eps <= 0, or an iteration that leaves its bounds         */
 } dcnv4_status_t;
 
 /* Variant switches of dcnv4_forward_ex / dcnv4_validate_ex (bitwise or).
@@ -238,6 +241,105 @@ DCNV4_API int dcnv4_backward(const void *x, const void *offset_mask, const void 
  * Asynchronous on `stream`; nothing is launched when M == 0. */
 DCNV4_API int dcnv4_predictor(const void *y, const void *weight, const float *bias, void *offset_mask,
                     int M, int C, int G, int K, unsigned int flags, int dtype, void *stream);
+
+/* Gradients of dcnv4_predictor, for training the projection: with params and
+ * records as there and gp[m, o] = dL/d(record entry of params[m, o]),
+ *   grad_y[m, c]      = sum_o gp[m, o] * weight[o, c]
+ *   grad_weight[o, c] = sum_m gp[m, o] * y[m, c]
+ *   grad_bias[o]      = sum_m gp[m, o].
+ * ("不只是卷积的平替" (jsqmd.com), section 4, fine-tunes through the block; the
+ * pages give no gradient: these are the derivatives of the projection.)
+ * y: device, dtype, [M, C]; weight: device, dtype, [NO, C]; grad_offset_mask:
+ * device fp32 [M, G, 3P], the records' gradients as dcnv4_backward writes them;
+ * grad_y: device fp32 [M, C]; grad_weight: device fp32 [NO, C]; grad_bias:
+ * device fp32 [NO], or NULL when it is not wanted. All three are fully
+ * overwritten (M == 0: the weight's and the bias's with zeros). flags as
+ * dcnv4_predictor. Sums are fp32 and their order is fixed by the sizes: the
+ * same bits in every run. workspace: device, 16-byte aligned, at least
+ * dcnv4_predictor_backward_workspace's bytes; its contents before and after
+ * do not matter, and calls whose work overlaps on the GPU need one each.
+ * Errors: those of dcnv4_predictor, DCNV4_ERR_WORKSPACE, and DCNV4_ERR_ALIAS
+ * when an output or the workspace overlaps an input or another output.
+ * Asynchronous on `stream`. */
+DCNV4_API int dcnv4_predictor_backward(const void *y, const void *weight, const float *grad_offset_mask,
+                                       float *grad_y, float *grad_weight, float *grad_bias,
+                                       void *workspace, size_t workspace_bytes,
+                                       int M, int C, int G, int K, unsigned int flags, int dtype, void *stream);
+
+/* Bytes of workspace that dcnv4_predictor_backward needs for these sizes (a
+ * function of the arguments alone). Host only. */
+DCNV4_API int dcnv4_predictor_backward_workspace(int M, int C, int G, int K, unsigned int flags, int dtype,
+                                                 size_t *bytes);
+
+/* Microscaled 4-bit floating point (OCP Microscaling Formats v1.0, MXFP4):
+ * each row of x [M, C] is cut into nb = ceil(C / 32) blocks of 32 channels (the
+ * last one padded with zeros). A block holds one scale byte s, worth
+ * 2^(s - 127), and 32 e2m1 elements (sign and 0, 0.5, 1, 1.5, 2, 3, 4 or 6).
+ * With amax the block's largest magnitude,
+ *   s - 127 = max(floor(log2(amax)) - 2, -127)   (amax == 0: s = 0)
+ * and each element is x / 2^(s - 127) rounded to the nearest value, ties to
+ * the even code, magnitudes above 6 to 6. A block with a NaN or an infinity
+ * gets s = 255 (all of it reads back as NaN) and element codes 0.
+ * x: device, dtype; codes: device, 16-byte aligned, [M, nb, 16] bytes, the
+ * block's element 2i in the low half of byte i and 2i + 1 in the high half;
+ * scales: device bytes [M, nb]. codes and scales are fully overwritten.
+ * Errors: DCNV4_ERR_SHAPE (M < 0, C <= 0), DCNV4_ERR_DTYPE,
+ * DCNV4_ERR_TOO_LARGE (M * nb * 32 >= 2^31), DCNV4_ERR_NULL, DCNV4_ERR_ALIGN,
+ * DCNV4_ERR_ALIAS (buffers overlap). Asynchronous on `stream`; nothing is
+ * launched when M == 0. */
+DCNV4_API int dcnv4_mx_quantize(const void *x, uint8_t *codes, uint8_t *scales, int M, int C, int dtype,
+                                void *stream);
+
+/* The inverse: x[m, c] = element * 2^(s - 127), rounded once to dtype (exact
+ * in fp32 for every scale dcnv4_mx_quantize writes). codes, scales: read only,
+ * as above; x: fully overwritten. Errors as dcnv4_mx_quantize. */
+DCNV4_API int dcnv4_mx_dequantize(const uint8_t *codes, const uint8_t *scales, void *x, int M, int C, int dtype,
+                                  void *stream);
+
+/* dcnv4_predictor with both operands in the format above, for serving: y is
+ * quantised on the way, each row's blocks of 32 channels as dcnv4_mx_quantize
+ * would, and weight_codes [NO, nb, 16] / weight_scales [NO, nb] are a
+ * [NO, C] weight quantised once by dcnv4_mx_quantize:
+ *   params[m, o] = bias[o] + sum_c weight'[o, c] * y'[m, c]
+ * with y', weight' the values the codes stand for (products exact, sums fp32,
+ * one rounding to dtype), packed into records as dcnv4_predictor does. y,
+ * bias, offset_mask, M, C, G, K, flags and dtype (the type of y and
+ * offset_mask) as there; C need not be a multiple of 32. A NaN or an infinity
+ * in a block of y makes that pixel's records NaN; weight scale bytes are those
+ * of dcnv4_mx_quantize (0..252 and 255). Errors as dcnv4_predictor, with
+ * weight_codes 16-byte aligned. Asynchronous on `stream`; nothing is launched
+ * when M == 0. */
+DCNV4_API int dcnv4_predictor_mx(const void *y, const uint8_t *weight_codes, const uint8_t *weight_scales,
+                                 const float *bias, void *offset_mask,
+                                 int M, int C, int G, int K, unsigned int flags, int dtype, void *stream);
+
+/* Orthogonalises a stack of weight updates by Newton-Schulz products, the step
+ * that the Muon optimiser applies to a weight's momentum: each matrix
+ * X [R, C] of x [B, R, C] is divided by (its Frobenius norm + eps), then
+ * `steps` times
+ *   X <- a X + (b A + c A A) X,  A = X X^T
+ * (on X^T when R > C), which keeps its singular vectors and moves every
+ * singular value s to a s + b s^3 + c s^5. x: device, dtype, read only; out:
+ * device, dtype, [B, R, C], fully overwritten. Sums and the iterates carry
+ * fp32 precision whatever dtype is; the result is rounded once. A matrix of zeros
+ * gives zeros; a NaN or an infinity makes its matrix NaN. steps: 0..64 (0:
+ * only the division). Refused with DCNV4_ERR_COEFFICIENTS: coefficients or
+ * eps that are not finite, eps <= 0, and coefficients that within `steps`
+ * steps could lift a singular value of [0, 1] above 4 or the factor
+ * |a + b s^2 + c s^4| above 64. workspace: device, 256-byte aligned, at least
+ * dcnv4_orthogonalize_workspace's bytes; its contents before and after do not
+ * matter, and calls whose work overlaps on the GPU need one each. Other
+ * errors: DCNV4_ERR_SHAPE (B < 0, R or C <= 0, steps out of range),
+ * DCNV4_ERR_DTYPE, DCNV4_ERR_TOO_LARGE (B*R*C >= 2^31), DCNV4_ERR_NULL,
+ * DCNV4_ERR_ALIGN, DCNV4_ERR_WORKSPACE, DCNV4_ERR_ALIAS (out, x and workspace
+ * overlap). Asynchronous on `stream`; nothing is launched when B == 0. */
+DCNV4_API int dcnv4_orthogonalize(const void *x, void *out, void *workspace, size_t workspace_bytes,
+                                  int B, int R, int C, int steps, float a, float b, float c, float eps,
+                                  int dtype, void *stream);
+
+/* Bytes of workspace that dcnv4_orthogonalize needs for these sizes (a
+ * function of the arguments alone). Host only. */
+DCNV4_API int dcnv4_orthogonalize_workspace(int B, int R, int C, int dtype, size_t *bytes);
 
 /* dcnv4_backward for the variant flags of dcnv4_forward_ex (flags == 0 is
  * dcnv4_backward). With m' the masks the aggregation used (softmax-normalised
