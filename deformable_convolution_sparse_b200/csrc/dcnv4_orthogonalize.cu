@@ -27,8 +27,8 @@ constexpr int kMaxSteps = 64;
 int check_stack(int B, int R, int C, int dtype) {
     if (B < 0 || R <= 0 || C <= 0) return DCNV4_ERR_SHAPE;
     if (!elem_size(dtype)) return DCNV4_ERR_DTYPE;
-    // |sizes| < 2^31 each, so the first product fits 62 bits
-    const long long rc = static_cast<long long>(R) * C;
+    // rows of the planes are padded to 8 elements; sizes are below 2^31, so the products fit 63 bits
+    const long long rc = static_cast<long long>(std::min(R, C)) * ((static_cast<long long>(std::max(R, C)) + 7) / 8 * 8);
     if (rc >= kLimit || (B > 0 && rc > (kLimit - 1) / B)) return DCNV4_ERR_TOO_LARGE;
     return DCNV4_OK;
 }
@@ -51,14 +51,19 @@ double poly_bound(double a, double b, double c, double r) {
 }
 
 // The iteration stays bounded: singular values start in [0, 1]; no step may
-// lift one above 4, nor the factor a + b s^2 + c s^4 above 64.
-bool coefficients_bounded(double a, double b, double c, int steps) {
+// lift one above 4, nor the factor |a + b s^2 + c s^4| above 64. down[k]: bits
+// by which the steps before k can have grown a matrix (the factor's bound,
+// rounded up to a power of two).
+bool coefficients_bounded(double a, double b, double c, int steps, int* down) {
     double r = 1.0;
+    down[0] = 0;
     for (int k = 0; k < steps; ++k) {
-        if (std::fabs(a) + std::fabs(b) * r * r + std::fabs(c) * r * r * r * r > 4096.0) return false;
         double q = std::max(std::fabs(a), std::fabs(a + b * r * r + c * r * r * r * r));
         if (c != 0.0 && -b / (2.0 * c) > 0.0 && -b / (2.0 * c) < r * r) q = std::max(q, std::fabs(a - b * b / (4.0 * c)));
         if (!(q <= 64.0)) return false;
+        int bits = 0;
+        while ((1 << bits) < q) ++bits;
+        down[k + 1] = down[k] + bits;
         r = poly_bound(a, b, c, r);
         if (!(r <= 4.0)) return false;
     }
@@ -69,52 +74,91 @@ dcnv4::OrthoParams make_params(int B, int R, int C) {
     dcnv4::OrthoParams p{};
     p.B = B; p.R = R; p.C = C;
     p.n = std::min(R, C); p.m = std::max(R, C); p.transposed = R > C ? 1 : 0;
+    p.np = (p.n + 7) / 8 * 8;
+    p.mp = (p.m + 7) / 8 * 8;
     // one chunk per 4096 elements, at most 64
     p.chunks = static_cast<int>(std::min<long long>(64, (static_cast<long long>(R) * C + 4095) / 4096));
     return p;
 }
 
+// Workspace: the sums of squares, the lifts, then the fp16 plane pairs of X (two, in turn), A and P.
 struct Layout {
-    size_t part, x0, x1, g, q, bytes;
+    size_t lift, x0, x1, a, p, bytes;
 };
 Layout layout(const dcnv4::OrthoParams& p) {
     Layout l{};
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-    const size_t xb = up(static_cast<size_t>(p.B) * p.n * p.m * 4), gb = up(static_cast<size_t>(p.B) * p.n * p.n * 4);
-    l.part = 0;
-    l.x0 = up(static_cast<size_t>(p.B) * p.chunks * 8);
+    const size_t xb = up(static_cast<size_t>(p.B) * p.n * p.mp * 4), ab = up(static_cast<size_t>(p.B) * p.n * p.np * 4);
+    l.lift = up(static_cast<size_t>(p.B) * p.chunks * 8);
+    l.x0 = l.lift + up(static_cast<size_t>(p.B) * 4);
     l.x1 = l.x0 + xb;
-    l.g = l.x1 + xb;
-    l.q = l.g + gb;
-    l.bytes = l.q + gb;
+    l.a = l.x1 + xb;
+    l.p = l.a + ab;
+    l.bytes = l.p + ab;
     return l;
 }
 
+// Map of a plane pair [2 * B][rows][cols] with boxes of 64 columns x `box` rows, 128-byte swizzle.
+bool plane_map(CUtensorMap* map, void* base, int cols, int pitch, int rows, int planes, int box) {
+    auto encode = tensor_map_encoder();
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(planes)};
+    const cuuint64_t str[2] = {static_cast<cuuint64_t>(pitch) * 2, static_cast<cuuint64_t>(pitch) * rows * 2};
+    const cuuint32_t bx[3] = {64u, static_cast<cuuint32_t>(box), 1u}, es[3] = {1u, 1u, 1u};
+    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, str, bx, es,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE, typename T>
+int product(const CUtensorMap& l, const CUtensorMap& r, const CUtensorMap& o, T* out, int cols, int k,
+            const int* down, const dcnv4::OrthoParams& p, cudaStream_t s) {
+    auto kern = dcnv4::ortho_product_kernel<MODE, T>;
+    if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(dcnv4::kOrthoSmem)) != cudaSuccess)
+        return DCNV4_ERR_LAUNCH;
+    dcnv4::OrthoTile g{};
+    g.tiles_i = (p.n + 127) / 128;
+    g.tiles_j = (cols + 63) / 64;
+    g.kblocks = (k + 63) / 64;
+    g.down = down[0];
+    g.down_next = down[1];
+    return launch_chained(kern, dim3(static_cast<unsigned>(p.B) * g.tiles_i * g.tiles_j), 192, dcnv4::kOrthoSmem, s, l, r,
+                          o, out, g, p);
+}
+
 template <typename T>
-int launch(const void* x, void* out, unsigned char* ws, int steps, const dcnv4::OrthoParams& p, cudaStream_t s) {
+int launch(const void* x, void* out, unsigned char* ws, int steps, const int* down, dcnv4::OrthoParams p,
+           cudaStream_t s) {
     const Layout l = layout(p);
-    double* part = reinterpret_cast<double*>(ws + l.part);
-    float *x0 = reinterpret_cast<float*>(ws + l.x0), *x1 = reinterpret_cast<float*>(ws + l.x1);
-    float *g = reinterpret_cast<float*>(ws + l.g), *q = reinterpret_cast<float*>(ws + l.q);
-    constexpr int t = dcnv4::kSimtTile;
-    const unsigned nt = static_cast<unsigned>((p.n + t - 1) / t), mt = static_cast<unsigned>((p.m + t - 1) / t);
-    const unsigned z = static_cast<unsigned>(std::min(p.B, 65535));
-    const unsigned flat = static_cast<unsigned>(p.B) * static_cast<unsigned>(p.chunks);
-    int rc = launch_chained(dcnv4::ortho_sumsq_kernel<T>, dim3(flat), 256, 0, s, static_cast<const T*>(x), part, p);
+    p.lift = reinterpret_cast<int*>(ws + l.lift);
+    double* part = reinterpret_cast<double*>(ws);
+    __half *x0 = reinterpret_cast<__half*>(ws + l.x0), *x1 = reinterpret_cast<__half*>(ws + l.x1);
+    __half *a = reinterpret_cast<__half*>(ws + l.a), *q = reinterpret_cast<__half*>(ws + l.p);
+    // maps of 128-row boxes (left operands, results) and of 64-row boxes (right operands)
+    CUtensorMap xm[2], xr[2], am, ar, qm;
+    const int planes = 2 * p.B;
+    for (int i = 0; i < 2; ++i)
+        if (!plane_map(&xm[i], i ? x1 : x0, p.m, p.mp, p.n, planes, 128) ||
+            !plane_map(&xr[i], i ? x1 : x0, p.m, p.mp, p.n, planes, 64))
+            return DCNV4_ERR_CUDA;
+    if (!plane_map(&am, a, p.n, p.np, p.n, planes, 128) || !plane_map(&ar, a, p.n, p.np, p.n, planes, 64) ||
+        !plane_map(&qm, q, p.n, p.np, p.n, planes, 128))
+        return DCNV4_ERR_CUDA;
+    int rc = launch_chained(dcnv4::ortho_sumsq_kernel<T>, dim3(static_cast<unsigned>(p.B) * p.chunks), 256, 0, s,
+                            static_cast<const T*>(x), part, p);
     if (rc) return rc;
-    rc = launch_chained(dcnv4::ortho_start_kernel<T>, dim3(flat), 256, 0, s, static_cast<const T*>(x),
-                        static_cast<const double*>(part), x0, p);
-    for (int k = 0; k < steps && !rc; ++k) {
-        rc = launch_chained(dcnv4::ortho_gram_kernel, dim3(nt, nt, z), 256, 0, s, static_cast<const float*>(x0), g, p);
-        if (!rc) rc = launch_chained(dcnv4::ortho_poly_kernel, dim3(nt, nt, z), 256, 0, s, static_cast<const float*>(g), q, p);
-        if (!rc)
-            rc = launch_chained(dcnv4::ortho_apply_kernel, dim3(nt, mt, z), 256, 0, s, static_cast<const float*>(q),
-                                static_cast<const float*>(x0), x1, p);
-        std::swap(x0, x1);
+    T* o = static_cast<T*>(out);
+    const unsigned st = static_cast<unsigned>(p.B) * ((p.R + 63) / 64) * ((p.C + 63) / 64);
+    rc = launch_chained(dcnv4::ortho_start_kernel<T>, dim3(st), 256, 0, s, static_cast<const T*>(x),
+                        static_cast<const double*>(part), x0, steps == 0 ? o : static_cast<T*>(nullptr), p);
+    for (int k = 0, cur = 0; k < steps && !rc; ++k, cur ^= 1) {
+        rc = product<dcnv4::kGram, float>(xm[cur], xr[cur], am, nullptr, p.n, p.m, down + k, p, s);
+        if (!rc) rc = product<dcnv4::kPoly, float>(am, ar, qm, nullptr, p.n, p.n, down + k, p, s);
+        if (rc) break;
+        if (k + 1 < steps) rc = product<dcnv4::kApply, float>(qm, xr[cur], xm[cur ^ 1], nullptr, p.m, p.n, down + k, p, s);
+        else rc = product<dcnv4::kLast, T>(qm, xr[cur], xm[cur ^ 1], o, p.m, p.n, down + k, p, s);
     }
-    if (rc) return rc;
-    return launch_chained(dcnv4::ortho_finish_kernel<T>, dim3(flat), 256, 0, s, static_cast<const float*>(x0),
-                          static_cast<T*>(out), p);
+    return rc;
 }
 
 }  // namespace
@@ -134,8 +178,9 @@ int dcnv4_orthogonalize(const void* x, void* out, void* workspace, size_t worksp
     const int rc = check_stack(B, R, C, dtype);
     if (rc) return rc;
     if (steps < 0 || steps > kMaxSteps) return DCNV4_ERR_SHAPE;
+    int down[kMaxSteps + 1];
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c) || !std::isfinite(eps) || !(eps > 0.f) ||
-        !coefficients_bounded(a, b, c, steps))
+        !coefficients_bounded(a, b, c, steps, down))
         return DCNV4_ERR_COEFFICIENTS;
     if (B == 0) return DCNV4_OK;
     if (!x || !out || !workspace) return DCNV4_ERR_NULL;
@@ -149,12 +194,14 @@ int dcnv4_orthogonalize(const void* x, void* out, void* workspace, size_t worksp
     if (overlap(out, nb, x, nb) || overlap(workspace, static_cast<long long>(need), x, nb) ||
         overlap(workspace, static_cast<long long>(need), out, nb))
         return DCNV4_ERR_ALIAS;
+    p.status = dcnv4_host::device_status_word();
+    if (!p.status) return DCNV4_ERR_CUDA;
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (dtype) {
-        case DCNV4_F32: return launch<float>(x, out, ws, steps, p, s);
-        case DCNV4_F16: return launch<__half>(x, out, ws, steps, p, s);
-        default: return launch<__nv_bfloat16>(x, out, ws, steps, p, s);
+        case DCNV4_F32: return launch<float>(x, out, ws, steps, down, p, s);
+        case DCNV4_F16: return launch<__half>(x, out, ws, steps, down, p, s);
+        default: return launch<__nv_bfloat16>(x, out, ws, steps, down, p, s);
     }
 }
 

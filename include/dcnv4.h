@@ -330,7 +330,8 @@ DCNV4_API int dcnv4_predictor_mx(const void *y, const uint8_t *weight_codes, con
  * dcnv4_orthogonalize_workspace's bytes; its contents before and after do not
  * matter, and calls whose work overlaps on the GPU need one each. Other
  * errors: DCNV4_ERR_SHAPE (B < 0, R or C <= 0, steps out of range),
- * DCNV4_ERR_DTYPE, DCNV4_ERR_TOO_LARGE (B*R*C >= 2^31), DCNV4_ERR_NULL,
+ * DCNV4_ERR_DTYPE, DCNV4_ERR_TOO_LARGE (B*R*C, its larger side rounded up to a
+ * multiple of 8, reaches 2^31), DCNV4_ERR_NULL,
  * DCNV4_ERR_ALIGN, DCNV4_ERR_WORKSPACE, DCNV4_ERR_ALIAS (out, x and workspace
  * overlap). Asynchronous on `stream`; nothing is launched when B == 0. */
 DCNV4_API int dcnv4_orthogonalize(const void *x, void *out, void *workspace, size_t workspace_bytes,
