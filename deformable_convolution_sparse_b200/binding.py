@@ -8,6 +8,7 @@ exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -208,7 +209,8 @@ def validate(x_ptr: int, om_ptr: int, out_ptr: int, N: int, H: int, W: int, C: i
 
 def _stream_handle(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current stream of the current device, without making a Stream object of it
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return int(stream.cuda_stream)
 
 
@@ -385,18 +387,21 @@ def predictor(y: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None, 
 def _output(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype, device) -> torch.Tensor:
     """``t`` checked against shape, dtype and device, or a new tensor of them."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
     if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device \
             or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _launching_on(device, stream):
     """Makes ``device`` current, and ``stream`` too when one is given: outputs and workspaces then come from
     the memory pool of the stream whose kernels use them, which is what orders their reuse."""
     if stream is None:
-        return torch.cuda.device(device)
+        return _HERE if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     return torch.cuda.stream(stream)

@@ -22,34 +22,103 @@ namespace {
 
 #include "dcnv4_unit_common.inl"
 
-// Pixel ranges of the weight gradient. From the sizes alone, so that the sums'
-// order (and the result's bits) are the same on every device and in every run.
-void split_pixels(int M, dcnv4::PredBwdParams* p) {
-    const int want = std::max(1, std::min(64, (M + 511) / 512));
-    p->split_pixels = static_cast<int>((static_cast<long long>(M) + want - 1) / want);
-    p->splits = M > 0 ? (M + p->split_pixels - 1) / p->split_pixels : 0;
+// Tiles, slices and walkers, from the sizes alone (and a nominal 148 SMs), so
+// that the sums' order, and with it the result's bits, are the same everywhere.
+dcnv4::PredBwdParams make_params(int M, int C, int G, long long P, long long NO) {
+    dcnv4::PredBwdParams p{};
+    p.M = M; p.C = C; p.G = G; p.P = static_cast<int>(P); p.NO = static_cast<int>(NO);
+    p.tiles = static_cast<int>((static_cast<long long>(M) + 127) / 128);
+    p.chunks = (p.NO + 63) / 64;
+    p.wrows = p.chunks * 64;
+    p.wpitch = (C + 63) / 64 * 64;
+    p.groups = (p.NO + 127) / 128;
+    const long long per = static_cast<long long>(p.groups) * ((C + 127) / 128);
+    p.walkers = static_cast<int>(std::max<long long>(1, std::min<long long>(p.tiles, 148 / per)));
+    return p;
 }
 
-long long workspace_bytes(const dcnv4::PredBwdParams& p) {
-    return 4LL * p.splits * (static_cast<long long>(p.NO) * p.C + p.NO);
+int planes_of(int dtype) { return dtype == DCNV4_F32 ? 3 : dtype == DCNV4_F16 ? 2 : 1; }
+
+// Workspace: W's planes, the walkers' partial sums of grad_weight, of grad_bias.
+struct Layout {
+    size_t part, pbias, bytes;
+};
+Layout layout(const dcnv4::PredBwdParams& p, int dtype) {
+    Layout l{};
+    auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+    l.part = up(static_cast<size_t>(planes_of(dtype)) * p.wrows * p.wpitch * 2);
+    l.pbias = l.part + up(static_cast<size_t>(p.walkers) * p.NO * p.C * 4);
+    l.bytes = p.M == 0 ? 0 : l.pbias + up(static_cast<size_t>(p.walkers) * p.NO * 4);
+    return l;
+}
+
+bool tile_map(CUtensorMap* map, CUtensorMapDataType type, int e, void* base, long long cols, long long rows,
+              long long planes, int box_cols, int box_rows) {
+    auto encode = tensor_map_encoder();
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(planes)};
+    const cuuint64_t str[2] = {static_cast<cuuint64_t>(cols * e), static_cast<cuuint64_t>(cols * rows * e)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1u}, es[3] = {1u, 1u, 1u};
+    return encode && encode(map, type, 3, base, dims, str, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int CT, int WP>
+int launch_grad_y(const CUtensorMap& wmap, const CUtensorMap& omap, const float* grec, float* gy,
+                  dcnv4::PredBwdParams p, int nsm, bool vec, cudaStream_t s) {
+    constexpr unsigned smem = dcnv4::GradYShape<CT, WP>::kSmem;
+    static_assert(smem <= kTileSmemLimit, "the stages do not fit");
+    auto kern = vec ? dcnv4::pred_grad_y_kernel<CT, WP, true> : dcnv4::pred_grad_y_kernel<CT, WP, false>;
+    if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess)
+        return DCNV4_ERR_LAUNCH;
+    p.slices = (p.C + CT - 1) / CT;
+    const long long items = static_cast<long long>(p.tiles) * p.slices;
+    return launch_chained(kern, dim3(static_cast<unsigned>(std::min<long long>(items, nsm))), 448, smem, s, wmap, omap,
+                          grec, gy, p);
 }
 
 template <typename T>
-int launch(const void* y, const void* w, const float* grec, float* gy, float* gw, float* gb, float* ws,
-           const dcnv4::PredBwdParams& p, cudaStream_t s) {
-    constexpr int t = dcnv4::kSimtTile;
-    const unsigned mt = static_cast<unsigned>((static_cast<long long>(p.M) + t - 1) / t);
-    const unsigned ct = static_cast<unsigned>((p.C + t - 1) / t), st = static_cast<unsigned>((p.NO + t - 1) / t);
-    int rc = launch_chained(dcnv4::pred_grad_y_kernel<T>, dim3(mt, ct), 256, 0, s, grec, static_cast<const T*>(w), gy, p);
+int launch(const void* y, const void* w, const float* grec, float* gy, float* gw, float* gb, unsigned char* ws,
+           dcnv4::PredBwdParams p, int dtype, cudaStream_t s) {
+    constexpr int WP = dcnv4::split_planes<T>();
+    const int nsm = sm_count();
+    if (nsm <= 0) return DCNV4_ERR_CUDA;
+    const Layout l = layout(p, dtype);
+    __nv_bfloat16* planes = reinterpret_cast<__nv_bfloat16*>(ws);
+    float *part = reinterpret_cast<float*>(ws + l.part), *pbias = gb ? reinterpret_cast<float*>(ws + l.pbias) : nullptr;
+    CUtensorMap wmap, omap;
+    if (!tile_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, planes, p.wpitch, p.wrows, WP, 64, 64)) return DCNV4_ERR_CUDA;
+    omap = wmap;
+    p.tma_out = p.C % 4 == 0 && aligned(gy, 16) ? 1 : 0;
+    if (p.tma_out && !tile_map(&omap, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, gy, p.C, p.M, 1, 32, 128)) return DCNV4_ERR_CUDA;
+    const long long pairs = static_cast<long long>(p.wrows) * p.wpitch / 2;
+    int rc = launch_chained(dcnv4::pred_split_weight_kernel<T>, dim3(static_cast<unsigned>(std::min<long long>((pairs + 255) / 256, 148 * 8))),
+                            256, 0, s, static_cast<const T*>(w), planes, p);
     if (rc) return rc;
-    float* part = ws;
-    float* pbias = ws + static_cast<size_t>(p.splits) * p.NO * p.C;
-    rc = launch_chained(dcnv4::pred_grad_w_partial_kernel<T>, dim3(st, ct, static_cast<unsigned>(p.splits)), 256, 0, s,
-                        grec, static_cast<const T*>(y), part, pbias, p);
+    const bool vec = p.NO % 4 == 0 && aligned(grec, 16);
+    // 128 channels per tile halve the readings of g; with many slots (long chains of truncated additions) or three
+    // weight planes (shared memory) 64 channels leave room for three accumulators of order 0
+    if constexpr (WP <= 2) {
+        if (p.C > 64 && p.NO <= 256) rc = launch_grad_y<128, WP>(wmap, omap, grec, gy, p, nsm, vec, s);
+        else rc = launch_grad_y<64, WP>(wmap, omap, grec, gy, p, nsm, vec, s);
+    } else {
+        rc = launch_grad_y<64, WP>(wmap, omap, grec, gy, p, nsm, vec, s);
+    }
     if (rc) return rc;
-    const long long n = static_cast<long long>(p.NO) * p.C + p.NO;
-    return launch_chained(dcnv4::pred_grad_w_join_kernel, dim3(static_cast<unsigned>(std::min<long long>((n + 255) / 256, 148 * 8))),
-                          256, 0, s, static_cast<const float*>(part), static_cast<const float*>(pbias), gw, gb, p);
+    const bool vecy = p.C % 8 == 0 && aligned(y, 16);
+    auto kern = vec ? (vecy ? dcnv4::pred_grad_w_kernel<T, true, true> : dcnv4::pred_grad_w_kernel<T, true, false>)
+                    : (vecy ? dcnv4::pred_grad_w_kernel<T, false, true> : dcnv4::pred_grad_w_kernel<T, false, false>);
+    constexpr unsigned smem = dcnv4::GradWShape<T>::kSmem;
+    static_assert(smem <= kTileSmemLimit, "the stages do not fit");
+    if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess) return DCNV4_ERR_LAUNCH;
+    p.slices = (p.C + 127) / 128;
+    rc = launch_chained(kern, dim3(static_cast<unsigned>(p.walkers) * p.slices * p.groups), 416, smem, s, grec,
+                        static_cast<const T*>(y), part, pbias, p);
+    if (rc) return rc;
+    const long long n = (static_cast<long long>(p.NO) * p.C + (gb ? p.NO : 0) + 31) / 32;
+    return launch_chained(dcnv4::pred_grad_w_join_kernel, dim3(static_cast<unsigned>(std::min<long long>(n, 148 * 8))), 256, 0, s,
+                          static_cast<const float*>(part), static_cast<const float*>(pbias), gw, gb, p);
 }
 
 }  // namespace
@@ -61,10 +130,7 @@ int dcnv4_predictor_backward_workspace(int M, int C, int G, int K, unsigned flag
     const int rc = check_projection(M, C, G, K, flags, dtype, &P, &NO);
     if (rc) return rc;
     if (!bytes) return DCNV4_ERR_NULL;
-    dcnv4::PredBwdParams p{};
-    p.M = M; p.C = C; p.G = G; p.P = static_cast<int>(P); p.NO = static_cast<int>(NO);
-    split_pixels(M, &p);
-    *bytes = static_cast<size_t>(workspace_bytes(p));
+    *bytes = layout(make_params(M, C, G, P, NO), dtype).bytes;
     return DCNV4_OK;
 }
 
@@ -74,16 +140,14 @@ int dcnv4_predictor_backward(const void* y, const void* weight, const float* gra
     long long P = 0, NO = 0;
     const int rc = check_projection(M, C, G, K, flags, dtype, &P, &NO);
     if (rc) return rc;
-    dcnv4::PredBwdParams p{};
-    p.M = M; p.C = C; p.G = G; p.P = static_cast<int>(P); p.NO = static_cast<int>(NO);
-    split_pixels(M, &p);
+    dcnv4::PredBwdParams p = make_params(M, C, G, P, NO);
     const int e = elem_size(dtype);
     const long long ny = static_cast<long long>(M) * C, nw = NO * C, nrec = M * NO;
-    const long long need = workspace_bytes(p);
+    const long long need = static_cast<long long>(layout(p, dtype).bytes);
     // without pixels the weight's gradients are still written (zeros)
     if (!grad_weight || (M > 0 && (!y || !weight || !grad_offset_mask || !grad_y || !workspace))) return DCNV4_ERR_NULL;
     if (!aligned(y, e) || !aligned(weight, e) || !aligned(grad_offset_mask, 4) || !aligned(grad_y, 4) ||
-        !aligned(grad_weight, 4) || !aligned(grad_bias, 4) || (M > 0 && !aligned(workspace, 16)))
+        !aligned(grad_weight, 4) || !aligned(grad_bias, 4) || (M > 0 && !aligned(workspace, 256)))
         return DCNV4_ERR_ALIGN;
     if (M > 0 && workspace_size < static_cast<size_t>(need)) return DCNV4_ERR_WORKSPACE;
     const void* in[3] = {y, weight, grad_offset_mask};
@@ -103,11 +167,13 @@ int dcnv4_predictor_backward(const void* y, const void* weight, const float* gra
             return DCNV4_ERR_CUDA;
         return DCNV4_OK;
     }
-    float* ws = static_cast<float*>(workspace);
+    p.status = dcnv4_host::device_status_word();
+    if (!p.status) return DCNV4_ERR_CUDA;
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
     switch (dtype) {
-        case DCNV4_F32: return launch<float>(y, weight, grad_offset_mask, grad_y, grad_weight, grad_bias, ws, p, s);
-        case DCNV4_F16: return launch<__half>(y, weight, grad_offset_mask, grad_y, grad_weight, grad_bias, ws, p, s);
-        default: return launch<__nv_bfloat16>(y, weight, grad_offset_mask, grad_y, grad_weight, grad_bias, ws, p, s);
+        case DCNV4_F32: return launch<float>(y, weight, grad_offset_mask, grad_y, grad_weight, grad_bias, ws, p, dtype, s);
+        case DCNV4_F16: return launch<__half>(y, weight, grad_offset_mask, grad_y, grad_weight, grad_bias, ws, p, dtype, s);
+        default: return launch<__nv_bfloat16>(y, weight, grad_offset_mask, grad_y, grad_weight, grad_bias, ws, p, dtype, s);
     }
 }
 

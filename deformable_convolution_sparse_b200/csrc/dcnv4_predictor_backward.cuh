@@ -1,10 +1,22 @@
 // sm_100a kernels of the offset/mask predictor's backward. With the projection
 //   record[m, slot(o)] = bias[o] + sum_c W[o, c] y[m, c]
-// and gp[m, o] = dL/drecord[m, slot(o)] (the fp32 records the aggregation's
-// backward writes), the gradients are
-//   dL/dy[m, c] = sum_o gp[m, o] W[o, c]
-//   dL/dW[o, c] = sum_m gp[m, o] y[m, c]
-//   dL/dbias[o] = sum_m gp[m, o].
+// and g[m, s] = dL/drecord[m, s] (the fp32 records the aggregation's backward
+// writes), the gradients are, over record slots s,
+//   dL/dy[m, c] = sum_s g[m, s] W[s, c]
+//   dL/dW[s, c] = sum_m g[m, s] y[m, c]
+//   dL/dbias[s] = sum_m g[m, s]
+// and the rows of the last two are moved to the projection's channel order.
+//
+// Precision on the tensor cores. An fp32 value is the exact sum of three bf16
+// values, h = bf16(v), m = bf16(v - h), l = v - h - m (24 bits in three times
+// 8, whatever the magnitude); fp16 takes two and bf16 one. A product of two
+// such sums keeps the pairs whose orders add to at most 2 (the others are
+// below 2^-26 of it): 3 tensor-core products for bf16 operands, 5 for fp16, 6
+// for fp32, each exact, summed in fp32. The tensor cores' additions truncate,
+// so a long chain of them drifts one way: the pairs of order 0 go to up to
+// three accumulators in turn, the small others to one of their own, and these
+// are added with rounding when they are read; the weight's gradient is read
+// out every kFlushTiles tiles of pixels.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -12,15 +24,23 @@
 
 #include "dcnv4_async.cuh"
 #include "dcnv4_kernels.cuh"
-#include "dcnv4_simt_gemm.cuh"
+#include "dcnv4_tcgen05.cuh"
 
 namespace dcnv4 {
 
 struct PredBwdParams {
     int M, C, G, P, NO;
-    int splits;          // ranges of pixels, each with its own partial sums of dL/dW and dL/dbias
-    int split_pixels;    // pixels per range
+    int tiles;           // tiles of 128 pixels
+    int chunks;          // chunks of 64 record slots
+    int slices;          // slices of the input channels: CT each (grad_y), 128 each (grad_weight)
+    int wrows, wpitch;   // rows and pitch of a plane of W in record order (multiples of 64)
+    int groups;          // groups of 128 slots (grad_weight)
+    int walkers;         // CTAs that share the pixel tiles of a (slice, group), each with partial sums of its own
+    int tma_out;         // grad_y by TMA
+    unsigned* status;
 };
+
+constexpr int kFlushTiles = 16;
 
 // projection channel of a record slot
 __host__ __device__ __forceinline__ int channel_of_slot(int s, int G, int P) {
@@ -29,65 +49,563 @@ __host__ __device__ __forceinline__ int channel_of_slot(int s, int G, int P) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256)
-pred_grad_y_kernel(const float* __restrict__ grec, const T* __restrict__ w, float* __restrict__ gy, PredBwdParams p) {
-    __shared__ SimtSmem sm;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    simt_tile(
-        sm, blockIdx.x * kSimtTile, blockIdx.y * kSimtTile, p.M, p.C, 0, p.NO,
-        [&](int m, int s) { return __ldg(grec + static_cast<size_t>(m) * p.NO + s); },
-        [&](int s, int c) {
-            return ElemTraits<T>::to_float(__ldg(w + static_cast<size_t>(channel_of_slot(s, p.G, p.P)) * p.C + c));
-        },
-        [&](int m, int c, float v) { gy[static_cast<size_t>(m) * p.C + c] = v; });
+constexpr int split_planes() {
+    return sizeof(T) == 4 ? 3 : std::is_same<T, __half>::value ? 2 : 1;
 }
 
-// Partial sums of one pixel range: part[split][slot][c], and pbias[split][slot].
-template <typename T>
-__global__ void __launch_bounds__(256)
-pred_grad_w_partial_kernel(const float* __restrict__ grec, const T* __restrict__ y, float* __restrict__ part,
-                           float* __restrict__ pbias, PredBwdParams p) {
-    __shared__ SimtSmem sm;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int split = blockIdx.z;
-    const int m0 = split * p.split_pixels, m1 = min(p.M, m0 + p.split_pixels);
-    simt_tile(
-        sm, blockIdx.x * kSimtTile, blockIdx.y * kSimtTile, p.NO, p.C, m0, m1,
-        [&](int s, int m) { return __ldg(grec + static_cast<size_t>(m) * p.NO + s); },
-        [&](int m, int c) { return ElemTraits<T>::to_float(__ldg(y + static_cast<size_t>(m) * p.C + c)); },
-        [&](int s, int c, float v) { part[(static_cast<size_t>(split) * p.NO + s) * p.C + c] = v; });
-    if (blockIdx.y == 0) {
-        const int s = blockIdx.x * kSimtTile + threadIdx.x;
-        if (threadIdx.x < kSimtTile && s < p.NO) {
-            float a = 0.f;
-            for (int m = m0; m < m1; ++m) a += __ldg(grec + static_cast<size_t>(m) * p.NO + s);
-            pbias[static_cast<size_t>(split) * p.NO + s] = a;
+// Two fp32 values as bf16 pairs of falling order (a in the low half).
+template <int PLANES>
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t (&w)[PLANES]) {
+#pragma unroll
+    for (int q = 0; q < PLANES; ++q) {
+        w[q] = pack2(a, b, static_cast<__nv_bfloat16*>(nullptr));
+        if (q + 1 < PLANES) {
+            a -= __uint_as_float(w[q] << 16);
+            b -= __uint_as_float(w[q] & 0xffff0000u);
         }
     }
 }
 
-// The ranges' partial sums added in order (the same order in every run), rows
-// moved from record order to the projection's channel order.
+// Eight values as 16-byte chunks of PLANES swizzled tiles `step` bytes apart:
+// row r, chunk ch of 128-byte rows.
+template <int PLANES>
+__device__ __forceinline__ void store_split8(unsigned char* tile, unsigned step, int r, int ch, const float (&v)[8]) {
+    uint32_t w[4][PLANES];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) split_pair<PLANES>(v[2 * q], v[2 * q + 1], w[q]);
+    unsigned char* at = tile + r * 128 + ((ch ^ (r & 7)) << 4);
+#pragma unroll
+    for (int q = 0; q < PLANES; ++q)
+        *reinterpret_cast<uint4*>(at + q * step) = make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
+}
+
+// W's planes in record order, zero padded: planes [PLANES][wrows][wpitch].
+template <typename T>
+__global__ void __launch_bounds__(256)
+pred_split_weight_kernel(const T* __restrict__ w, __nv_bfloat16* __restrict__ planes, PredBwdParams p) {
+    constexpr int PL = split_planes<T>();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const long long n = static_cast<long long>(p.wrows) * p.wpitch / 2;
+    for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < n;
+         i += static_cast<long long>(gridDim.x) * 256) {
+        const int s = static_cast<int>(2 * i / p.wpitch), c = static_cast<int>(2 * i - static_cast<long long>(s) * p.wpitch);
+        float a = 0.f, b = 0.f;
+        if (s < p.NO) {
+            const T* row = w + static_cast<size_t>(channel_of_slot(s, p.G, p.P)) * p.C;
+            if (c < p.C) a = ElemTraits<T>::to_float(__ldg(row + c));
+            if (c + 1 < p.C) b = ElemTraits<T>::to_float(__ldg(row + c + 1));
+        }
+        uint32_t q[PL];
+        split_pair<PL>(a, b, q);
+#pragma unroll
+        for (int k = 0; k < PL; ++k) reinterpret_cast<uint32_t*>(planes)[k * n + i] = q[k];
+    }
+}
+
+// The records' gradients of 128 pixels x 64 slots in registers: this
+// thread's (0..255) four rows tid / 8 + 32 q, slots 8 (tid % 8) .. + 7.
+struct GradPiece {
+    float4 v[4][2];
+};
+template <bool VEC>
+__device__ __forceinline__ void load_grad(GradPiece& r, const float* __restrict__ g, long long m0, int s0, int tid,
+                                          const PredBwdParams& p) {
+    const int s = s0 + (tid & 7) * 8;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const long long m = m0 + (tid >> 3) + 32 * q;
+        const float* src = g + m * p.NO + s;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if constexpr (VEC) {
+                r.v[q][h] = m < p.M && s + 4 * h < p.NO ? __ldg(reinterpret_cast<const float4*>(src + 4 * h))
+                                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+            } else {
+                float e[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) e[k] = m < p.M && s + 4 * h + k < p.NO ? __ldg(src + 4 * h + k) : 0.f;
+                r.v[q][h] = make_float4(e[0], e[1], e[2], e[3]);
+            }
+        }
+    }
+}
+__device__ __forceinline__ void store_grad(unsigned char* stage, const GradPiece& r, int tid) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float v[8] = {r.v[q][0].x, r.v[q][0].y, r.v[q][0].z, r.v[q][0].w,
+                            r.v[q][1].x, r.v[q][1].y, r.v[q][1].z, r.v[q][1].w};
+        store_split8<3>(stage, 16384u, (tid >> 3) + 32 * q, tid & 7, v);
+    }
+}
+
+// grad_y: tiles of 128 pixels x CT channels. Warps 0..7 read g 64 slots at a
+// time (two chunks ahead, in registers) and write its planes as the left
+// operand (K-major); warp 8 loads the same slots' rows of W's planes by TMA as
+// the right one (its rows run along the channels: MN-major); warp 9 issues the
+// products; warps 10..13 read the accumulators (two sets, in turn) and write
+// the tile through shared memory and TMA.
+template <int CT, int WP>
+struct GradYShape {
+    static constexpr int kStages = 2;
+    static constexpr int kHigh = CT == 64 ? 3 : 1;  // accumulators of order 0
+    static constexpr unsigned kWBytes = WP * (CT / 64) * 8192u;
+    static constexpr unsigned kStage = 3u * 16384u + kWBytes;
+    static constexpr unsigned kOut = (CT / 32) * 16384u;
+    static constexpr unsigned kSmem = 1024u + kStages * kStage + kOut + 256u;
+    static constexpr unsigned kAcc = (kHigh + 1) * CT;  // columns of one set
+};
+
+template <int CT, int WP, bool VEC>
+__global__ void __launch_bounds__(448, 1)
+pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap omap,
+                   const float* __restrict__ grec, float* __restrict__ gy, PredBwdParams p) {
+    using S = GradYShape<CT, WP>;
+    extern __shared__ unsigned char pb_smem_raw[];
+    unsigned char* sm = pb_smem_raw + ((1024u - (smem_addr(pb_smem_raw) & 1023u)) & 1023u);
+    unsigned char* outs = sm + S::kStages * S::kStage;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(outs + S::kOut);
+    uint64_t *full_g = bars, *full_w = bars + 2, *empty = bars + 4, *acc_full = bars + 6, *acc_empty = bars + 8;
+    uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 10);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&full_g[s], 256);
+            mbar_init(&full_w[s], 1);
+            mbar_init(&empty[s], 1);
+            mbar_init(&acc_full[s], 1);
+            mbar_init(&acc_empty[s], 128);
+        }
+        fence_barrier_init();
+    }
+    if (warp == 8) tc::alloc(slot, 512u);
+    tc::fence_before();
+    __syncthreads();  // every CTA holds its tensor memory before the next launch may start
+    tc::fence_after();
+    const uint32_t tmem = *slot;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // items: (tile, slice), slices of a tile side by side
+    const long long items = static_cast<long long>(p.tiles) * p.slices;
+    const long long mine = blockIdx.x < items ? (items - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+    const long long steps = mine * p.chunks;
+    bool ok = true;
+
+    if (warp < 8) {
+        auto where = [&](long long it, long long& m0, int& s0) {
+            const long long item = blockIdx.x + (it / p.chunks) * gridDim.x;
+            m0 = item / p.slices * 128;
+            s0 = static_cast<int>(it % p.chunks) * 64;
+        };
+        GradPiece ra, rb;
+        long long m0;
+        int s0;
+        if (steps > 0) {
+            where(0, m0, s0);
+            load_grad<VEC>(ra, grec, m0, s0, tid, p);
+        }
+        auto step = [&](long long it, GradPiece& now, GradPiece& next) {
+            if (it + 1 < steps) {
+                where(it + 1, m0, s0);
+                load_grad<VEC>(next, grec, m0, s0, tid, p);
+            }
+            const int s = static_cast<int>(it & 1);
+            if (it >= 2) ok = mbar_wait_bounded(&empty[s], static_cast<unsigned>((it >> 1) - 1) & 1u, kCopyWaitLimitNs);
+            if (!ok) return;
+            store_grad(sm + s * S::kStage, now, tid);
+            fence_proxy_async();
+            mbar_arrive(&full_g[s]);
+        };
+        for (long long it = 0; it < steps && ok; it += 2) {
+            step(it, ra, rb);
+            if (it + 1 < steps && ok) step(it + 1, rb, ra);
+        }
+    } else if (warp == 8) {
+        if (lane == 0) {
+            for (long long it = 0; it < steps && ok; ++it) {
+                const int s = static_cast<int>(it & 1);
+                if (it >= 2) ok = mbar_wait_bounded(&empty[s], static_cast<unsigned>((it >> 1) - 1) & 1u, kCopyWaitLimitNs);
+                if (!ok) break;
+                const long long item = blockIdx.x + (it / p.chunks) * gridDim.x;
+                const int c0 = static_cast<int>(item % p.slices) * CT, s0 = static_cast<int>(it % p.chunks) * 64;
+                unsigned char* w = sm + s * S::kStage + 3 * 16384;
+                mbar_expect_tx(&full_w[s], S::kWBytes);
+                for (int pl = 0; pl < WP; ++pl)
+                    for (int b = 0; b < CT / 64; ++b)
+                        tc::tma_load_3d(w + (pl * (CT / 64) + b) * 8192, &wmap, c0 + b * 64, s0, pl, &full_w[s]);
+                mbar_arrive(&full_w[s]);
+            }
+        }
+    } else if (warp == 9) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = tc::idesc_f16(tc::kFmtBf16, CT, false, true);
+            for (long long it = 0; it < steps && ok; ++it) {
+                const int s = static_cast<int>(it & 1), chunk = static_cast<int>(it % p.chunks);
+                const long long n = it / p.chunks;
+                const int b = static_cast<int>(n & 1);
+                if (chunk == 0 && n >= 2)
+                    ok = mbar_wait_bounded(&acc_empty[b], static_cast<unsigned>((n >> 1) - 1) & 1u, kCopyWaitLimitNs);
+                ok = ok && mbar_wait_bounded(&full_g[s], static_cast<unsigned>(it >> 1) & 1u, kCopyWaitLimitNs) &&
+                     mbar_wait_bounded(&full_w[s], static_cast<unsigned>(it >> 1) & 1u, kCopyWaitLimitNs);
+                if (!ok) break;
+                tc::fence_after();
+                const uint32_t acc = tmem + b * S::kAcc, low = acc + S::kHigh * CT;
+                const unsigned a = smem_addr(sm + s * S::kStage), w = a + 3u * 16384u;
+                const int ksteps = (min(64, p.NO - chunk * 64) + 15) / 16;
+                for (int k = 0; k < ksteps; ++k) {
+                    const int n16 = chunk * 4 + k;
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+#pragma unroll
+                        for (int j = 0; j < WP; ++j) {
+                            if (i + j > 2) continue;
+                            const uint64_t ad = tc::sw128_desc(a + i * 16384u + k * 32u);
+                            const uint64_t bd = tc::sw128_desc(w + j * (CT / 64) * 8192u + k * 2048u, 8192u);
+                            if (i + j == 0) tc::mma_f16(acc + (n16 % S::kHigh) * CT, ad, bd, idesc, n16 >= S::kHigh);
+                            else tc::mma_f16(low, ad, bd, idesc, n16 > 0 || !(i == (WP > 1 ? 0 : 1) && j == (WP > 1 ? 1 : 0)));
+                        }
+                }
+                tc::commit(&empty[s]);
+                if (chunk == p.chunks - 1) tc::commit(&acc_full[b]);
+            }
+        }
+    } else {
+        const int quarter = warp & 3, row = quarter * 32 + lane, et = tid - 320;
+        const int high = min(S::kHigh, (p.NO + 15) / 16);
+        for (long long n = 0; n < mine; ++n) {
+            const long long item = blockIdx.x + n * gridDim.x;
+            const long long m0 = item / p.slices * 128;
+            const int c0 = static_cast<int>(item % p.slices) * CT, b = static_cast<int>(n & 1);
+            if (et == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            ok = tc::bar_and(1, 128, mbar_wait_bounded(&acc_full[b], static_cast<unsigned>(n >> 1) & 1u, kCopyWaitLimitNs));
+            if (!ok) break;
+            tc::fence_after();
+            const uint32_t acc = tmem + b * S::kAcc + (static_cast<uint32_t>(quarter * 32) << 16);
+            for (int cc = 0; cc < CT / 16; ++cc) {
+                float v[16], w[16];
+                tc::ld16(acc + S::kHigh * CT + cc * 16, v);
+                for (int q = 0; q < high; ++q) {
+                    tc::ld16(acc + q * CT + cc * 16, w);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] += w[e];
+                }
+                // 32 channels (128 bytes) per block of the staging tile
+                unsigned char* o = outs + (cc >> 1) * 16384 + row * 128;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<float4*>(o + ((((cc & 1) * 4 + q) ^ (row & 7)) << 4)) =
+                        make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            }
+            tc::fence_before();
+            mbar_arrive(&acc_empty[b]);
+            if (p.tma_out) fence_proxy_async();
+            tc::bar_sync(1, 128);
+            if (p.tma_out) {
+                if (et == 0) {
+                    for (int q = 0; q < CT / 32; ++q)
+                        if (c0 + q * 32 < p.C) tc::tma_store_3d(&omap, c0 + q * 32, static_cast<int>(m0), 0, outs + q * 16384);
+                    tc::bulk_commit();
+                }
+            } else {
+                const int rows = static_cast<int>(min(128LL, p.M - m0)), cols = min(CT, p.C - c0);
+                for (int r = quarter; r < rows; r += 4)
+                    for (int c = lane; c < cols; c += 32)
+                        gy[(m0 + r) * p.C + c0 + c] = *reinterpret_cast<const float*>(
+                            outs + (c >> 5) * 16384 + r * 128 + ((((c & 31) >> 2) ^ (r & 7)) << 4) + (c & 3) * 4);
+                tc::bar_sync(1, 128);
+            }
+        }
+        if (et == 0) tc::bulk_wait_all();
+    }
+    if (!ok) atomicOr(p.status, kStatusCopyTimeout);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 8) tc::dealloc(tmem, 512u);
+}
+
+// grad_weight and grad_bias, partial sums: 128 channels x 128 slots per CTA,
+// the pixels of every walkers-th tile. Warps 0..7 write the planes of y (the
+// left operand) and, 64 slots at a time, of g (the right one), both with rows
+// that run along channels or slots: MN-major; the same threads sum g for the
+// bias. Warp 8 issues the products, warps 9..12 read the accumulators out to
+// part [walkers][NO][C], lanes along the channels. A slice of at most 64
+// channels reads its one block of 64 for both halves of the M = 128 products.
+template <typename T>
+struct GradWShape {
+    static constexpr int YP = split_planes<T>();
+    static constexpr int kYStages = YP <= 2 ? 2 : 1;
+    static constexpr unsigned kY = YP * 32768u;
+    static constexpr unsigned kG = 3u * 16384u;
+    static constexpr unsigned kSmem = 1024u + kYStages * kY + 2u * kG + 256u;
+};
+
+// Eight channels of y at (m, c), zeros outside.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_y8(const T* __restrict__ y, long long m, int c, const PredBwdParams& p, uint4 (&w)[sizeof(T) / 2]) {
+    const T* src = y + m * p.C + c;
+    if constexpr (VEC) {
+        const bool on = m < p.M && c < p.C;
+#pragma unroll
+        for (int q = 0; q < static_cast<int>(sizeof(T) / 2); ++q)
+            w[q] = on ? __ldg(reinterpret_cast<const uint4*>(src) + q) : make_uint4(0, 0, 0, 0);
+    } else {
+        T* d = reinterpret_cast<T*>(w);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            if (m < p.M && c + q < p.C) d[q] = __ldg(src + q);
+            else if constexpr (sizeof(T) == 4) d[q] = 0.f;
+            else reinterpret_cast<uint16_t*>(w)[q] = 0;
+        }
+    }
+}
+
+template <typename T, bool VEC, bool VECY>
+__global__ void __launch_bounds__(416, 1)
+pred_grad_w_kernel(const float* __restrict__ grec, const T* __restrict__ y, float* __restrict__ part,
+                   float* __restrict__ pbias, PredBwdParams p) {
+    using S = GradWShape<T>;
+    constexpr int YP = S::YP, kQ = sizeof(T) / 2;
+    extern __shared__ unsigned char pb_smem_raw[];
+    unsigned char* sm = pb_smem_raw + ((1024u - (smem_addr(pb_smem_raw) & 1023u)) & 1023u);
+    unsigned char* gsm = sm + S::kYStages * S::kY;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(gsm + 2 * S::kG);
+    uint64_t *full_y = bars, *empty_y = bars + 2, *full_g = bars + 4, *empty_g = bars + 6, *acc_full = bars + 8,
+             *acc_empty = bars + 9;
+    uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 10);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&full_y[s], 256);
+            mbar_init(&empty_y[s], 1);
+            mbar_init(&full_g[s], 256);
+            mbar_init(&empty_g[s], 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 128);
+        fence_barrier_init();
+    }
+    if (warp == 8) tc::alloc(slot, 512u);
+    tc::fence_before();
+    __syncthreads();  // every CTA holds its tensor memory before the next launch may start
+    tc::fence_after();
+    const uint32_t tmem = *slot;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // CTA -> walker, (slice, group); the slices and groups of one walker side by side
+    const int per = p.slices * p.groups;
+    const int walker = static_cast<int>(blockIdx.x) / per, which = static_cast<int>(blockIdx.x) % per;
+    const int c0 = which % p.slices * 128, g0 = which / p.slices * 128;
+    const int nch = (min(128, p.NO - g0) + 63) / 64;    // chunks of this group
+    const bool wide = p.C - c0 > 64;
+    const int mine = walker < p.tiles ? (p.tiles - walker + p.walkers - 1) / p.walkers : 0;
+    bool ok = true;
+
+    if (warp < 8) {
+        const bool sums = c0 == 0 && pbias != nullptr;
+        float bs[2][8] = {};
+        GradPiece ra;
+        const int npiece = wide ? 8 : 4;  // eight-channel pieces of y per thread
+        const int per_row = wide ? 16 : 8;
+        uint4 yr[4][kQ];
+        auto fetch_y = [&](long long m0, int q0) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int e = (q0 + q) * 256 + tid;
+                load_y8<T, VECY>(y, m0 + e / per_row, c0 + e % per_row * 8, p, yr[q]);
+            }
+        };
+        if (mine > 0) {
+            const long long m0 = static_cast<long long>(walker) * 128;
+            fetch_y(m0, 0);
+            load_grad<VEC>(ra, grec, m0, g0, tid, p);
+        }
+        for (int i = 0; i < mine && ok; ++i) {
+            const long long m0 = (static_cast<long long>(walker) + static_cast<long long>(i) * p.walkers) * 128;
+            const long long m1 = m0 + static_cast<long long>(p.walkers) * 128;  // the next tile
+            const int ys = i % S::kYStages, yn = i / S::kYStages;
+            if (yn > 0) ok = mbar_wait_bounded(&empty_y[ys], static_cast<unsigned>(yn - 1) & 1u, kCopyWaitLimitNs);
+            if (!ok) break;
+            for (int q0 = 0; q0 < npiece; q0 += 4) {
+                if (q0 > 0) fetch_y(m0, q0);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int e = (q0 + q) * 256 + tid, r = e / per_row, ch = e % per_row;
+                    float v[8];
+                    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = reinterpret_cast<const float*>(yr[q])[k];
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 f = unpack2(reinterpret_cast<const uint32_t*>(yr[q])[k], static_cast<T*>(nullptr));
+                            v[2 * k] = f.x;
+                            v[2 * k + 1] = f.y;
+                        }
+                    }
+                    store_split8<YP>(sm + ys * S::kY + (ch >> 3) * 16384, 32768u, r, ch & 7, v);
+                }
+            }
+            fence_proxy_async();
+            mbar_arrive(&full_y[ys]);
+            if (i + 1 < mine) fetch_y(m1, 0);
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {
+                if (ch >= nch) break;
+                const int gi = i * nch + ch, s = gi & 1;
+                if (gi >= 2) ok = mbar_wait_bounded(&empty_g[s], static_cast<unsigned>((gi >> 1) - 1) & 1u, kCopyWaitLimitNs);
+                if (!ok) break;
+                store_grad(gsm + s * S::kG, ra, tid);
+                fence_proxy_async();
+                mbar_arrive(&full_g[s]);
+                if (sums) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        bs[ch][0] += ra.v[q][0].x; bs[ch][1] += ra.v[q][0].y; bs[ch][2] += ra.v[q][0].z; bs[ch][3] += ra.v[q][0].w;
+                        bs[ch][4] += ra.v[q][1].x; bs[ch][5] += ra.v[q][1].y; bs[ch][6] += ra.v[q][1].z; bs[ch][7] += ra.v[q][1].w;
+                    }
+                }
+                if (ch + 1 < nch) load_grad<VEC>(ra, grec, m0, g0 + 64, tid, p);
+                else if (i + 1 < mine) load_grad<VEC>(ra, grec, m1, g0, tid, p);
+            }
+        }
+        if (sums) {
+            // the last products may still read the operand tiles: the sums go through shuffles and the first
+            // planes once those are done (every commit below orders them)
+            const int last = mine * nch;
+            if (ok && last > 0) {
+                const int s = (last - 1) & 1;
+                ok = mbar_wait_bounded(&empty_g[s], static_cast<unsigned>((last - 1) >> 1) & 1u, kCopyWaitLimitNs);
+            }
+            float* red = reinterpret_cast<float*>(gsm);  // [8 warps][128 slots]
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    float v = bs[ch][k];
+                    v += __shfl_xor_sync(0xffffffffu, v, 8);
+                    v += __shfl_xor_sync(0xffffffffu, v, 16);
+                    if (lane < 8 && ok) red[warp * 128 + ch * 64 + lane * 8 + k] = v;
+                }
+            tc::bar_sync(2, 256);
+            if (ok && tid < 128 && g0 + tid < p.NO) {
+                float v = 0.f;
+                for (int k = 0; k < 8; ++k) v += red[k * 128 + tid];
+                pbias[static_cast<size_t>(walker) * p.NO + g0 + tid] = v;
+            }
+        }
+    } else if (warp == 8) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = tc::idesc_f16(tc::kFmtBf16, 64, true, true);
+            const unsigned second = wide ? 16384u : 0u;
+            int flushed = 0;
+            for (int i = 0; i < mine && ok; ++i) {
+                const int ys = i % S::kYStages, t = i % kFlushTiles;
+                if (i > 0 && t == 0) ok = mbar_wait_bounded(acc_empty, static_cast<unsigned>(flushed++) & 1u, kCopyWaitLimitNs);
+                ok = ok && mbar_wait_bounded(&full_y[ys], static_cast<unsigned>(i / S::kYStages) & 1u, kCopyWaitLimitNs);
+                for (int ch = 0; ch < nch && ok; ++ch) {
+                    const int gi = i * nch + ch, s = gi & 1;
+                    ok = mbar_wait_bounded(&full_g[s], static_cast<unsigned>(gi >> 1) & 1u, kCopyWaitLimitNs);
+                    if (!ok) break;
+                    tc::fence_after();
+                    const unsigned a = smem_addr(sm + ys * S::kY), b = smem_addr(gsm + s * S::kG);
+                    for (int k = 0; k < 8; ++k) {
+                        const int n16 = t * 8 + k;
+#pragma unroll
+                        for (int gi3 = 0; gi3 < 3; ++gi3)
+#pragma unroll
+                            for (int j = 0; j < YP; ++j) {
+                                if (gi3 + j > 2) continue;
+                                const uint64_t ad = tc::sw128_desc(a + j * 32768u + k * 2048u, second);
+                                const uint64_t bd = tc::sw128_desc(b + gi3 * 16384u + k * 2048u);
+                                if (gi3 + j == 0) tc::mma_f16(tmem + (n16 % 3) * 128 + ch * 64, ad, bd, idesc, n16 >= 3);
+                                else tc::mma_f16(tmem + 384 + ch * 64, ad, bd, idesc,
+                                                 n16 > 0 || !(gi3 == (YP > 1 ? 0 : 1) && j == (YP > 1 ? 1 : 0)));
+                            }
+                    }
+                    tc::commit(&empty_g[s]);
+                }
+                if (!ok) break;
+                tc::commit(&empty_y[ys]);
+                if (t == kFlushTiles - 1 || i == mine - 1) tc::commit(acc_full);
+            }
+        }
+    } else {
+        const int quarter = warp & 3, row = quarter * 32 + lane, c = c0 + row;
+        const int flushes = (mine + kFlushTiles - 1) / kFlushTiles;
+        const bool on = c < p.C && (wide || row < 64);
+        for (int f = 0; f < flushes; ++f) {
+            ok = tc::bar_and(1, 128, mbar_wait_bounded(acc_full, static_cast<unsigned>(f) & 1u, kCopyWaitLimitNs));
+            if (!ok) break;
+            tc::fence_after();
+            const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+            for (int q = 0; q < nch * 4; ++q) {
+                float v[16], w[16];
+                tc::ld16(acc + 384 + q * 16, v);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    tc::ld16(acc + k * 128 + q * 16, w);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] += w[e];
+                }
+                const int s = g0 + q * 16;
+                float* o = part + (static_cast<size_t>(walker) * p.NO + s) * p.C + c;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (on && s + e < p.NO) {
+                        float* at = o + static_cast<size_t>(e) * p.C;
+                        *at = f == 0 ? v[e] : *at + v[e];
+                    }
+            }
+            tc::fence_before();
+            mbar_arrive(acc_empty);
+        }
+    }
+    if (!ok) atomicOr(p.status, kStatusCopyTimeout);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 8) tc::dealloc(tmem, 512u);
+}
+
+// The walkers' partial sums added in a fixed order (eight strided runs of
+// walkers, then the eight), rows moved from record order to the projection's
+// channel order: 32 entries per CTA.
 __global__ void __launch_bounds__(256)
 pred_grad_w_join_kernel(const float* __restrict__ part, const float* __restrict__ pbias, float* __restrict__ gw,
                         float* __restrict__ gb, PredBwdParams p) {
+    __shared__ float red[8][32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const long long n = static_cast<long long>(p.NO) * p.C;
-    for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < n + p.NO;
-         i += static_cast<long long>(gridDim.x) * 256) {
+    const long long n = static_cast<long long>(p.NO) * p.C, total = n + (gb ? p.NO : 0);
+    const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
+    for (long long i0 = static_cast<long long>(blockIdx.x) * 32; i0 < total; i0 += static_cast<long long>(gridDim.x) * 32) {
+        const long long i = i0 + lane;
         float a = 0.f;
-        if (i < n) {
-            for (int k = 0; k < p.splits; ++k) a += __ldg(part + k * n + i);
-            const int s = static_cast<int>(i / p.C), c = static_cast<int>(i - static_cast<long long>(s) * p.C);
-            gw[static_cast<size_t>(channel_of_slot(s, p.G, p.P)) * p.C + c] = a;
-        } else if (gb) {
-            const int s = static_cast<int>(i - n);
-            for (int k = 0; k < p.splits; ++k) a += __ldg(pbias + static_cast<size_t>(k) * p.NO + s);
-            gb[channel_of_slot(s, p.G, p.P)] = a;
+        if (i < total) {
+            const float* src = i < n ? part + i : pbias + (i - n);
+            const long long step = i < n ? n : p.NO;
+#pragma unroll 8
+            for (int k = run; k < p.walkers; k += 8) a += __ldg(src + k * step);
         }
+        red[run][lane] = a;
+        __syncthreads();
+        if (run == 0 && i < total) {
+            for (int k = 1; k < 8; ++k) a += red[k][lane];
+            if (i < n) {
+                const int s = static_cast<int>(i / p.C), c = static_cast<int>(i - static_cast<long long>(s) * p.C);
+                gw[static_cast<size_t>(channel_of_slot(s, p.G, p.P)) * p.C + c] = a;
+            } else {
+                gb[channel_of_slot(static_cast<int>(i - n), p.G, p.P)] = a;
+            }
+        }
+        __syncthreads();
     }
 }
 
