@@ -22,7 +22,7 @@ namespace {
 
 #include "dcnv4_unit_common.inl"
 
-constexpr int kMaxSteps = 64;
+constexpr int kMaxSteps = dcnv4::kOrthoMaxSteps;
 
 int check_stack(int B, int R, int C, int dtype) {
     if (B < 0 || R <= 0 || C <= 0) return DCNV4_ERR_SHAPE;
@@ -110,25 +110,54 @@ bool plane_map(CUtensorMap* map, void* base, int cols, int pitch, int rows, int 
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Matrices that fit one CTA's shared memory run the whole iteration in one
+// kernel, one CTA each.
+bool fits_one_cta(const dcnv4::OrthoParams& p) {
+    if (const char* e = std::getenv("DCNV4_ORTHO_FORM"); e && std::strcmp(e, "products") == 0) return false;
+    return p.n <= 128 && (p.n + 63) / 64 + (p.m + 63) / 64 <= dcnv4::kOrthoSmallBlocks;
+}
+
+template <typename T>
+int launch_small(const void* x, void* out, int steps, const int* down, const dcnv4::OrthoParams& p, cudaStream_t s) {
+    dcnv4::OrthoSmall g{};
+    g.steps = steps;
+    g.xb = (p.m + 63) / 64;
+    g.nb = (p.n + 63) / 64;
+    g.n16 = (p.n + 15) / 16 * 16;
+    g.m16 = (p.m + 15) / 16 * 16;
+    const unsigned cols = static_cast<unsigned>(std::max(4 * g.n16, 2 * std::min(256, g.m16)));
+    g.tmem_cols = 32;
+    while (g.tmem_cols < cols) g.tmem_cols <<= 1;
+    for (int k = 0; k <= steps; ++k) g.down[k] = static_cast<short>(down[k]);
+    const unsigned smem = 1024u + static_cast<unsigned>(g.xb + g.nb) * dcnv4::kOrthoBlock;
+    auto kern = dcnv4::ortho_small_kernel<T>;
+    constexpr unsigned most = 1024u + dcnv4::kOrthoSmallBlocks * dcnv4::kOrthoBlock;
+    static_assert(most <= kTileSmemLimit, "the blocks do not fit");
+    if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(most)) != cudaSuccess) return DCNV4_ERR_LAUNCH;
+    return launch_chained(kern, dim3(static_cast<unsigned>(p.B)), dcnv4::kOrthoSmallThreads, smem, s,
+                          static_cast<const T*>(x), static_cast<T*>(out), g, p);
+}
+
 template <int MODE, typename T>
-int product(const CUtensorMap& l, const CUtensorMap& r, const CUtensorMap& o, T* out, int cols, int k,
+int product(const CUtensorMap& l, const CUtensorMap& r, const CUtensorMap& o, const __half* a, T* out, int cols, int k,
             const int* down, const dcnv4::OrthoParams& p, cudaStream_t s) {
     auto kern = dcnv4::ortho_product_kernel<MODE, T>;
     if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(dcnv4::kOrthoSmem)) != cudaSuccess)
         return DCNV4_ERR_LAUNCH;
-    dcnv4::OrthoTile g{};
+    dcnv4::OrthoTiles g{};
     g.tiles_i = (p.n + 127) / 128;
     g.tiles_j = (cols + 63) / 64;
     g.kblocks = (k + 63) / 64;
     g.down = down[0];
     g.down_next = down[1];
-    return launch_chained(kern, dim3(static_cast<unsigned>(p.B) * g.tiles_i * g.tiles_j), 192, dcnv4::kOrthoSmem, s, l, r,
-                          o, out, g, p);
+    return launch_chained(kern, dim3(static_cast<unsigned>(p.B) * g.tiles_i * g.tiles_j), dcnv4::kOrthoThreads, dcnv4::kOrthoSmem,
+                          s, l, r, o, a, out, g, p);
 }
 
 template <typename T>
 int launch(const void* x, void* out, unsigned char* ws, int steps, const int* down, dcnv4::OrthoParams p,
            cudaStream_t s) {
+    if (steps > 0 && fits_one_cta(p)) return launch_small<T>(x, out, steps, down, p, s);
     const Layout l = layout(p);
     p.lift = reinterpret_cast<int*>(ws + l.lift);
     double* part = reinterpret_cast<double*>(ws);
@@ -144,19 +173,19 @@ int launch(const void* x, void* out, unsigned char* ws, int steps, const int* do
     if (!plane_map(&am, a, p.n, p.np, p.n, planes, 128) || !plane_map(&ar, a, p.n, p.np, p.n, planes, 64) ||
         !plane_map(&qm, q, p.n, p.np, p.n, planes, 128))
         return DCNV4_ERR_CUDA;
+    T* o = static_cast<T*>(out);
     int rc = launch_chained(dcnv4::ortho_sumsq_kernel<T>, dim3(static_cast<unsigned>(p.B) * p.chunks), 256, 0, s,
                             static_cast<const T*>(x), part, p);
     if (rc) return rc;
-    T* o = static_cast<T*>(out);
     const unsigned st = static_cast<unsigned>(p.B) * ((p.R + 63) / 64) * ((p.C + 63) / 64);
     rc = launch_chained(dcnv4::ortho_start_kernel<T>, dim3(st), 256, 0, s, static_cast<const T*>(x),
                         static_cast<const double*>(part), x0, steps == 0 ? o : static_cast<T*>(nullptr), p);
     for (int k = 0, cur = 0; k < steps && !rc; ++k, cur ^= 1) {
-        rc = product<dcnv4::kGram, float>(xm[cur], xr[cur], am, nullptr, p.n, p.m, down + k, p, s);
-        if (!rc) rc = product<dcnv4::kPoly, float>(am, ar, qm, nullptr, p.n, p.n, down + k, p, s);
+        rc = product<dcnv4::kGram, float>(xm[cur], xr[cur], am, a, static_cast<float*>(nullptr), p.n, p.m, down + k, p, s);
+        if (!rc) rc = product<dcnv4::kPoly, float>(am, ar, qm, a, static_cast<float*>(nullptr), p.n, p.n, down + k, p, s);
         if (rc) break;
-        if (k + 1 < steps) rc = product<dcnv4::kApply, float>(qm, xr[cur], xm[cur ^ 1], nullptr, p.m, p.n, down + k, p, s);
-        else rc = product<dcnv4::kLast, T>(qm, xr[cur], xm[cur ^ 1], o, p.m, p.n, down + k, p, s);
+        if (k + 1 < steps) rc = product<dcnv4::kApply, float>(qm, xr[cur], xm[cur ^ 1], a, static_cast<float*>(nullptr), p.m, p.n, down + k, p, s);
+        else rc = product<dcnv4::kLast, T>(qm, xr[cur], xm[cur ^ 1], a, o, p.m, p.n, down + k, p, s);
     }
     return rc;
 }

@@ -16,8 +16,8 @@
 // the step can grow X. A product is three tensor-core products, hi hi + hi lo + lo hi (lo lo
 // is below 2^-24 of it), each exact, summed in fp32. The tensor cores' fp32
 // additions truncate, so a long chain of them drifts one way: the hi hi terms
-// go to up to six accumulators in turn and the small cross terms to one of
-// their own, and the epilogue adds these with rounding.
+// go to three accumulators in turn and the small cross terms to one of their
+// own, and the epilogue adds these with rounding.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -33,40 +33,15 @@ struct OrthoParams {
     int B, R, C;
     int n, m;          // smaller and larger side
     int transposed;    // R > C
-    int chunks;        // partial sums of squares per matrix
+    int chunks;        // partial sums of squares per matrix (one kernel per product)
     int np, mp;        // row pitches of the n x n and n x m planes, multiples of 8 elements
     float a, b, c, eps;
-    int* lift;         // [B] the exponents e of the first step
+    int* lift;         // [B] the exponents e of the first step (one kernel per product)
     unsigned* status;
 };
 
 // scales of the planes of X, A, P
 constexpr float kOrthoSX = 4096.f, kOrthoSA = 1024.f, kOrthoSP = 256.f;
-
-// Sum of squares of one chunk of a matrix, in fp64 (squares of fp32 values
-// neither overflow nor vanish there).
-template <typename T>
-__global__ void __launch_bounds__(256)
-ortho_sumsq_kernel(const T* __restrict__ x, double* __restrict__ part, OrthoParams p) {
-    __shared__ double ws[8];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const long long n = static_cast<long long>(p.R) * p.C;
-    const int mat = blockIdx.x / p.chunks, ch = blockIdx.x - mat * p.chunks;
-    const T* xm = x + mat * n;
-    double a = 0.0;
-    for (long long i = static_cast<long long>(ch) * 256 + threadIdx.x; i < n; i += static_cast<long long>(p.chunks) * 256) {
-        const double v = ElemTraits<T>::to_float(__ldg(xm + i));
-        a += v * v;
-    }
-    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    if ((threadIdx.x & 31) == 0) ws[threadIdx.x >> 5] = a;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < 8; ++i) a += ws[i];
-        part[blockIdx.x] = a;
-    }
-}
 
 template <typename T>
 __device__ __forceinline__ T ortho_from_float(float v) {
@@ -75,42 +50,67 @@ __device__ __forceinline__ T ortho_from_float(float v) {
     else return __float2bfloat16_rn(v);
 }
 
-// v * scale as an fp16 pair
+// v as an fp16 pair
 __device__ __forceinline__ void ortho_split(float v, __half& hi, __half& lo) {
     hi = __float2half_rn(v);
     lo = __float2half_rn(v - __half2float(hi));
 }
 
-// X / (norm + eps) as planes, 64 x 64 entries per CTA; with `out` (no steps)
-// the quotient itself. planes: [2][B][n][mp].
+// Sum of the squares of elements first, first + stride, ... of a matrix over
+// one CTA, in fp64 (squares of fp32 values neither overflow nor vanish there);
+// the result is thread 0's. ws: one double per warp.
 template <typename T>
-__global__ void __launch_bounds__(256)
-ortho_start_kernel(const T* __restrict__ x, const double* __restrict__ part, __half* __restrict__ planes,
-                   T* __restrict__ out, OrthoParams p) {
-    __shared__ float tile[64][65];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tr = (p.R + 63) / 64, tcn = (p.C + 63) / 64;
-    const int mat = static_cast<int>(blockIdx.x / (static_cast<unsigned>(tr) * tcn));
-    const int t = static_cast<int>(blockIdx.x - static_cast<unsigned>(mat) * tr * tcn);
-    const int r0 = (t / tcn) * 64, c0 = (t % tcn) * 64;
-    double sum = 0.0;
-    for (int i = 0; i < p.chunks; ++i) sum += part[static_cast<size_t>(mat) * p.chunks + i];
-    const double norm = sqrt(sum), den = norm + p.eps;
-    // v / den = (v 2^-k) / (den 2^-k) with den 2^-k in [1/2, 1): no overflow, whatever the norm
-    int k = 0;
-    const float mant = isfinite(den) ? static_cast<float>(frexp(den, &k)) : __uint_as_float(0x7fc00000u);
-    // norm / den in [2^(-1-e), 2^-e)
-    const int e = norm > 0.0 && isfinite(den) ? min(120, max(0, -ilogb(norm / den) - 1)) : 0;
-    const int shift = out ? -k : e - k;
-    if (p.lift && t == 0 && threadIdx.x == 0) p.lift[mat] = e;
+__device__ __forceinline__ double ortho_sumsq(const T* __restrict__ x, long long n, long long first, long long stride,
+                                              double* ws) {
+    double a = 0.0;
+    for (long long i = first; i < n; i += 8 * stride) {
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = i + q * stride < n ? ElemTraits<T>::to_float(__ldg(x + i + q * stride)) : 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) a = fma(static_cast<double>(v[q]), static_cast<double>(v[q]), a);
+    }
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    if ((threadIdx.x & 31) == 0) ws[threadIdx.x >> 5] = a;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (unsigned i = 1; i < blockDim.x / 32; ++i) a += ws[i];
+    return a;
+}
+
+// The division by den = norm + eps and the lift, from the sum of squares:
+// v / den = (v 2^-k) / (den 2^-k) with den 2^-k in [1/2, 1), so nothing
+// overflows whatever the norm; norm / den lies in [2^(-1-e), 2^-e).
+struct OrthoScale {
+    float mant;
+    int k, e;
+};
+__device__ __forceinline__ OrthoScale ortho_scale(double sum, float eps) {
+    OrthoScale s;
+    const double norm = sqrt(sum), den = norm + eps;
+    s.k = 0;
+    s.mant = isfinite(den) ? static_cast<float>(frexp(den, &s.k)) : __uint_as_float(0x7fc00000u);
+    s.e = norm > 0.0 && isfinite(den) ? min(120, max(0, -ilogb(norm / den) - 1)) : 0;
+    return s;
+}
+
+// 64 x 64 entries of X / den at (r0, c0) of a matrix as planes [2][B][n][mp]
+// (lifted and scaled), transposed on the way when R > C; with `out` (no steps)
+// the quotient itself. All threads of the CTA; tile: 64 x 65 floats.
+template <typename T>
+__device__ __forceinline__ void ortho_start_tile(const T* __restrict__ x, __half* __restrict__ planes, T* __restrict__ out,
+                                                 int mat, int r0, int c0, const OrthoScale& sc, float* tile,
+                                                 const OrthoParams& p) {
     const size_t base = static_cast<size_t>(mat) * p.R * p.C;
-    for (int q = threadIdx.x; q < 4096; q += 256) {
+    // scale, then divide: exact powers of two around one rounding
+    const int shift = out ? -sc.k : sc.e - sc.k;
+    for (int q = threadIdx.x; q < 4096; q += blockDim.x) {
         const int r = r0 + (q >> 6), c = c0 + (q & 63);
         if (r < p.R && c < p.C) {
-            const float v = scalbnf(ElemTraits<T>::to_float(__ldg(x + base + static_cast<size_t>(r) * p.C + c)), shift) / mant;
-            if (out) out[base + static_cast<size_t>(r) * p.C + c] = ortho_from_float<T>(v);
-            tile[q >> 6][q & 63] = v;
+            const size_t at = base + static_cast<size_t>(r) * p.C + c;
+            const float v = scalbnf(ElemTraits<T>::to_float(__ldg(x + at)), shift) / sc.mant;
+            if (out) out[at] = ortho_from_float<T>(v);
+            tile[(q >> 6) * 65 + (q & 63)] = v;
         }
     }
     if (out) return;
@@ -118,51 +118,107 @@ ortho_start_kernel(const T* __restrict__ x, const double* __restrict__ part, __h
     const size_t plane = static_cast<size_t>(p.B) * p.n * p.mp;
     __half* o = planes + static_cast<size_t>(mat) * p.n * p.mp;
     const int i0 = p.transposed ? c0 : r0, j0 = p.transposed ? r0 : c0;
-    for (int q = threadIdx.x; q < 4096; q += 256) {
-        const int i = q >> 6, j = q & 63;
+    for (int q = threadIdx.x; q < 2048; q += blockDim.x) {
+        const int i = q >> 5, j = (q & 31) * 2;
         if (i0 + i < p.n && j0 + j < p.m) {
-            __half hi, lo;
-            ortho_split((p.transposed ? tile[j][i] : tile[i][j]) * kOrthoSX, hi, lo);
+            // pairs of columns (the pitch is a multiple of 8; a last odd column's partner is padding)
+            __half2 hi, lo;
+            const float a = p.transposed ? tile[j * 65 + i] : tile[i * 65 + j];
+            const float b = j0 + j + 1 < p.m ? (p.transposed ? tile[(j + 1) * 65 + i] : tile[i * 65 + j + 1]) : 0.f;
+            ortho_split(a * kOrthoSX, hi.x, lo.x);
+            ortho_split(b * kOrthoSX, hi.y, lo.y);
             const size_t at = static_cast<size_t>(i0 + i) * p.mp + j0 + j;
-            o[at] = hi;
-            o[plane + at] = lo;
+            *reinterpret_cast<__half2*>(o + at) = hi;
+            *reinterpret_cast<__half2*>(o + plane + at) = lo;
         }
     }
+    __syncthreads();
 }
 
-// One product of the iteration, a 128 x 64 tile of the result per CTA.
+template <typename T>
+__global__ void __launch_bounds__(256)
+ortho_sumsq_kernel(const T* __restrict__ x, double* __restrict__ part, OrthoParams p) {
+    __shared__ double ws[8];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const long long n = static_cast<long long>(p.R) * p.C;
+    const int mat = blockIdx.x / p.chunks, ch = blockIdx.x - mat * p.chunks;
+    const double a = ortho_sumsq(x + mat * n, n, static_cast<long long>(ch) * 256 + threadIdx.x,
+                                 static_cast<long long>(p.chunks) * 256, ws);
+    if (threadIdx.x == 0) part[blockIdx.x] = a;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+ortho_start_kernel(const T* __restrict__ x, const double* __restrict__ part, __half* __restrict__ planes,
+                   T* __restrict__ out, OrthoParams p) {
+    __shared__ float tile[64 * 65];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const unsigned tr = static_cast<unsigned>((p.R + 63) / 64), tcn = static_cast<unsigned>((p.C + 63) / 64);
+    const int mat = static_cast<int>(blockIdx.x / (tr * tcn));
+    const unsigned t = blockIdx.x - static_cast<unsigned>(mat) * tr * tcn;
+    // at most 64 partial sums: two per lane, then a fixed tree
+    const int lane = threadIdx.x & 31;
+    const double* pm = part + static_cast<size_t>(mat) * p.chunks;
+    double sum = (lane < p.chunks ? pm[lane] : 0.0) + (lane + 32 < p.chunks ? pm[lane + 32] : 0.0);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const OrthoScale sc = ortho_scale(sum, p.eps);
+    if (t == 0 && threadIdx.x == 0) p.lift[mat] = sc.e;
+    ortho_start_tile(x, planes, out, mat, static_cast<int>(t / tcn) * 64, static_cast<int>(t % tcn) * 64, sc, tile, p);
+}
+
+// Four accumulators at `at`, `step` columns apart (the cross terms' last), 16
+// columns each, as one rounded sum.
+__device__ __forceinline__ void ortho_sum4(uint32_t at, uint32_t step, float (&v)[16]) {
+    float w[2][16];
+    tc::ld16(at + 3 * step, v);
+    tc::ld16(at + 2 * step, w[0]);
+    tc::ld16(at + step, w[1]);
+    tc::wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = (v[e] + w[0][e]) + w[1][e];
+    tc::ld16(at, w[0]);
+    tc::wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] += w[0][e];
+}
+
+// One product of the iteration, a 128 x 64 tile of the result per CTA:
 //   kGram:  A = X X^T          (k over m; both operands K-major rows of X)
 //   kPoly:  P = aI + bA + cAA  (k over n; A is symmetric: both K-major)
 //   kApply: X' = P X           (k over n; X's rows run along the result's
 //                               columns: an MN-major operand)
 //   kLast:  kApply with the result rounded to T and written to `out`
 // Warp 0 (one lane) loads 64 k at a time by TMA: 128 rows x 64 k of the left
-// planes, 64 x 64 of the right ones, in a ring of kOrthoStages; warp 1 (one
-// lane) issues the products; warps 2..5 read the accumulators, form the result
-// and write it as planes through shared memory and TMA.
+// planes, 64 x 64 of the right ones, in a ring of two stages; warp 1 (one
+// lane) issues the products; warps 2..9 read the accumulators, form the result
+// and write it as planes through shared memory (the idle ring) and TMA. Two
+// CTAs share an SM (256 columns of tensor memory, 98 KB of shared memory
+// each): one's loads cover the other's epilogue, and the next product's CTAs
+// set themselves up while this one's finish.
 constexpr int kGram = 0, kPoly = 1, kApply = 2, kLast = 3;
-constexpr int kOrthoStages = 3, kOrthoHH = 6;
+constexpr int kOrthoStages = 2, kOrthoEpi = 256, kOrthoThreads = 64 + kOrthoEpi;
 constexpr unsigned kOrthoStageBytes = 2u * 16384u + 2u * 8192u;
-constexpr unsigned kOrthoSmem = 1024u + kOrthoStages * kOrthoStageBytes + 2u * 16384u + 256u;
+constexpr unsigned kOrthoSmem = 1024u + kOrthoStages * kOrthoStageBytes + 128u;
 
-struct OrthoTile {
+struct OrthoTiles {
     int tiles_i, tiles_j;  // tiles of the result
     int kblocks;           // 64 k each
     int down, down_next;   // bits the lift has gone down before and after this step
 };
 
 template <int MODE, typename T>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(kOrthoThreads, 2)
 ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ CUtensorMap rmap,
-                     const __grid_constant__ CUtensorMap omap, T* __restrict__ out, OrthoTile g, OrthoParams p) {
+                     const __grid_constant__ CUtensorMap omap, const __half* __restrict__ aplanes, T* __restrict__ out,
+                     OrthoTiles g, OrthoParams p) {
     extern __shared__ unsigned char ortho_smem_raw[];
     unsigned char* sm = ortho_smem_raw + ((1024u - (smem_addr(ortho_smem_raw) & 1023u)) & 1023u);
-    unsigned char* res = sm + kOrthoStages * kOrthoStageBytes;  // two 128 x 64 fp16 planes, 128-byte swizzle
-    uint64_t* bars = reinterpret_cast<uint64_t*>(res + 2u * 16384u);
-    uint64_t *full = bars, *empty = bars + kOrthoStages, *done = bars + 2 * kOrthoStages, *extra = done + 1;
-    uint32_t* slot = reinterpret_cast<uint32_t*>(extra + 1);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOrthoStages * kOrthoStageBytes);
+    uint64_t *full = bars, *empty = bars + kOrthoStages, *done = bars + 2 * kOrthoStages;
+    uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
     const unsigned per = static_cast<unsigned>(g.tiles_i) * g.tiles_j;
     const int mat = static_cast<int>(blockIdx.x / per);
     const unsigned t = blockIdx.x - static_cast<unsigned>(mat) * per;
@@ -174,33 +230,27 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
             mbar_init(&empty[s], 1);
         }
         mbar_init(done, 1);
-        mbar_init(extra, 1);
         fence_barrier_init();
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&lmap)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&rmap)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&omap)) : "memory");
     }
-    if (warp == 0) tc::alloc(slot, 512u);
+    if (warp == 0) tc::alloc(slot, 256u);
     tc::fence_before();
     __syncthreads();  // every CTA holds its tensor memory before the next launch may start
     tc::fence_after();
     const uint32_t tmem = *slot;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    bool ok = true;
 
     if (warp == 0) {
         if (lane == 0) {
-            if (MODE == kPoly) {
-                // A's own tile, for the b A term
-                mbar_expect_tx(extra, 2u * 16384u);
-                for (int pl = 0; pl < 2; ++pl)
-                    tc::tma_load_3d(res + pl * 16384, &lmap, j0, i0, pl * p.B + mat, extra);
-                mbar_arrive(extra);
-            }
             for (int kb = 0; kb < g.kblocks; ++kb) {
                 const int s = kb % kOrthoStages;
-                if (kb >= kOrthoStages &&
-                    !mbar_wait_bounded(&empty[s], static_cast<unsigned>(kb / kOrthoStages - 1) & 1u, kCopyWaitLimitNs)) {
-                    atomicOr(p.status, kStatusCopyTimeout);
-                    break;
-                }
+                if (kb >= kOrthoStages)
+                    ok = mbar_wait_bounded(&empty[s], static_cast<unsigned>(kb / kOrthoStages - 1) & 1u, kCopyWaitLimitNs);
+                if (!ok) break;
                 unsigned char* st = sm + s * kOrthoStageBytes;
                 mbar_expect_tx(&full[s], kOrthoStageBytes);
                 for (int pl = 0; pl < 2; ++pl) {
@@ -217,59 +267,60 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
         if (lane == 0) {
             constexpr bool mn = MODE >= kApply;
             constexpr uint32_t idesc = tc::idesc_f16(tc::kFmtF16, 64, false, mn);
-            bool ok = true;
             for (int kb = 0; kb < g.kblocks; ++kb) {
                 const int s = kb % kOrthoStages;
                 ok = mbar_wait_bounded(&full[s], static_cast<unsigned>(kb / kOrthoStages) & 1u, kCopyWaitLimitNs);
                 if (!ok) break;
                 tc::fence_after();
                 const unsigned a = smem_addr(sm + s * kOrthoStageBytes), b = a + 32768u;
-                const uint32_t hh = tmem + static_cast<uint32_t>(kb % kOrthoHH) * 64u, cross = tmem + kOrthoHH * 64u;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const unsigned bo = b + (mn ? k * 2048u : k * 32u);
                     const uint64_t ah = tc::sw128_desc(a + k * 32u), al = tc::sw128_desc(a + 16384u + k * 32u);
                     const uint64_t bh = tc::sw128_desc(bo), bl = tc::sw128_desc(bo + 8192u);
-                    tc::mma_f16(hh, ah, bh, idesc, kb >= kOrthoHH || k > 0);
-                    tc::mma_f16(cross, ah, bl, idesc, (kb | k) != 0);
-                    tc::mma_f16(cross, al, bh, idesc, true);
+                    const int n16 = kb * 4 + k;
+                    tc::mma_f16(tmem + 192u, ah, bl, idesc, n16 > 0);
+                    tc::mma_f16(tmem + 192u, al, bh, idesc, true);
+                    tc::mma_f16(tmem + static_cast<uint32_t>(n16 % 3) * 64u, ah, bh, idesc, n16 >= 3);
                 }
                 tc::commit(&empty[s]);
             }
             if (ok) tc::commit(done);
-            else atomicOr(p.status, kStatusCopyTimeout);
         }
     } else {
-        const int quarter = warp & 3, row = quarter * 32 + lane, et = tid - 64;
-        bool ok = mbar_wait_bounded(done, 0u, kCopyWaitLimitNs);
-        if (MODE == kPoly) ok = ok && mbar_wait_bounded(extra, 0u, kCopyWaitLimitNs);
-        if (!ok) atomicOr(p.status, kStatusCopyTimeout);
-        ok = tc::bar_and(1, 128, ok);  // one decision for all four warps
-        tc::fence_after();
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        const int nacc = min(g.kblocks, kOrthoHH);
-        if (ok) {
-            const int i = i0 + row;
-            const int lift = max(0, p.lift[mat] - g.down);
-            // powers of two that undo the lift (A carries it twice, A A four times)
-            const float ub = scalbnf(p.b, -2 * lift), uc = scalbnf(p.c, -4 * lift);
-            const float ux = scalbnf(1.f, MODE == kLast ? -lift : max(0, p.lift[mat] - g.down_next) - lift);
-            float* stage = reinterpret_cast<float*>(sm);  // kLast: 128 x 65 floats over the idle ring
-            for (int cc = 0; cc < 4; ++cc) {
-                float v[16], w[16];
-                tc::ld16(lanes + kOrthoHH * 64 + cc * 16, v);
-                for (int q = 0; q < nacc; ++q) {
-                    tc::ld16(lanes + q * 64 + cc * 16, w);
-                    tc::wait_ld();
+        const int quarter = warp & 3, row = quarter * 32 + lane, et = tid - 64, half = (warp - 2) >> 2;
+        const int i = i0 + row, lift = p.lift[mat];
+        const int now = max(0, lift - g.down), next = max(0, lift - g.down_next);
+        // kPoly: this thread's 32 entries of A, read while the products run
+        uint4 ah[4], al[4];
+        if constexpr (MODE == kPoly) {
+            const size_t plane = static_cast<size_t>(p.B) * p.n * p.np;
+            const __half* ar = aplanes + (static_cast<size_t>(mat) * p.n + i) * p.np + j0 + half * 32;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] += w[e];
-                }
-                // chunks 2cc, 2cc + 1 of this row in the swizzled planes
-                uint4* hp = reinterpret_cast<uint4*>(res + row * 128);
-                uint4* lp = reinterpret_cast<uint4*>(res + 16384 + row * 128);
+            for (int q = 0; q < 4; ++q) {
+                // the pitch is a multiple of 8: a chunk of 8 that starts before it lies inside the row
+                const bool on = i < p.n && j0 + half * 32 + q * 8 < p.np;
+                ah[q] = on ? *reinterpret_cast<const uint4*>(ar + q * 8) : make_uint4(0, 0, 0, 0);
+                al[q] = on ? *reinterpret_cast<const uint4*>(ar + plane + q * 8) : make_uint4(0, 0, 0, 0);
+            }
+        }
+        // powers of two that undo the lift (A carries it twice, A A four times)
+        const float ux = scalbnf(1.f, (MODE == kLast ? 0 : next) - now);
+        const float ub = MODE == kPoly ? scalbnf(p.b, -2 * now) : 0.f, uc = MODE == kPoly ? scalbnf(p.c, -4 * now) : 0.f;
+        ok = tc::bar_and(1, kOrthoEpi, mbar_wait_bounded(done, 0u, kCopyWaitLimitNs));  // one decision for all the warps
+        if (ok) {
+            tc::fence_after();
+            const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 32;
+            float* fres = reinterpret_cast<float*>(sm);
+            uint4 *hp = reinterpret_cast<uint4*>(sm + row * 128), *lp = reinterpret_cast<uint4*>(sm + 16384 + row * 128);
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+                float v[16];
+                ortho_sum4(at + cc * 16, 64u, v);
                 if constexpr (MODE == kLast) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) stage[row * 65 + cc * 16 + e] = v[e] * (1.f / (kOrthoSP * kOrthoSX)) * ux;
+                    for (int e = 0; e < 16; ++e)
+                        fres[row * 64 + ((half * 32 + cc * 16 + e) ^ (row & 31))] = v[e] * (1.f / (kOrthoSP * kOrthoSX)) * ux;
                 } else {
                     float scale;  // accumulator to plane units
                     if constexpr (MODE == kGram) scale = kOrthoSA / (kOrthoSX * kOrthoSX);
@@ -277,55 +328,266 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
                     else scale = ux / kOrthoSP;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int ch = (2 * cc + h) ^ (row & 7);
                         __half hi[8], lo[8];
                         if constexpr (MODE == kPoly) {
-                            *reinterpret_cast<uint4*>(hi) = hp[ch];
-                            *reinterpret_cast<uint4*>(lo) = lp[ch];
+                            *reinterpret_cast<uint4*>(hi) = ah[cc * 2 + h];
+                            *reinterpret_cast<uint4*>(lo) = al[cc * 2 + h];
                         }
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             float r = v[h * 8 + e] * scale;
                             if constexpr (MODE == kPoly) {
                                 const float av = (__half2float(hi[e]) + __half2float(lo[e])) * (kOrthoSP / kOrthoSA);
-                                const int j = j0 + cc * 16 + h * 8 + e;
+                                const int j = j0 + half * 32 + cc * 16 + h * 8 + e;
                                 r = fmaf(uc, r, fmaf(ub, av, i == j ? p.a * kOrthoSP : 0.f));
                             }
                             ortho_split(r, hi[e], lo[e]);
                         }
+                        const int ch = (half * 4 + cc * 2 + h) ^ (row & 7);
                         hp[ch] = *reinterpret_cast<uint4*>(hi);
                         lp[ch] = *reinterpret_cast<uint4*>(lo);
                     }
                 }
             }
             if constexpr (MODE == kLast) {
-                tc::bar_sync(1, 128);
+                tc::bar_sync(1, kOrthoEpi);
                 const int ni = min(128, p.n - i0), nj = min(64, p.m - j0);
                 T* o = out + static_cast<size_t>(mat) * p.n * p.m;
-                for (int e = et; e < 8192; e += 128) {
+                for (int e = et; e < 8192; e += kOrthoEpi) {
                     // lanes along the result's contiguous side
                     const int ii = p.transposed ? e & 127 : e >> 6, jj = p.transposed ? e >> 7 : e & 63;
                     if (ii < ni && jj < nj) {
-                        const size_t at = p.transposed ? static_cast<size_t>(j0 + jj) * p.n + i0 + ii
+                        const size_t to = p.transposed ? static_cast<size_t>(j0 + jj) * p.n + i0 + ii
                                                        : static_cast<size_t>(i0 + ii) * p.m + j0 + jj;
-                        o[at] = ortho_from_float<T>(stage[ii * 65 + jj]);
+                        o[to] = ortho_from_float<T>(fres[ii * 64 + (jj ^ (ii & 31))]);
                     }
                 }
             } else {
                 fence_proxy_async();
-                tc::bar_sync(1, 128);
+                tc::bar_sync(1, kOrthoEpi);
                 if (et == 0) {
-                    for (int pl = 0; pl < 2; ++pl) tc::tma_store_3d(&omap, j0, i0, pl * p.B + mat, res + pl * 16384);
+                    for (int pl = 0; pl < 2; ++pl) tc::tma_store_3d(&omap, j0, i0, pl * p.B + mat, sm + pl * 16384);
                     tc::bulk_commit();
                     tc::bulk_wait_all();
                 }
             }
         }
     }
+    if (!ok) atomicOr(p.status, kStatusCopyTimeout);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    if (warp == 0) tc::dealloc(tmem, 512u);
+    if (warp == 0) tc::dealloc(tmem, 256u);
+}
+
+// The whole iteration of one small matrix (n <= 128, X and A together at most
+// seven blocks of 64 columns) in one CTA, its planes in shared memory all the
+// while. A block is 64 columns: the hi plane and the lo plane, 128 rows of 128
+// bytes each, 128-byte swizzle; rows and columns past the matrix are zero. X's
+// blocks serve as both operands of the Gram product (K-major) and as the right
+// one of the application (MN-major), A's as both of the polynomial, which
+// overwrites them with P. One thread issues a product's instructions, then all
+// warps turn the accumulators into the next operand. What bounds it is the
+// chain of 3 * steps dependent products, each a few hundred cycles of tensor
+// work between two barriers.
+constexpr int kOrthoSmallThreads = 512, kOrthoSmallBlocks = 7;
+constexpr unsigned kOrthoBlock = 2u * 16384u;
+constexpr int kOrthoMaxSteps = 64;
+struct OrthoSmall {
+    int steps, xb, nb;       // blocks of X, of A
+    int n16, m16;            // n, m rounded up to 16
+    unsigned tmem_cols;
+    short down[kOrthoMaxSteps + 1];
+};
+
+// hi and lo of entry (i, j), scaled, in a row of blocks
+__device__ __forceinline__ void ortho_put(unsigned char* blocks, int i, int j, float v) {
+    __half hi, lo;
+    ortho_split(v, hi, lo);
+    unsigned char* at = blocks + (j >> 6) * kOrthoBlock + i * 128 + ((((j & 63) >> 3) ^ (i & 7)) << 4) + (j & 7) * 2;
+    *reinterpret_cast<__half*>(at) = hi;
+    *reinterpret_cast<__half*>(at + 16384) = lo;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kOrthoSmallThreads, 1)
+ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_constant__ OrthoSmall g, OrthoParams p) {
+    extern __shared__ unsigned char ortho_smem_raw[];
+    __shared__ double ws[kOrthoSmallThreads / 32];
+    __shared__ double total;
+    __shared__ __align__(8) uint64_t done_bar;
+    __shared__ uint32_t slot;
+    unsigned char* xs = ortho_smem_raw + ((1024u - (smem_addr(ortho_smem_raw) & 1023u)) & 1023u);
+    unsigned char* as = xs + g.xb * kOrthoBlock;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int quarter = warp & 3, row = quarter * 32 + lane, part = warp >> 2;
+    if (tid == 0) {
+        mbar_init(&done_bar, 1);
+        fence_barrier_init();
+    }
+    if (warp == 0) tc::alloc(&slot, g.tmem_cols);
+    for (unsigned i = tid; i < (g.xb + g.nb) * kOrthoBlock / 16; i += kOrthoSmallThreads)
+        reinterpret_cast<uint4*>(xs)[i] = make_uint4(0, 0, 0, 0);
+    tc::fence_before();
+    __syncthreads();  // every CTA holds its tensor memory before the next launch may start
+    tc::fence_after();
+    const uint32_t tmem = slot, lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const int mat = blockIdx.x, count = p.R * p.C;
+    const T* xm = x + static_cast<size_t>(mat) * count;
+    const double a = ortho_sumsq(xm, count, tid, kOrthoSmallThreads, ws);
+    if (tid == 0) total = a;
+    __syncthreads();
+    const OrthoScale sc = ortho_scale(total, p.eps);
+    for (int e = tid; e < count; e += kOrthoSmallThreads) {
+        const int r = e / p.C, c = e - r * p.C;
+        const float v = scalbnf(ElemTraits<T>::to_float(__ldg(xm + e)), sc.e - sc.k) / sc.mant;
+        ortho_put(xs, p.transposed ? c : r, p.transposed ? r : c, v * kOrthoSX);
+    }
+    fence_proxy_async();
+    __syncthreads();
+
+    unsigned phase = 0;
+    bool ok = true;
+    // hands the operands over to the tensor cores, lets thread 0 issue, and waits for the products
+    auto product = [&](auto issue) {
+        fence_proxy_async();
+        tc::fence_before();
+        __syncthreads();
+        if (tid == 0) {
+            tc::fence_after();
+            issue();
+            tc::commit(&done_bar);
+        }
+        ok = __syncthreads_and(mbar_wait_bounded(&done_bar, phase & 1u, kCopyWaitLimitNs)) != 0;
+        ++phase;
+        tc::fence_after();
+    };
+    // square products: n columns, four accumulators n16 columns apart; K-major operands with ksteps of 16 k
+    auto square = [&](unsigned base, int ksteps) {
+        const uint32_t idesc = tc::idesc_f16(tc::kFmtF16, g.n16, false, false);
+        for (int k = 0; k < ksteps; ++k) {
+            const unsigned o = base + (k >> 2) * kOrthoBlock + (k & 3) * 32u;
+            const uint64_t h = tc::sw128_desc(o), l = tc::sw128_desc(o + 16384u);
+            tc::mma_f16(tmem + 3 * g.n16, h, l, idesc, k > 0);
+            tc::mma_f16(tmem + 3 * g.n16, l, h, idesc, true);
+            tc::mma_f16(tmem + (k % 3) * g.n16, h, h, idesc, k >= 3);
+        }
+    };
+    const int nchunks = g.n16 / 16;
+    for (int s = 0; s < g.steps && ok; ++s) {
+        const int now = max(0, sc.e - g.down[s]), next = max(0, sc.e - g.down[s + 1]);
+        // accumulators of order 0 past the number of k steps hold nothing: left out of the sums
+        auto sums = [&](int cc, int ksteps, float (&v)[16]) {
+            if (ksteps >= 3) {
+                ortho_sum4(lanes + cc * 16, g.n16, v);
+            } else {
+                float w[16];
+                tc::ld16(lanes + 3 * g.n16 + cc * 16, v);
+                for (int q = 0; q < ksteps; ++q) {
+                    tc::ld16(lanes + q * g.n16 + cc * 16, w);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] += w[e];
+                }
+            }
+        };
+        auto chunk_of = [&](unsigned char* blocks, int cc, int h) {
+            return reinterpret_cast<uint4*>(blocks + (cc >> 2) * kOrthoBlock + row * 128 + ((((cc & 3) * 2 + h) ^ (row & 7)) << 4));
+        };
+        auto put_chunk = [&](unsigned char* blocks, int cc, int h, const __half (&hi)[8], const __half (&lo)[8]) {
+            uint4* at = chunk_of(blocks, cc, h);
+            *at = *reinterpret_cast<const uint4*>(hi);
+            at[1024] = *reinterpret_cast<const uint4*>(lo);
+        };
+        // A = X X^T
+        product([&] { square(smem_addr(xs), g.m16 / 16); });
+        if (!ok) break;
+        for (int cc = part; cc < nchunks; cc += 4) {
+            float v[16];
+            sums(cc, g.m16 / 16, v);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                __half hi[8], lo[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ortho_split(v[h * 8 + e] * (kOrthoSA / (kOrthoSX * kOrthoSX)), hi[e], lo[e]);
+                put_chunk(as, cc, h, hi, lo);
+            }
+        }
+        // P = a I + b A + c A A, over A
+        product([&] { square(smem_addr(as), nchunks); });
+        if (!ok) break;
+        const float ub = scalbnf(p.b, -2 * now), uc = scalbnf(p.c, -4 * now) * (kOrthoSP / (kOrthoSA * kOrthoSA));
+        for (int cc = part; cc < nchunks; cc += 4) {
+            float v[16];
+            sums(cc, nchunks, v);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                __half hi[8], lo[8];
+                const uint4* at = chunk_of(as, cc, h);
+                *reinterpret_cast<uint4*>(hi) = *at;
+                *reinterpret_cast<uint4*>(lo) = at[1024];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float av = (__half2float(hi[e]) + __half2float(lo[e])) * (kOrthoSP / kOrthoSA);
+                    const bool diagonal = row == cc * 16 + h * 8 + e && row < p.n;
+                    ortho_split(fmaf(uc, v[h * 8 + e], fmaf(ub, av, diagonal ? p.a * kOrthoSP : 0.f)), hi[e], lo[e]);
+                }
+                put_chunk(as, cc, h, hi, lo);
+            }
+        }
+        // X = P X, up to 256 columns at a time: hi hi in columns 0.., the cross terms 256 (or the group's width) on
+        const bool last = s + 1 == g.steps;
+        for (int j0 = 0; j0 < g.m16 && ok; j0 += 256) {
+            const int width = min(256, g.m16 - j0);
+            product([&] {
+                const uint32_t idesc = tc::idesc_f16(tc::kFmtF16, width, false, true);
+                for (int k = 0; k < nchunks; ++k) {
+                    const unsigned ao = smem_addr(as) + (k >> 2) * kOrthoBlock + (k & 3) * 32u;
+                    const unsigned bo = smem_addr(xs) + (j0 >> 6) * kOrthoBlock + k * 2048u;
+                    const uint64_t ah = tc::sw128_desc(ao), al = tc::sw128_desc(ao + 16384u);
+                    const uint64_t bh = tc::sw128_desc(bo, kOrthoBlock), bl = tc::sw128_desc(bo + 16384u, kOrthoBlock);
+                    tc::mma_f16(tmem + width, ah, bl, idesc, k > 0);
+                    tc::mma_f16(tmem + width, al, bh, idesc, true);
+                    tc::mma_f16(tmem, ah, bh, idesc, k > 0);
+                }
+            });
+            if (!ok) break;
+            const float ux = scalbnf(1.f, (last ? 0 : next) - now) / (last ? kOrthoSP * kOrthoSX : kOrthoSP);
+            for (int cc = part; cc < width / 16; cc += 4) {
+                float v[16], w[16];
+                tc::ld16(lanes + cc * 16, v);
+                tc::ld16(lanes + width + cc * 16, w);
+                tc::wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = (v[e] + w[e]) * ux;
+                if (last) {
+                    // straight to `out`: a lane's 16 columns are neighbours (R <= C), or the lanes are (R > C)
+                    T* o = out + static_cast<size_t>(mat) * count;
+                    const int j = j0 + cc * 16;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (row < p.n && j + e < p.m)
+                            o[p.transposed ? (j + e) * p.n + row : row * p.m + j + e] = ortho_from_float<T>(v[e]);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        __half hi[8], lo[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) ortho_split(v[h * 8 + e], hi[e], lo[e]);
+                        put_chunk(xs, (j0 >> 4) + cc, h, hi, lo);
+                    }
+                }
+            }
+        }
+    }
+    if (!ok) atomicOr(p.status, kStatusCopyTimeout);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 0) tc::dealloc(tmem, g.tmem_cols);
 }
 
 }  // namespace dcnv4

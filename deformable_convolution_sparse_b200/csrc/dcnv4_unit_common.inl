@@ -6,7 +6,7 @@
 // executes griddepcontrol.wait before its first global access (DCNV4_PDL=0:
 // plain serialisation).
 template <typename... KA, typename... A>
-int launch_chained(void (*kern)(KA...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+int launch_chained(void (*kern)(KA...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads));

@@ -397,6 +397,18 @@ def test_orthogonalize(shape, co, dtype, cuda_device):
     assert torch.equal(dcn.orthogonalize(xd, coefficients=co), out)
 
 
+@pytest.mark.parametrize("shape", [(2, 5, 8), (3, 108, 64), (2, 129, 257), (1, 300, 128), (1, 60, 384), (1, 64, 385)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_orthogonalize_one_kernel_per_product(shape, cuda_device, monkeypatch):
+    """Matrices that one CTA holds, through the kernels of the larger ones too."""
+    x = torch.randn(*shape, generator=torch.Generator().manual_seed(5))
+    for form in ("", "products"):
+        monkeypatch.setenv("DCNV4_ORTHO_FORM", form)
+        out = dcn.orthogonalize(x.to(cuda_device))
+        assert dcn.device_status() == 0
+        _check_ortho(out, x, 5, MUON, 1e-7, "f32")
+
+
 @pytest.mark.parametrize("steps", [0, 1, 2, 12])
 def test_orthogonalize_steps_leading_shape_and_misaligned_rows(steps, cuda_device):
     g = torch.Generator().manual_seed(steps)
