@@ -42,7 +42,7 @@ int check_mx(const void* x, const void* codes, const void* scales, int M, int C,
 }
 
 unsigned mx_grid(long long blocks) {
-    // 64 blocks (256 threads) per CTA and round, at most 16 CTAs per SM's worth of CTAs
+    // 64 or 128 blocks (256 threads) per CTA and round, at most 16 CTAs per SM
     return static_cast<unsigned>(std::min<long long>((blocks + 63) / 64, 148LL * 16));
 }
 
@@ -50,8 +50,8 @@ template <typename T>
 int launch_quantize(const void* x, uint8_t* codes, uint8_t* scales, int C, long long blocks, cudaStream_t s) {
     const bool vec = C % 8 == 0 && aligned(x, 16);
     auto kern = vec ? dcnv4::mx_quantize_kernel<T, true> : dcnv4::mx_quantize_kernel<T, false>;
-    return launch_chained(kern, dim3(mx_grid(blocks)), 256, 0, s, static_cast<const T*>(x),
-                          reinterpret_cast<uint32_t*>(codes), scales, static_cast<unsigned>(blocks),
+    return launch_chained(kern, dim3(mx_grid((blocks + 1) / 2)), 256, 0, s, static_cast<const T*>(x),
+                          reinterpret_cast<uint2*>(codes), scales, static_cast<unsigned>(blocks),
                           dcnv4::make_fastdiv(static_cast<unsigned>((C + 31) / 32)), C);
 }
 
@@ -64,11 +64,9 @@ int launch_dequantize(const uint8_t* codes, const uint8_t* scales, void* x, int 
                           dcnv4::make_fastdiv(static_cast<unsigned>((C + 31) / 32)), C);
 }
 
-constexpr int kMxCtaThreads = 256;
-
 // Shape of the tensor-core kernel: how many record slots a CTA owns, and its
 // shared- and tensor-memory layout. False: a row does not fit.
-bool plan_mx(dcnv4::MxProjParams* p, int e, bool out16, int nsm, unsigned* smem, int* ntiles, int* per_sm) {
+bool plan_mx(dcnv4::MxProjParams* p, int e, bool out16, int nsm, unsigned* smem, int* ntiles, int* threads) {
     p->k64 = (p->nb + 1) / 2;
     p->kc = (p->nb + 3) / 4;
     p->mtiles = static_cast<int>((static_cast<long long>(p->M) + 127) / 128);
@@ -80,8 +78,9 @@ bool plan_mx(dcnv4::MxProjParams* p, int e, bool out16, int nsm, unsigned* smem,
     int n = std::max(1, (no16 + most - 1) / most);
     const int want = static_cast<int>(std::min<long long>((no16 + 31) / 32, nsm / std::max(1, p->mtiles)));
     n = std::max(n, want);
-    for (; n <= no16 / 16; ++n) {
-        const int nt = ((p->NO + n - 1) / n + 15) / 16 * 16;
+    for (; n <= (p->NO + 31) / 32; ++n) {
+        // several slot tiles: multiples of 32 slots, so that each starts on a whole block of the staging tile
+        const int each = (p->NO + n - 1) / n, nt = n == 1 ? no16 : (each + 31) / 32 * 32;
         p->NT = nt;
         p->groups = (nt + 127) / 128;
         p->sfa_col = static_cast<unsigned>(nt);
@@ -91,61 +90,91 @@ bool plan_mx(dcnv4::MxProjParams* p, int e, bool out16, int nsm, unsigned* smem,
         p->tmem_cols = 32;
         while (p->tmem_cols < cols) p->tmem_cols <<= 1;
         *ntiles = (p->NO + nt - 1) / nt;
-        // rows of the staging tile: packed when they are whole records whose stride spreads over the
-        // shared-memory banks (at most 4 lanes on one), else on 16-byte boundaries an odd number of
-        // 16-byte units apart
-        const int row = nt * e;
-        const bool whole = *ntiles == 1;
-        if (whole && out16 && (p->NO * e) % 8 == 0 && (p->NO * e) % 32 != 0) {
+        // the staging tile: records back to back when a CTA writes whole ones whose stride spreads over the
+        // shared-memory banks (at most 4 lanes on one); else swizzled blocks for TMA where the records' rows
+        // allow it; else rows an odd number of 16-byte units apart
+        const int row = p->NO * e;
+        unsigned stage_bytes;
+        if (*ntiles == 1 && out16 && row % 32 != 0) {
             p->store = dcnv4::kMxStoreTile;
-            p->pitch = p->NO * e;
+            p->pitch = row;
+            stage_bytes = 128u * row;
+        } else if (out16 && row % 16 == 0) {
+            p->store = dcnv4::kMxStoreTma;
+            p->pitch = *ntiles == 1 || nt * e % 128 == 0 ? 128 : 64;
+            stage_bytes = static_cast<unsigned>((nt * e + p->pitch - 1) / p->pitch) * 128u * p->pitch;
         } else {
-            const bool rows_ok = out16 && (p->NO * e) % 16 == 0 && ((p->NO - (*ntiles - 1) * nt) * e) % 16 == 0;
-            p->store = rows_ok ? dcnv4::kMxStoreRows : dcnv4::kMxStoreElems;
-            p->pitch = (row + 15) / 16 * 16;
+            p->store = dcnv4::kMxStoreElems;
+            p->pitch = (nt * e + 15) / 16 * 16;
             if (p->pitch % 32 == 0) p->pitch += 16;
+            stage_bytes = 128u * p->pitch;
         }
-        unsigned at = static_cast<unsigned>(p->k64) * 4096u;
+        // the staging tile first (TMA's swizzle counts from 1024-byte boundaries), the rest on 128-byte ones;
+        // what has to start as zeros (A, its scales, W, its scales) lies together
+        unsigned at = 0;
         auto take = [&](unsigned bytes) {
             const unsigned o = at;
             at += (bytes + 127u) / 128u * 128u;
             return o;
         };
+        p->smem_stage = take(stage_bytes);
+        p->smem_a = take(static_cast<unsigned>(p->k64) * 4096u);
         p->smem_sfa = take(512u * p->kc);
         p->smem_b = take(static_cast<unsigned>(p->k64) * 32u * nt);
         p->smem_sfb = take(512u * p->kc * p->groups);
-        p->smem_bias = take(4u * nt);
-        // the last chunk of a packed row may be written past its end, into the next row's start, by nobody:
-        // columns past `width` are not written
-        p->smem_stage = take(128u * p->pitch);
+        p->smem_bias = take(8u * nt);
         p->smem_bars = take(16u);
-        *smem = at + 128u;
-        if (*smem <= kTileSmemLimit) {
-            const unsigned sm_total = 227u * 1024u;
-            *per_sm = static_cast<int>(std::min({sm_total / (*smem + 1024u), 512u / p->tmem_cols, 4u}));
-            return true;
+        p->smem_ring = at;
+        // four CTAs of 256 threads per SM where they fit, else CTAs of 512
+        const unsigned quarter = (227u * 1024u / 4u) - 1024u - 1024u, ring = 2u * 16u * e;  // bytes per thread
+        if (p->tmem_cols <= 128 && at + 256u * ring <= quarter) {
+            *threads = 256;
+            *smem = at + 256u * ring + 1024u;
+        } else {
+            *threads = 512;
+            *smem = at + 512u * ring + 1024u;
         }
+        if (*smem <= kTileSmemLimit) return true;
     }
     return false;
+}
+
+template <typename T, int THREADS>
+int launch_mx_tc(const void* y, const uint8_t* wc, const uint8_t* ws, const float* bias, void* rec,
+                 dcnv4::MxProjParams p, unsigned smem, int ntiles, int nsm, cudaStream_t s) {
+    static_assert(dcnv4::MxShape<T, THREADS>::kRing == THREADS * 2u * 16u * sizeof(T), "the plan's ring");
+    const bool vec = p.C % 8 == 0 && aligned(y, 16);
+    CUtensorMap rmap{};
+    if (p.store == dcnv4::kMxStoreTma) {
+        auto encode = tensor_map_encoder();
+        const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.NO), static_cast<cuuint64_t>(p.M), 1u};
+        const cuuint64_t row = static_cast<cuuint64_t>(p.NO) * sizeof(T), str[2] = {row, row * static_cast<cuuint64_t>(p.M)};
+        const cuuint32_t box[3] = {static_cast<cuuint32_t>(p.pitch / sizeof(T)), 128u, 1u}, es[3] = {1u, 1u, 1u};
+        if (!encode || encode(&rmap, tma_dtype<T>(), 3, rec, dims, str, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              p.pitch == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return DCNV4_ERR_CUDA;
+    }
+    auto kern = vec ? dcnv4::predictor_mx_kernel<T, true, THREADS> : dcnv4::predictor_mx_kernel<T, false, THREADS>;
+    if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(kTileSmemLimit)) != cudaSuccess)
+        return DCNV4_ERR_LAUNCH;
+    const int per_sm = static_cast<int>(std::min({227u * 1024u / (smem + 1024u), 512u / p.tmem_cols, 1024u / THREADS}));
+    p.walkers = std::min(p.mtiles, std::max(1, nsm * std::max(1, per_sm) / ntiles));
+    return launch_chained(kern, dim3(static_cast<unsigned>(p.walkers) * static_cast<unsigned>(ntiles)), THREADS, smem, s,
+                          rmap, static_cast<const T*>(y), reinterpret_cast<const uint4*>(wc), ws, bias, static_cast<T*>(rec), p);
 }
 
 template <typename T>
 int launch_predictor_mx(const void* y, const uint8_t* wc, const uint8_t* ws, const float* bias, void* rec,
                         dcnv4::MxProjParams p, cudaStream_t s) {
-    const bool vec = p.C % 8 == 0 && aligned(y, 16);
     const int nsm = sm_count();
     if (nsm <= 0) return DCNV4_ERR_CUDA;
     unsigned smem = 0;
-    int ntiles = 0, per_sm = 0;
-    if (plan_mx(&p, sizeof(T), aligned(rec, 16), nsm, &smem, &ntiles, &per_sm)) {
-        auto kern = vec ? dcnv4::predictor_mx_kernel<T, true> : dcnv4::predictor_mx_kernel<T, false>;
-        if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(kTileSmemLimit)) != cudaSuccess)
-            return DCNV4_ERR_LAUNCH;
-        p.walkers = std::min(p.mtiles, std::max(1, nsm * per_sm / ntiles));
-        return launch_chained(kern, dim3(static_cast<unsigned>(p.walkers) * static_cast<unsigned>(ntiles)), kMxCtaThreads, smem, s,
-                              static_cast<const T*>(y), reinterpret_cast<const uint4*>(wc), ws, bias,
-                              static_cast<T*>(rec), p);
-    }
+    int ntiles = 0, threads = 0;
+    if (plan_mx(&p, sizeof(T), aligned(rec, 16), nsm, &smem, &ntiles, &threads))
+        return threads == 256 ? launch_mx_tc<T, 256>(y, wc, ws, bias, rec, p, smem, ntiles, nsm, s)
+                              : launch_mx_tc<T, 512>(y, wc, ws, bias, rec, p, smem, ntiles, nsm, s);
+    const bool vec = p.C % 8 == 0 && aligned(y, 16);
     auto kern = vec ? dcnv4::predictor_mx_plain_kernel<T, true> : dcnv4::predictor_mx_plain_kernel<T, false>;
     const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.M) + 31) / 32), static_cast<unsigned>((p.NO + 63) / 64));
     return launch_chained(kern, grid, 256, 0, s, static_cast<const T*>(y), reinterpret_cast<const uint32_t*>(wc), ws,

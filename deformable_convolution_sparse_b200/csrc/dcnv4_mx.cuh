@@ -27,7 +27,7 @@ constexpr int kMxBlock = 32;       // channels that share a scale
 constexpr int kMxBlockBytes = 16;  // their codes
 
 // Eight fp32 values as e2m1 codes, value 2i in the low half of byte i.
-__device__ __forceinline__ uint32_t e2m1_pack8(const float (&q)[8]) {
+__device__ __forceinline__ uint32_t e2m1_pack8(const float* q) {
     uint32_t r;
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
@@ -40,30 +40,12 @@ __device__ __forceinline__ uint32_t e2m1_pack8(const float (&q)[8]) {
     return r;
 }
 
-// Bits of the largest magnitude of 8 values (NaN above infinity above numbers).
-__device__ __forceinline__ uint32_t amax_bits8(const float (&v)[8]) {
-    uint32_t m = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-    return m;
-}
-
 // Scale byte of a block from the bits of its largest magnitude: the biased
 // exponent less 2 (a subnormal's biased exponent reads 0 and gives 2^-127 as
 // the clamp does), 255 for infinities and NaN.
 __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits) {
     const uint32_t ex = amax_bits >> 23;
     return ex == 255u ? 255u : (ex > 2u ? ex - 2u : 0u);
-}
-
-// 8 values of a block with scale byte s (below 255) as codes: 2^(127 - s) is a
-// normal fp32 number, s being at most 252.
-__device__ __forceinline__ uint32_t mx_codes8(float (&v)[8], uint32_t s) {
-    if (s == 255u) return 0u;
-    const float inv = __uint_as_float((254u - s) << 23);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= inv;
-    return e2m1_pack8(v);
 }
 
 // 2^(s - 127) in fp32 (s = 0: the subnormal 2^-127; s = 255: NaN)
@@ -80,35 +62,82 @@ __device__ __forceinline__ float e2m1_value(uint32_t c) {
     return (c & 8u) ? -v : v;
 }
 
-// Channels c0 .. c0+7 of a row of C channels, zeros past the end. VEC: C is a
+// Sixteen channels (half a block) as they lie in memory: 32 bytes of 16-bit
+// values, 64 of fp32.
+template <typename T>
+struct MxRaw {
+    static constexpr int kVecs = sizeof(T);
+    uint4 w[kVecs];
+};
+
+// Channels c0 .. c0+15 of a row of C channels, zeros past the end. VEC: C is a
 // multiple of 8 and the row is 16-byte aligned.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* __restrict__ row, int c0, int C, float (&v)[8]) {
+__device__ __forceinline__ void mx_load(const T* __restrict__ row, int c0, int C, MxRaw<T>& r) {
+    constexpr int per = 16 / sizeof(T);
     if constexpr (VEC) {
-        if (c0 >= C) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.f;
-            return;
-        }
-        if constexpr (sizeof(T) == 4) {
-            const float4 a = __ldg(reinterpret_cast<const float4*>(row + c0));
-            const float4 b = __ldg(reinterpret_cast<const float4*>(row + c0 + 4));
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        } else {
-            const uint4 a = __ldg(reinterpret_cast<const uint4*>(row + c0));
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack2(w[i], static_cast<T*>(nullptr));
-                v[2 * i] = f.x;
-                v[2 * i + 1] = f.y;
-            }
-        }
+        for (int q = 0; q < MxRaw<T>::kVecs; ++q)
+            r.w[q] = c0 + q * per < C ? __ldg(reinterpret_cast<const uint4*>(row + c0) + q) : make_uint4(0, 0, 0, 0);
     } else {
+        uint32_t w[4 * MxRaw<T>::kVecs];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c0 + i < C ? ElemTraits<T>::to_float(__ldg(row + c0 + i)) : 0.f;
+        for (int q = 0; q < 16; q += 4 / sizeof(T)) {
+            uint32_t v = 0u;
+#pragma unroll
+            for (int k = 0; k < 4 / static_cast<int>(sizeof(T)); ++k)
+                if (c0 + q + k < C) {
+                    if constexpr (sizeof(T) == 4) v = __float_as_uint(__ldg(row + c0 + q));
+                    else v |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(row) + c0 + q + k)) << (16 * k);
+                }
+            w[q * sizeof(T) / 4] = v;
+        }
+#pragma unroll
+        for (int q = 0; q < MxRaw<T>::kVecs; ++q) r.w[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
     }
+}
+
+// Quantises a block whose halves two neighbouring lanes hold: its scale byte,
+// and the codes of this lane's half. Bit patterns without their sign order as
+// the magnitudes do (NaN above infinity above numbers), so the largest one
+// takes integer maxima, two 16-bit values at a time. KEEP_ZERO: the codes of a
+// block of NaN (scale byte 255) are 0 (else they are arbitrary).
+template <bool KEEP_ZERO, typename T>
+__device__ __forceinline__ uint32_t mx_half_block(const MxRaw<T>& r, uint2& codes) {
+    constexpr int NW = 4 * MxRaw<T>::kVecs;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(r.w);
+    uint32_t bits;
+    if constexpr (sizeof(T) == 4) {
+        uint32_t m = 0u;
+#pragma unroll
+        for (int q = 0; q < NW; ++q) m = max(m, w[q] & 0x7fffffffu);
+        bits = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    } else {
+        uint32_t m = 0u;
+#pragma unroll
+        for (int q = 0; q < NW; ++q) m = __vmaxu2(m, w[q] & 0x7fff7fffu);
+        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m & 0xffffu, m >> 16);
+        if constexpr (std::is_same<T, __half>::value) bits = __float_as_uint(__half2float(__ushort_as_half(static_cast<uint16_t>(m))));
+        else bits = m << 16;
+    }
+    const uint32_t s = mx_scale_byte(bits);
+    // 2^(127 - s) is a normal fp32 number, s being at most 252 or 255
+    const float inv = __uint_as_float((254u - s) << 23);
+    float v[16];
+#pragma unroll
+    for (int q = 0; q < NW; ++q) {
+        if constexpr (sizeof(T) == 4) {
+            v[q] = __uint_as_float(w[q]) * inv;
+        } else {
+            const float2 f = unpack2(w[q], static_cast<T*>(nullptr));
+            v[2 * q] = f.x * inv;
+            v[2 * q + 1] = f.y * inv;
+        }
+    }
+    codes = make_uint2(e2m1_pack8(v), e2m1_pack8(v + 8));
+    if (KEEP_ZERO && s == 255u) codes = make_uint2(0u, 0u);
+    return s;
 }
 
 template <typename T>
@@ -118,33 +147,29 @@ __device__ __forceinline__ T mx_from_float(float v) {
     else return __float2bfloat16_rn(v);
 }
 
-// Quantisation: four lanes per block, 8 channels each, so that a warp reads 8
-// blocks as one contiguous run with 16-byte loads and writes their codes as
-// 128 contiguous bytes; the block's largest magnitude takes two shuffles.
+// Quantisation: two lanes per block, so that a warp reads 16 blocks as one
+// contiguous run with 16-byte loads and writes their codes as 256 contiguous
+// bytes.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256)
-mx_quantize_kernel(const T* __restrict__ x, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales,
+mx_quantize_kernel(const T* __restrict__ x, uint2* __restrict__ codes, uint8_t* __restrict__ scales,
                    unsigned blocks, FastDiv nb, int C) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int part = threadIdx.x & 3;
-    const unsigned stride = gridDim.x * (blockDim.x / 4);
+    const int half = threadIdx.x & 1;
+    const unsigned stride = gridDim.x * (blockDim.x / 2);
     // every lane of a warp makes the same number of rounds (the shuffles need all of them)
-    for (unsigned b0 = blockIdx.x * (blockDim.x / 4) + ((threadIdx.x & ~31u) >> 2); b0 < blocks; b0 += stride) {
-        const unsigned b = b0 + ((threadIdx.x & 31u) >> 2);
-        const bool on = b < blocks;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (on) {
-            const unsigned row = fdiv(b, nb);
-            load8<T, VEC>(x + static_cast<size_t>(row) * C, static_cast<int>(b - row * nb.d) * kMxBlock + part * 8, C, v);
-        }
-        uint32_t m = amax_bits8(v);
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const uint32_t s = mx_scale_byte(m);
-        if (on) {
-            codes[static_cast<size_t>(b) * 4 + part] = mx_codes8(v, s);
-            if (part == 0) scales[b] = static_cast<uint8_t>(s);
+    for (unsigned b0 = blockIdx.x * (blockDim.x / 2) + ((threadIdx.x & ~31u) >> 1); b0 < blocks; b0 += stride) {
+        const unsigned b = b0 + ((threadIdx.x & 31u) >> 1);
+        const unsigned row = fdiv(min(b, blocks - 1u), nb);
+        MxRaw<T> r;
+        // past the last block: the last one again, not written
+        mx_load<T, VEC>(x + static_cast<size_t>(row) * C, static_cast<int>(min(b, blocks - 1u) - row * nb.d) * kMxBlock + half * 16, C, r);
+        uint2 c;
+        const uint32_t s = mx_half_block<true>(r, c);
+        if (b < blocks) {
+            codes[static_cast<size_t>(b) * 2 + half] = c;
+            if (half == 0) scales[b] = static_cast<uint8_t>(s);
         }
     }
 }
@@ -208,17 +233,17 @@ struct MxProjParams {
     int NT;             // record slots per CTA (a multiple of 16)
     int k64, kc;        // steps of 64 channels (one instruction), groups of 128 (one column of scales)
     int groups;         // ceil(NT / 128)
-    int pitch;          // bytes between the rows of the output staging tile
+    int pitch;          // bytes between the rows of the staging tile (kMxStoreTma: of a block, 128 or 64)
     int store;          // kMxStore*
     unsigned tmem_cols, sfa_col, sfb_col;
-    unsigned smem_sfa, smem_b, smem_sfb, smem_bias, smem_stage, smem_bars;
+    unsigned smem_a, smem_sfa, smem_b, smem_sfb, smem_bias, smem_stage, smem_ring, smem_bars;
     unsigned* status;
 };
 
 // How a tile of records leaves the staging tile: as one bulk copy (rows are
-// whole records, back to back), as one bulk copy per row (16-byte multiples),
-// or element by element.
-constexpr int kMxStoreTile = 0, kMxStoreRows = 1, kMxStoreElems = 2;
+// whole records, back to back as in memory), by TMA (blocks of 128 or 64 bytes
+// of columns x 128 rows, swizzled), or element by element.
+constexpr int kMxStoreTile = 0, kMxStoreTma = 1, kMxStoreElems = 2;
 
 namespace tc {
 // kind::mxf4, both operands e2m1 K-major, one ue8m0 scale per 32 k, M = 128:
@@ -247,54 +272,43 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, unsigned saddr) {
 }
 }  // namespace tc
 
-// Eight channels of one block as loaded: 16 bytes of 16-bit values, 32 of fp32.
-template <typename T>
-struct MxRaw {
-    uint4 w[sizeof(T) == 4 ? 2 : 1];
-};
-template <typename T>
-__device__ __forceinline__ void mx_unpack(const MxRaw<T>& r, float (&v)[8]) {
-    if constexpr (sizeof(T) == 4) {
-        const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
-    } else {
-        const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = unpack2(w[i], static_cast<T*>(nullptr));
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
-        }
-    }
-}
-
-// The projection on the tensor cores. A CTA of 8 warps owns NT record slots
-// and walks tiles of 128 pixels: the tile is read as it lies in
-// memory (four lanes per block of 32 channels), quantised in registers and
+// The projection on the tensor cores. A CTA owns NT record slots and walks
+// tiles of 128 pixels: the tile is read as it lies in memory (two lanes per
+// block of 32 channels) through a ring of kAhead pieces per thread that runs
+// ahead across tiles with asynchronous copies, quantised in registers and
 // written to shared memory as tcgen05 operand (a block is one 16-byte row of
 // an unswizzled 8 x 16-byte core matrix) with its scale bytes beside it; one
 // thread moves the scales to tensor memory and issues the products (64
 // channels each); then all warps read the accumulators, add the bias, round,
-// and stage the records for bulk copies. The first loads of the next tile are
-// issued before the wait for the products. Several CTAs share an SM (tensor
-// memory: 128 or 256 columns each), so that one's loads overlap another's
-// epilogue.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(256, 4)
-predictor_mx_kernel(const T* __restrict__ y, const uint4* __restrict__ wcodes, const uint8_t* __restrict__ wscales,
-                    const float* __restrict__ bias, T* __restrict__ rec, MxProjParams p) {
+// and stage the records for bulk copies. Two CTAs of 512 threads share an SM,
+// or four of 256 where 128 columns of tensor memory and a quarter of the
+// shared memory do, so that one's loads overlap another's epilogue.
+template <typename T, int THREADS>
+struct MxShape {
+    static constexpr int kPiece = 16 * sizeof(T);  // sixteen channels
+    static constexpr int kAhead = 2;
+    static constexpr unsigned kRing = kAhead * THREADS * kPiece;
+};
+
+template <typename T, bool VEC, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+predictor_mx_kernel(const __grid_constant__ CUtensorMap rmap, const T* __restrict__ y, const uint4* __restrict__ wcodes,
+                    const uint8_t* __restrict__ wscales, const float* __restrict__ bias, T* __restrict__ rec,
+                    MxProjParams p) {
+    using S = MxShape<T, THREADS>;
     extern __shared__ unsigned char mx_smem_raw[];
-    unsigned char* sm = mx_smem_raw + ((128u - (smem_addr(mx_smem_raw) & 127u)) & 127u);
+    unsigned char* sm = mx_smem_raw + ((1024u - (smem_addr(mx_smem_raw) & 1023u)) & 1023u);
+    unsigned char* asm_ = sm + p.smem_a;
     unsigned char* sfa = sm + p.smem_sfa;
     unsigned char* bsm = sm + p.smem_b;
     unsigned char* sfb = sm + p.smem_sfb;
     float* bias_s = reinterpret_cast<float*>(sm + p.smem_bias);
+    int* channel = reinterpret_cast<int*>(bias_s + p.NT);  // projection channel of each slot
     unsigned char* stage = sm + p.smem_stage;
+    unsigned char* ring = sm + p.smem_ring;
     uint64_t* done = reinterpret_cast<uint64_t*>(sm + p.smem_bars);
     uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
     constexpr int E = sizeof(T);
-    constexpr int kBatch = E == 4 ? 2 : 4;  // eight-channel pieces loaded ahead
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = static_cast<int>(blockIdx.x) % p.walkers, walkers = p.walkers;
     const int s0 = static_cast<int>(blockIdx.x) / p.walkers * p.NT, width = min(p.NT, p.NO - s0), np = (width + 15) / 16 * 16;
@@ -304,6 +318,9 @@ predictor_mx_kernel(const T* __restrict__ y, const uint4* __restrict__ wcodes, c
         fence_barrier_init();
     }
     if (warp == 0) tc::alloc(slot, p.tmem_cols);
+    // what is not written below is padding: zero weights, zero scales, zero pixels
+    for (unsigned i = tid; i < (p.smem_bias - p.smem_a) / 16; i += THREADS) reinterpret_cast<uint4*>(asm_)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < width; i += THREADS) channel[i] = slot_channel(s0 + i, p.G, p.P);
     tc::fence_before();
     __syncthreads();  // every CTA holds its tensor memory before the next launch may start
     tc::fence_after();
@@ -311,78 +328,105 @@ predictor_mx_kernel(const T* __restrict__ y, const uint4* __restrict__ wcodes, c
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    const int pieces = 2 * p.nb;  // per thread and tile
-    MxRaw<T> ahead[kBatch];
-    // piece i of this thread in a tile: block (i * 256 + tid) / 4 of the tile's 128 * nb, eighth tid % 4
-    auto fetch = [&](int tile, int i, MxRaw<T>& r) {
-        const unsigned b = static_cast<unsigned>(i * 64 + (tid >> 2));
-        const unsigned row = fdiv(b, p.nbd);
-        const int c0 = static_cast<int>(b - row * p.nb) * kMxBlock + (tid & 3) * 8;
-        const long long m = static_cast<long long>(tile) * 128 + row;
-        const T* src = y + m * p.C + c0;
-        if constexpr (VEC) {
-            const bool on = m < p.M && c0 < p.C;
-#pragma unroll
-            for (int q = 0; q < (E == 4 ? 2 : 1); ++q)
-                r.w[q] = on ? __ldg(reinterpret_cast<const uint4*>(src) + q) : make_uint4(0, 0, 0, 0);
-        } else {
-            T* d = reinterpret_cast<T*>(&r);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) d[q] = m < p.M && c0 + q < p.C ? __ldg(src + q) : mx_from_float<T>(0.f);
+    // Pieces: the half blocks of a tile (two per block, 128 * nb blocks) go round the threads; (row, j) of this
+    // thread's current one, and the step to its next. With an odd nb the last round of 512 threads is half empty
+    // (whole warps).
+    const unsigned step_row = fdiv(THREADS / 2, p.nbd), step_j = THREADS / 2 - step_row * p.nb;
+    const unsigned first = static_cast<unsigned>(tid >> 1), first_row = fdiv(first, p.nbd), first_j = first - first_row * p.nb;
+    const int half = tid & 1;
+    auto advance = [&](unsigned& row, unsigned& j) {
+        row += step_row;
+        j += step_j;
+        if (j >= static_cast<unsigned>(p.nb)) {
+            j -= p.nb;
+            ++row;
         }
     };
-    auto fetch_batch = [&](int tile, int i0) {
+    // the ring: slots of this thread alone, so a wait for its own copies is all it takes
+    int ahead_tile = first_row < 128u ? cta : p.mtiles;  // (one block per row leaves half of 512 threads without any)
+    unsigned ahead_row = first_row, ahead_j = first_j, ahead_slot = 0;
+    const unsigned my_ring = smem_addr(ring) + tid * 16u;
+    auto fetch = [&]() {
+        if constexpr (VEC) {
+            if (ahead_tile < p.mtiles) {
+                const unsigned c0 = ahead_j * kMxBlock + half * 16;
+                if (static_cast<int>(ahead_row) < p.M - ahead_tile * 128) {
+                    const T* src = y + static_cast<size_t>(ahead_tile) * 128 * p.C + (ahead_row * p.C + c0);
+                    const unsigned dst = my_ring + ahead_slot;
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q)
-            if (i0 + q < pieces) fetch(tile, i0 + q, ahead[q]);
+                    for (int q = 0; q < MxRaw<T>::kVecs; ++q)
+                        if (static_cast<int>(c0) + q * (16 / E) < p.C)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + q * (S::kAhead * THREADS * 16)),
+                                         "l"(src + q * (16 / E))
+                                         : "memory");
+                }
+                ahead_slot = ahead_slot == (S::kAhead - 1) * THREADS * 16u ? 0u : ahead_slot + THREADS * 16u;
+                advance(ahead_row, ahead_j);
+                if (ahead_row >= 128u) {
+                    ahead_row = first_row;
+                    ahead_j = first_j;
+                    ahead_tile += walkers;
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
     };
-    int tile = cta;
-    if (tile < p.mtiles) fetch_batch(tile, 0);
+    for (int n = 0; n < S::kAhead; ++n) fetch();
 
-    // the weight's rows in record order, its scales, the bias; padding is zero
-    for (int i = tid; i < 2 * p.k64 * p.NT; i += 256) {
-        const int j = i / p.NT, s = i - j * p.NT;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (s < width && j < p.nb)
-            v = __ldg(wcodes + static_cast<size_t>(slot_channel(s0 + s, p.G, p.P)) * p.nb + j);
-        *reinterpret_cast<uint4*>(bsm + static_cast<size_t>(j) * p.NT * 16 + s * 16) = v;
+    // the weight's rows in record order with their scales, four blocks in flight per thread, and the bias
+    {
+        const int items = width * p.nb;
+        for (int i0 = tid; i0 < items; i0 += 4 * THREADS) {
+            uint4 v[4];
+            uint8_t sc[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int i = i0 + q * THREADS;
+                if (i < items) {
+                    const int s = static_cast<int>(fdiv(static_cast<unsigned>(i), p.nbd)), j = i - s * p.nb;
+                    const size_t at = static_cast<size_t>(channel[s]) * p.nb + j;
+                    v[q] = __ldg(wcodes + at);
+                    sc[q] = __ldg(wscales + at);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int i = i0 + q * THREADS;
+                if (i < items) {
+                    const int s = static_cast<int>(fdiv(static_cast<unsigned>(i), p.nbd)), j = i - s * p.nb;
+                    *reinterpret_cast<uint4*>(bsm + static_cast<size_t>(j) * p.NT * 16 + s * 16) = v[q];
+                    sfb[((j >> 2) * p.groups + (s >> 7)) * 512 + (s & 31) * 16 + ((s >> 5) & 3) * 4 + (j & 3)] = sc[q];
+                }
+            }
+        }
+        for (int i = tid; i < p.NT; i += THREADS) bias_s[i] = bias && i < width ? __ldg(bias + channel[i]) : 0.f;
     }
-    for (int i = tid; i < p.kc * p.groups * 128; i += 256) {
-        const int s = i % (p.groups * 128), k = i / (p.groups * 128);
-        uint32_t v = 0u;
-        if (s < width)
-            for (int q = 0; q < 4; ++q)
-                if (k * 4 + q < p.nb)
-                    v |= static_cast<uint32_t>(__ldg(wscales + static_cast<size_t>(slot_channel(s0 + s, p.G, p.P)) * p.nb +
-                                                     k * 4 + q)) << (8 * q);
-        *reinterpret_cast<uint32_t*>(sfb + (k * p.groups + (s >> 7)) * 512 + (s & 31) * 16 + ((s >> 5) & 3) * 4) = v;
-    }
-    for (int i = tid; i < p.kc * 128; i += 256) reinterpret_cast<uint32_t*>(sfa)[i] = 0u;
-    if (p.nb & 1)
-        for (int i = tid; i < 128; i += 256)
-            *reinterpret_cast<uint4*>(sm + static_cast<size_t>(p.nb) * 2048 + i * 16) = make_uint4(0, 0, 0, 0);
-    for (int i = tid; i < p.NT; i += 256) bias_s[i] = bias && i < width ? __ldg(bias + slot_channel(s0 + i, p.G, p.P)) : 0.f;
     __syncthreads();
 
     bool ok = true;
-    for (int it = 0; tile < p.mtiles; tile += walkers, ++it) {
-        for (int i0 = 0; i0 < pieces; i0 += kBatch) {
-            if (i0 > 0) fetch_batch(tile, i0);
+    unsigned at_slot = 0;
+    for (int tile = cta, it = 0; tile < p.mtiles; tile += walkers, ++it) {
+        const int rows = static_cast<int>(min(128LL, p.M - static_cast<long long>(tile) * 128));
+        for (unsigned row = first_row, j = first_j; row < 128u; advance(row, j)) {
+            const int c0 = static_cast<int>(j) * kMxBlock + half * 16;
+            MxRaw<T> r;
+            if constexpr (VEC) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(S::kAhead - 1) : "memory");
+                const unsigned char* at = ring + at_slot + tid * 16;
+                at_slot = at_slot == (S::kAhead - 1) * THREADS * 16u ? 0u : at_slot + THREADS * 16u;
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-                if (i0 + q >= pieces) break;
-                float v[8];
-                mx_unpack<T>(ahead[q], v);
-                uint32_t m = amax_bits8(v);
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                const uint32_t s = mx_scale_byte(m);
-                const unsigned b = static_cast<unsigned>((i0 + q) * 64 + (tid >> 2));
-                const unsigned row = fdiv(b, p.nbd), j = b - row * p.nb;
-                *reinterpret_cast<uint32_t*>(sm + j * 2048u + row * 16u + (tid & 3) * 4u) = mx_codes8(v, s);
-                if ((tid & 3) == 0)
-                    sfa[(j >> 2) * 512u + (row & 31u) * 16u + (row >> 5) * 4u + (j & 3u)] = static_cast<unsigned char>(s);
+                for (int q = 0; q < MxRaw<T>::kVecs; ++q)
+                    r.w[q] = static_cast<int>(row) < rows && c0 + q * (16 / E) < p.C
+                                 ? *reinterpret_cast<const uint4*>(at + q * (S::kAhead * THREADS * 16)) : make_uint4(0, 0, 0, 0);
+            } else {
+                mx_load<T, false>(y + (static_cast<long long>(tile) * 128 + min(static_cast<int>(row), rows - 1)) * p.C, c0, p.C, r);
             }
+            uint2 codes;
+            const uint32_t s = mx_half_block<false>(r, codes);
+            fetch();  // into the slot just read (the shuffle used what it held)
+            *reinterpret_cast<uint2*>(asm_ + j * 2048u + row * 16u + half * 8u) = codes;
+            if (half == 0)
+                sfa[(j >> 2) * 512u + (row & 31u) * 16u + (row >> 5) * 4u + (j & 3u)] = static_cast<unsigned char>(s);
         }
         fence_proxy_async();
         // the bulk copies that read the staging tile have done so
@@ -395,22 +439,24 @@ predictor_mx_kernel(const T* __restrict__ y, const uint4* __restrict__ wcodes, c
                 for (int i = 0; i < p.kc * p.groups; ++i) tc::copy_scales(tmem + p.sfb_col + i * 4, smem_addr(sfb + i * 512));
             for (int i = 0; i < p.kc; ++i) tc::copy_scales(tmem + p.sfa_col + i * 4, smem_addr(sfa + i * 512));
             for (int k = 0; k < p.k64; ++k)
-                tc::mma_mxf4(tmem, tc::smem_desc(smem_addr(sm) + k * 4096u, 2048u, 128u, 0u),
+                tc::mma_mxf4(tmem, tc::smem_desc(smem_addr(asm_) + k * 4096u, 2048u, 128u, 0u),
                              tc::smem_desc(smem_addr(bsm) + k * 32u * p.NT, 16u * p.NT, 128u, 0u),
                              tc::idesc_mxf4(np, (k & 1) * 2u), tmem + p.sfa_col + (k >> 1) * 4,
                              tmem + p.sfb_col + (k >> 1) * 4 * p.groups, k > 0);
             tc::commit(done);
         }
-        if (tile + walkers < p.mtiles) fetch_batch(tile + walkers, 0);
         ok = __syncthreads_and(mbar_wait_bounded(done, static_cast<unsigned>(it) & 1u, kCopyWaitLimitNs)) != 0;
         if (!ok) break;
         tc::fence_after();
 
-        // accumulator row = pixel: lane 32 * (warp % 4) + lane; 16-column chunks shared by two warps
+        // accumulator row = pixel: lane 32 * (warp % 4) + lane; 16-column chunks shared out among a quarter's warps
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         unsigned char* orow = stage + static_cast<size_t>(row) * p.pitch;
-        for (int c0 = (warp >> 2) * 16; c0 < np; c0 += 32) {
+        // kMxStoreTma: 16-byte chunk k of a row of a 128-byte block lies at k ^ (row mod 8), of a 64-byte one at
+        // k ^ (row / 2 mod 4), as the map's swizzle has it
+        const unsigned twist = p.pitch == 128 ? row & 7 : (row >> 1) & 3, cpb = static_cast<unsigned>(p.pitch) >> 4;
+        for (int c0 = (warp >> 2) * 16; c0 < np; c0 += THREADS / 8) {
             float v[16];
             tc::ld16(lanes + c0, v);
             tc::wait_ld();
@@ -419,16 +465,23 @@ predictor_mx_kernel(const T* __restrict__ y, const uint4* __restrict__ wcodes, c
                 const float4 b4 = *reinterpret_cast<const float4*>(bias_s + c0 + q);
                 v[q] += b4.x; v[q + 1] += b4.y; v[q + 2] += b4.z; v[q + 3] += b4.w;
             }
-            if (p.store != kMxStoreElems && c0 + 16 <= width) {
-                // rows start on 8-byte boundaries at least, on 16-byte ones unless they are packed
-                uint32_t w[16 * E / 4];
-                if constexpr (E == 4) {
+            uint32_t w[4 * E];
+            if constexpr (E == 4) {
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) w[q] = __float_as_uint(v[q]);
-                } else {
+                for (int q = 0; q < 16; ++q) w[q] = __float_as_uint(v[q]);
+            } else {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) w[q] = pack2(v[2 * q], v[2 * q + 1], static_cast<T*>(nullptr));
+                for (int q = 0; q < 8; ++q) w[q] = pack2(v[2 * q], v[2 * q + 1], static_cast<T*>(nullptr));
+            }
+            if (p.store == kMxStoreTma) {
+#pragma unroll
+                for (int q = 0; q < E; ++q) {
+                    const unsigned k = static_cast<unsigned>(c0) * E / 16u + q;
+                    const unsigned block = cpb == 8 ? k >> 3 : k >> 2, kk = k & (cpb - 1);
+                    *reinterpret_cast<uint4*>(stage + block * 128u * p.pitch + row * p.pitch + ((kk ^ twist) << 4)) =
+                        make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
                 }
+            } else if ((p.pitch & 7) == 0 && c0 + 16 <= width) {
                 if (p.pitch & 15) {
 #pragma unroll
                     for (int q = 0; q < 4 * E; q += 2)
@@ -447,7 +500,6 @@ predictor_mx_kernel(const T* __restrict__ y, const uint4* __restrict__ wcodes, c
         fence_proxy_async();
         tc::fence_before();
         __syncthreads();
-        const int rows = static_cast<int>(min(128LL, p.M - static_cast<long long>(tile) * 128));
         T* dst = rec + static_cast<size_t>(tile) * 128 * p.NO + s0;
         const unsigned row_bytes = static_cast<unsigned>(width) * E;
         if (p.store == kMxStoreTile && (rows * row_bytes) % 16u == 0u) {
@@ -455,15 +507,12 @@ predictor_mx_kernel(const T* __restrict__ y, const uint4* __restrict__ wcodes, c
                 asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
                              "r"(smem_addr(stage)), "r"(rows * row_bytes)
                              : "memory");
-        } else if (p.store == kMxStoreRows) {
-            if (warp == 0)
-                for (int r = lane; r < rows; r += 32)
-                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                                     dst + static_cast<size_t>(r) * p.NO),
-                                 "r"(smem_addr(stage + static_cast<size_t>(r) * p.pitch)), "r"(row_bytes)
-                                 : "memory");
+        } else if (p.store == kMxStoreTma) {
+            if (tid == 0)
+                for (unsigned q = 0; q * p.pitch < row_bytes; ++q)
+                    tc::tma_store_3d(&rmap, s0 + static_cast<int>(q * p.pitch / E), tile * 128, 0, stage + q * 128u * p.pitch);
         } else {
-            for (int r = warp; r < rows; r += 8)
+            for (int r = warp; r < rows; r += THREADS / 32)
                 for (int c = lane; c < width; c += 32)
                     dst[static_cast<size_t>(r) * p.NO + c] =
                         reinterpret_cast<const T*>(stage + static_cast<size_t>(r) * p.pitch)[c];
@@ -497,19 +546,14 @@ predictor_mx_plain_kernel(const T* __restrict__ y, const uint32_t* __restrict__ 
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     const int px = tid >> 3, sl = tid & 7;  // this thread's pixel and its slots sl, sl + 8, ...
     for (int b = 0; b < p.nb; ++b) {
-        if (tid < 128) {
-            const int r = tid >> 2, part = tid & 3;
-            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (m0 + r < p.M)
-                load8<T, VEC>(y + static_cast<size_t>(m0 + r) * p.C, b * kMxBlock + part * 8, p.C, v);
-            uint32_t m = amax_bits8(v);
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            const uint32_t s = mx_scale_byte(m);
-            const uint32_t c = mx_codes8(v, s);
-            const float sc = mx_scale_value(s);
+        if (tid < 64) {
+            const int r = tid >> 1, half = tid & 1;
+            MxRaw<T> raw;
+            mx_load<T, VEC>(y + static_cast<size_t>(min(m0 + r, p.M - 1LL)) * p.C, b * kMxBlock + half * 16, p.C, raw);
+            uint2 c;
+            const float sc = mx_scale_value(mx_half_block<true>(raw, c));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ys[r][part * 8 + i] = e2m1_value((c >> (4 * i)) & 15u) * sc;
+            for (int i = 0; i < 16; ++i) ys[r][half * 16 + i] = e2m1_value(((i < 8 ? c.x : c.y) >> (4 * (i & 7))) & 15u) * sc;
         }
         {
             const int r = tid >> 2, part = tid & 3;

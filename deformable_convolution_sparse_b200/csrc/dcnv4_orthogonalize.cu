@@ -140,18 +140,19 @@ int launch_small(const void* x, void* out, int steps, const int* down, const dcn
 
 template <int MODE, typename T>
 int product(const CUtensorMap& l, const CUtensorMap& r, const CUtensorMap& o, const __half* a, T* out, int cols, int k,
-            const int* down, const dcnv4::OrthoParams& p, cudaStream_t s) {
-    auto kern = dcnv4::ortho_product_kernel<MODE, T>;
-    if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(dcnv4::kOrthoSmem)) != cudaSuccess)
-        return DCNV4_ERR_LAUNCH;
+            const int* down, int nsm, const dcnv4::OrthoParams& p, cudaStream_t s) {
     dcnv4::OrthoTiles g{};
     g.tiles_i = (p.n + 127) / 128;
     g.tiles_j = (cols + 63) / 64;
     g.kblocks = (k + 63) / 64;
     g.down = down[0];
     g.down_next = down[1];
-    return launch_chained(kern, dim3(static_cast<unsigned>(p.B) * g.tiles_i * g.tiles_j), dcnv4::kOrthoThreads, dcnv4::kOrthoSmem,
-                          s, l, r, o, a, out, g, p);
+    const unsigned tiles = static_cast<unsigned>(p.B) * g.tiles_i * g.tiles_j;
+    const bool deep = tiles <= static_cast<unsigned>(nsm);
+    auto kern = deep ? dcnv4::ortho_product_kernel<MODE, T, 4> : dcnv4::ortho_product_kernel<MODE, T, 2>;
+    const unsigned smem = dcnv4::ortho_smem(deep ? 4 : 2);
+    if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess) return DCNV4_ERR_LAUNCH;
+    return launch_chained(kern, dim3(tiles), dcnv4::kOrthoThreads, smem, s, l, r, o, a, out, g, p);
 }
 
 template <typename T>
@@ -174,6 +175,8 @@ int launch(const void* x, void* out, unsigned char* ws, int steps, const int* do
         !plane_map(&qm, q, p.n, p.np, p.n, planes, 128))
         return DCNV4_ERR_CUDA;
     T* o = static_cast<T*>(out);
+    const int nsm = sm_count();
+    if (nsm <= 0) return DCNV4_ERR_CUDA;
     int rc = launch_chained(dcnv4::ortho_sumsq_kernel<T>, dim3(static_cast<unsigned>(p.B) * p.chunks), 256, 0, s,
                             static_cast<const T*>(x), part, p);
     if (rc) return rc;
@@ -181,11 +184,11 @@ int launch(const void* x, void* out, unsigned char* ws, int steps, const int* do
     rc = launch_chained(dcnv4::ortho_start_kernel<T>, dim3(st), 256, 0, s, static_cast<const T*>(x),
                         static_cast<const double*>(part), x0, steps == 0 ? o : static_cast<T*>(nullptr), p);
     for (int k = 0, cur = 0; k < steps && !rc; ++k, cur ^= 1) {
-        rc = product<dcnv4::kGram, float>(xm[cur], xr[cur], am, a, static_cast<float*>(nullptr), p.n, p.m, down + k, p, s);
-        if (!rc) rc = product<dcnv4::kPoly, float>(am, ar, qm, a, static_cast<float*>(nullptr), p.n, p.n, down + k, p, s);
+        rc = product<dcnv4::kGram, float>(xm[cur], xr[cur], am, a, static_cast<float*>(nullptr), p.n, p.m, down + k, nsm, p, s);
+        if (!rc) rc = product<dcnv4::kPoly, float>(am, ar, qm, a, static_cast<float*>(nullptr), p.n, p.n, down + k, nsm, p, s);
         if (rc) break;
-        if (k + 1 < steps) rc = product<dcnv4::kApply, float>(qm, xr[cur], xm[cur ^ 1], a, static_cast<float*>(nullptr), p.m, p.n, down + k, p, s);
-        else rc = product<dcnv4::kLast, T>(qm, xr[cur], xm[cur ^ 1], a, o, p.m, p.n, down + k, p, s);
+        if (k + 1 < steps) rc = product<dcnv4::kApply, float>(qm, xr[cur], xm[cur ^ 1], a, static_cast<float*>(nullptr), p.m, p.n, down + k, nsm, p, s);
+        else rc = product<dcnv4::kLast, T>(qm, xr[cur], xm[cur ^ 1], a, o, p.m, p.n, down + k, nsm, p, s);
     }
     return rc;
 }

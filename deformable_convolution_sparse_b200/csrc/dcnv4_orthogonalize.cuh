@@ -184,6 +184,13 @@ __device__ __forceinline__ void ortho_sum4(uint32_t at, uint32_t step, float (&v
     for (int e = 0; e < 16; ++e) v[e] += w[0][e];
 }
 
+// 16 bytes, loaded where it is written (not moved behind a later wait)
+__device__ __forceinline__ uint4 ortho_load(const __half* p) {
+    uint4 v;
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
 // One product of the iteration, a 128 x 64 tile of the result per CTA:
 //   kGram:  A = X X^T          (k over m; both operands K-major rows of X)
 //   kPoly:  P = aI + bA + cAA  (k over n; A is symmetric: both K-major)
@@ -191,16 +198,20 @@ __device__ __forceinline__ void ortho_sum4(uint32_t at, uint32_t step, float (&v
 //                               columns: an MN-major operand)
 //   kLast:  kApply with the result rounded to T and written to `out`
 // Warp 0 (one lane) loads 64 k at a time by TMA: 128 rows x 64 k of the left
-// planes, 64 x 64 of the right ones, in a ring of two stages; warp 1 (one
+// planes, 64 x 64 of the right ones, in a ring of STAGES; warp 1 (one
 // lane) issues the products; warps 2..9 read the accumulators, form the result
-// and write it as planes through shared memory (the idle ring) and TMA. Two
-// CTAs share an SM (256 columns of tensor memory, 98 KB of shared memory
-// each): one's loads cover the other's epilogue, and the next product's CTAs
-// set themselves up while this one's finish.
+// and write it as planes through shared memory (the idle ring) and TMA. A
+// product's time is mostly latency (per tile: first load 0.7 us, products 0.4
+// us per 64 k, epilogue 0.5, store 0.6; the launch about 2 us more), so the
+// ring is deep, four stages, while the tiles fit the SMs once; when there are
+// more tiles than SMs, two stages leave room for two CTAs per SM (256 columns
+// of tensor memory each) whose latencies overlap. Whole iteration, 432 x 256:
+// 18 matrices 147 us with four stages against 157 with two, 40 matrices 328
+// against 248.
 constexpr int kGram = 0, kPoly = 1, kApply = 2, kLast = 3;
-constexpr int kOrthoStages = 2, kOrthoEpi = 256, kOrthoThreads = 64 + kOrthoEpi;
+constexpr int kOrthoEpi = 256, kOrthoThreads = 64 + kOrthoEpi;
 constexpr unsigned kOrthoStageBytes = 2u * 16384u + 2u * 8192u;
-constexpr unsigned kOrthoSmem = 1024u + kOrthoStages * kOrthoStageBytes + 128u;
+constexpr unsigned ortho_smem(int stages) { return 1024u + stages * kOrthoStageBytes + 128u; }
 
 struct OrthoTiles {
     int tiles_i, tiles_j;  // tiles of the result
@@ -208,15 +219,15 @@ struct OrthoTiles {
     int down, down_next;   // bits the lift has gone down before and after this step
 };
 
-template <int MODE, typename T>
-__global__ void __launch_bounds__(kOrthoThreads, 2)
+template <int MODE, typename T, int STAGES>
+__global__ void __launch_bounds__(kOrthoThreads, STAGES == 2 ? 2 : 1)
 ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ CUtensorMap rmap,
                      const __grid_constant__ CUtensorMap omap, const __half* __restrict__ aplanes, T* __restrict__ out,
                      OrthoTiles g, OrthoParams p) {
     extern __shared__ unsigned char ortho_smem_raw[];
     unsigned char* sm = ortho_smem_raw + ((1024u - (smem_addr(ortho_smem_raw) & 1023u)) & 1023u);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOrthoStages * kOrthoStageBytes);
-    uint64_t *full = bars, *empty = bars + kOrthoStages, *done = bars + 2 * kOrthoStages;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + STAGES * kOrthoStageBytes);
+    uint64_t *full = bars, *empty = bars + STAGES, *done = bars + 2 * STAGES;
     uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const unsigned per = static_cast<unsigned>(g.tiles_i) * g.tiles_j;
@@ -225,7 +236,7 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
     const int i0 = static_cast<int>(t / g.tiles_j) * 128, j0 = static_cast<int>(t % g.tiles_j) * 64;
 
     if (tid == 0) {
-        for (int s = 0; s < kOrthoStages; ++s) {
+        for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -247,9 +258,9 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
     if (warp == 0) {
         if (lane == 0) {
             for (int kb = 0; kb < g.kblocks; ++kb) {
-                const int s = kb % kOrthoStages;
-                if (kb >= kOrthoStages)
-                    ok = mbar_wait_bounded(&empty[s], static_cast<unsigned>(kb / kOrthoStages - 1) & 1u, kCopyWaitLimitNs);
+                const int s = kb % STAGES;
+                if (kb >= STAGES)
+                    ok = mbar_wait_bounded(&empty[s], static_cast<unsigned>(kb / STAGES - 1) & 1u, kCopyWaitLimitNs);
                 if (!ok) break;
                 unsigned char* st = sm + s * kOrthoStageBytes;
                 mbar_expect_tx(&full[s], kOrthoStageBytes);
@@ -268,8 +279,8 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
             constexpr bool mn = MODE >= kApply;
             constexpr uint32_t idesc = tc::idesc_f16(tc::kFmtF16, 64, false, mn);
             for (int kb = 0; kb < g.kblocks; ++kb) {
-                const int s = kb % kOrthoStages;
-                ok = mbar_wait_bounded(&full[s], static_cast<unsigned>(kb / kOrthoStages) & 1u, kCopyWaitLimitNs);
+                const int s = kb % STAGES;
+                ok = mbar_wait_bounded(&full[s], static_cast<unsigned>(kb / STAGES) & 1u, kCopyWaitLimitNs);
                 if (!ok) break;
                 tc::fence_after();
                 const unsigned a = smem_addr(sm + s * kOrthoStageBytes), b = a + 32768u;
@@ -300,8 +311,11 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
             for (int q = 0; q < 4; ++q) {
                 // the pitch is a multiple of 8: a chunk of 8 that starts before it lies inside the row
                 const bool on = i < p.n && j0 + half * 32 + q * 8 < p.np;
-                ah[q] = on ? *reinterpret_cast<const uint4*>(ar + q * 8) : make_uint4(0, 0, 0, 0);
-                al[q] = on ? *reinterpret_cast<const uint4*>(ar + plane + q * 8) : make_uint4(0, 0, 0, 0);
+                ah[q] = al[q] = make_uint4(0, 0, 0, 0);
+                if (on) {
+                    ah[q] = ortho_load(ar + q * 8);
+                    al[q] = ortho_load(ar + plane + q * 8);
+                }
             }
         }
         // powers of two that undo the lift (A carries it twice, A A four times)
