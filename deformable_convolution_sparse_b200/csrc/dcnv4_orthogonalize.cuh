@@ -283,16 +283,14 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
                 ok = mbar_wait_bounded(&full[s], static_cast<unsigned>(kb / STAGES) & 1u, kCopyWaitLimitNs);
                 if (!ok) break;
                 tc::fence_after();
-                const unsigned a = smem_addr(sm + s * kOrthoStageBytes), b = a + 32768u;
+                const unsigned base = smem_addr(sm + s * kOrthoStageBytes);
+                const uint32_t a = tc::sw128(base), b = tc::sw128(base + 32768u);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const unsigned bo = b + (mn ? k * 2048u : k * 32u);
-                    const uint64_t ah = tc::sw128_desc(a + k * 32u), al = tc::sw128_desc(a + 16384u + k * 32u);
-                    const uint64_t bh = tc::sw128_desc(bo), bl = tc::sw128_desc(bo + 8192u);
-                    const int n16 = kb * 4 + k;
-                    tc::mma_f16(tmem + 192u, ah, bl, idesc, n16 > 0);
+                    const uint32_t ah = a + k * 2, al = ah + 1024, bh = b + (mn ? k * 128 : k * 2), bl = bh + 512;
+                    tc::mma_f16(tmem + 192u, ah, bl, idesc, kb > 0 || k > 0);
                     tc::mma_f16(tmem + 192u, al, bh, idesc, true);
-                    tc::mma_f16(tmem + static_cast<uint32_t>(n16 % 3) * 64u, ah, bh, idesc, n16 >= 3);
+                    tc::mma_f16(tmem + (k % 3) * 64u, ah, bh, idesc, kb > 0 || k >= 3);
                 }
                 tc::commit(&empty[s]);
             }
@@ -482,13 +480,17 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
     // square products: n columns, four accumulators n16 columns apart; K-major operands with ksteps of 16 k
     auto square = [&](unsigned base, int ksteps) {
         const uint32_t idesc = tc::idesc_f16(tc::kFmtF16, g.n16, false, false);
-        for (int k = 0; k < ksteps; ++k) {
-            const unsigned o = base + (k >> 2) * kOrthoBlock + (k & 3) * 32u;
-            const uint64_t h = tc::sw128_desc(o), l = tc::sw128_desc(o + 16384u);
-            tc::mma_f16(tmem + 3 * g.n16, h, l, idesc, k > 0);
-            tc::mma_f16(tmem + 3 * g.n16, l, h, idesc, true);
-            tc::mma_f16(tmem + (k % 3) * g.n16, h, h, idesc, k >= 3);
-        }
+        const uint32_t cross = tmem + 3 * g.n16;
+        uint32_t h = tc::sw128(base);
+        for (int k0 = 0; k0 < ksteps; k0 += 4, h += kOrthoBlock / 16)  // a block of 64 k
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k0 + k >= ksteps) break;
+                const uint32_t hk = h + k * 2, lk = hk + 1024;
+                tc::mma_f16(cross, hk, lk, idesc, k0 > 0 || k > 0);
+                tc::mma_f16(cross, lk, hk, idesc, true);
+                tc::mma_f16(tmem + (k % 3) * g.n16, hk, hk, idesc, k0 > 0 || k >= 3);
+            }
     };
     const int nchunks = g.n16 / 16;
     for (int s = 0; s < g.steps && ok; ++s) {
@@ -558,15 +560,16 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
             const int width = min(256, g.m16 - j0);
             product([&] {
                 const uint32_t idesc = tc::idesc_f16(tc::kFmtF16, width, false, true);
-                for (int k = 0; k < nchunks; ++k) {
-                    const unsigned ao = smem_addr(as) + (k >> 2) * kOrthoBlock + (k & 3) * 32u;
-                    const unsigned bo = smem_addr(xs) + (j0 >> 6) * kOrthoBlock + k * 2048u;
-                    const uint64_t ah = tc::sw128_desc(ao), al = tc::sw128_desc(ao + 16384u);
-                    const uint64_t bh = tc::sw128_desc(bo, kOrthoBlock), bl = tc::sw128_desc(bo + 16384u, kOrthoBlock);
-                    tc::mma_f16(tmem + width, ah, bl, idesc, k > 0);
-                    tc::mma_f16(tmem + width, al, bh, idesc, true);
-                    tc::mma_f16(tmem, ah, bh, idesc, k > 0);
-                }
+                uint32_t a = tc::sw128(smem_addr(as)), b = tc::sw128(smem_addr(xs) + (j0 >> 6) * kOrthoBlock, kOrthoBlock);
+                for (int k0 = 0; k0 < nchunks; k0 += 4, a += kOrthoBlock / 16, b += 4 * 128)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k0 + k >= nchunks) break;
+                        const uint32_t ah = a + k * 2, al = ah + 1024, bh = b + k * 128, bl = bh + 1024;
+                        tc::mma_f16(tmem + width, ah, bl, idesc, k0 > 0 || k > 0);
+                        tc::mma_f16(tmem + width, al, bh, idesc, true);
+                        tc::mma_f16(tmem, ah, bh, idesc, k0 > 0 || k > 0);
+                    }
             });
             if (!ok) break;
             const float ux = scalbnf(1.f, (last ? 0 : next) - now) / (last ? kOrthoSP * kOrthoSX : kOrthoSP);

@@ -74,7 +74,7 @@ int launch_grad_y(const CUtensorMap& wmap, const CUtensorMap& omap, const float*
         return DCNV4_ERR_LAUNCH;
     p.slices = (p.C + CT - 1) / CT;
     const long long items = static_cast<long long>(p.tiles) * p.slices;
-    return launch_chained(kern, dim3(static_cast<unsigned>(std::min<long long>(items, nsm))), 448, smem, s, wmap, omap,
+    return launch_chained(kern, dim3(static_cast<unsigned>(std::min<long long>(items, nsm))), dcnv4::kGradYThreads, smem, s, wmap, omap,
                           grec, gy, p);
 }
 
@@ -113,11 +113,11 @@ int launch(const void* y, const void* w, const float* grec, float* gy, float* gw
     static_assert(smem <= kTileSmemLimit, "the stages do not fit");
     if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess) return DCNV4_ERR_LAUNCH;
     p.slices = (p.C + 127) / 128;
-    rc = launch_chained(kern, dim3(static_cast<unsigned>(p.walkers) * p.slices * p.groups), 416, smem, s, grec,
+    rc = launch_chained(kern, dim3(static_cast<unsigned>(p.walkers) * p.slices * p.groups), dcnv4::kGradWThreads, smem, s, grec,
                         static_cast<const T*>(y), part, pbias, p);
     if (rc) return rc;
     const long long n = (static_cast<long long>(p.NO) * p.C + (gb ? p.NO : 0) + 31) / 32;
-    return launch_chained(dcnv4::pred_grad_w_join_kernel, dim3(static_cast<unsigned>(std::min<long long>(n, 148 * 8))), 256, 0, s,
+    return launch_chained(dcnv4::pred_grad_w_join_kernel, dim3(static_cast<unsigned>(std::min<long long>(n, 148 * 4))), 512, 0, s,
                           static_cast<const float*>(part), static_cast<const float*>(pbias), gw, gb, p);
 }
 

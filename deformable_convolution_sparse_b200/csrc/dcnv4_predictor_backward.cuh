@@ -41,6 +41,8 @@ struct PredBwdParams {
 };
 
 constexpr int kFlushTiles = 16;
+// the wait for a run of kFlushTiles tiles: every copy of it has its own limit, one after the other at worst
+constexpr uint64_t kFlushWaitLimitNs = 2 * kCopyWaitLimitNs;
 
 // projection channel of a record slot
 __host__ __device__ __forceinline__ int channel_of_slot(int s, int G, int P) {
@@ -103,48 +105,71 @@ pred_split_weight_kernel(const T* __restrict__ w, __nv_bfloat16* __restrict__ pl
     }
 }
 
-// The records' gradients of 128 pixels x 64 slots in registers: this
-// thread's (0..255) four rows tid / 8 + 32 q, slots 8 (tid % 8) .. + 7.
+// The records' gradients of 128 pixels x one chunk of up to 64 slots, spread
+// over kConv threads in pieces of eight slots: only the groups of eight below
+// the chunk's last 16-slot step are touched (a chunk's other columns are never
+// read, or only into sums that nobody reads). A thread has two pieces at most,
+// of one group and rows `rows` apart.
+constexpr int kConv = 512;
 struct GradPiece {
-    float4 v[4][2];
+    float4 v[2][2];
+};
+struct ChunkWalk {
+    int ng, row, grp, rows;  // groups of eight slots; this thread's first row, its group, rows per round
+    __device__ __forceinline__ ChunkWalk(int slots, int tid) {
+        ng = min(8, (slots + 15) / 16 * 2);
+        rows = kConv / ng;
+        row = tid / ng;
+        grp = tid - row * ng;
+        if (row >= rows) row = 128;  // the threads left over
+    }
 };
 template <bool VEC>
-__device__ __forceinline__ void load_grad(GradPiece& r, const float* __restrict__ g, long long m0, int s0, int tid,
-                                          const PredBwdParams& p) {
-    const int s = s0 + (tid & 7) * 8;
+__device__ __forceinline__ void load_grad(GradPiece& r, const ChunkWalk& walk, const float* __restrict__ g, long long m0,
+                                          int s0, const PredBwdParams& p) {
+    const int s = s0 + walk.grp * 8;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const long long m = m0 + (tid >> 3) + 32 * q;
-        const float* src = g + m * p.NO + s;
+    for (int q = 0; q < 2; ++q) {
+        const int row = walk.row + q * walk.rows;
+        const bool on = row < 128 && m0 + row < p.M;
+        const float* src = g + (m0 + row) * p.NO + s;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             if constexpr (VEC) {
-                r.v[q][h] = m < p.M && s + 4 * h < p.NO ? __ldg(reinterpret_cast<const float4*>(src + 4 * h))
-                                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+                r.v[q][h] = on && s + 4 * h < p.NO ? __ldg(reinterpret_cast<const float4*>(src + 4 * h))
+                                                   : make_float4(0.f, 0.f, 0.f, 0.f);
             } else {
                 float e[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) e[k] = m < p.M && s + 4 * h + k < p.NO ? __ldg(src + 4 * h + k) : 0.f;
+                for (int k = 0; k < 4; ++k) e[k] = on && s + 4 * h + k < p.NO ? __ldg(src + 4 * h + k) : 0.f;
                 r.v[q][h] = make_float4(e[0], e[1], e[2], e[3]);
             }
         }
     }
 }
-__device__ __forceinline__ void store_grad(unsigned char* stage, const GradPiece& r, int tid) {
+__device__ __forceinline__ void store_grad(unsigned char* stage, const ChunkWalk& walk, const GradPiece& r) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 2; ++q) {
+        const int row = walk.row + q * walk.rows;
+        if (row >= 128) continue;
         const float v[8] = {r.v[q][0].x, r.v[q][0].y, r.v[q][0].z, r.v[q][0].w,
                             r.v[q][1].x, r.v[q][1].y, r.v[q][1].z, r.v[q][1].w};
-        store_split8<3>(stage, 16384u, (tid >> 3) + 32 * q, tid & 7, v);
+        store_split8<3>(stage, 16384u, row, walk.grp, v);
     }
 }
+// the operand tiles this warp's threads wrote, handed over (one arrival per warp)
+__device__ __forceinline__ void hand_over(uint64_t* bar, int lane) {
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
 
-// grad_y: tiles of 128 pixels x CT channels. Warps 0..7 read g 64 slots at a
-// time (two chunks ahead, in registers) and write its planes as the left
-// operand (K-major); warp 8 loads the same slots' rows of W's planes by TMA as
-// the right one (its rows run along the channels: MN-major); warp 9 issues the
-// products; warps 10..13 read the accumulators (two sets, in turn) and write
-// the tile through shared memory and TMA.
+// grad_y: tiles of 128 pixels x CT channels. Warps 0..15 read g 64 slots at a
+// time (three chunks ahead, in registers) and write its planes as the left
+// operand (K-major); warp 16 loads the same slots' rows of W's planes by TMA
+// as the right one (its rows run along the channels: MN-major); warp 17 issues
+// the products; warps 18..21 read the accumulators (two sets, in turn) and
+// write the tile through shared memory and TMA.
 template <int CT, int WP>
 struct GradYShape {
     static constexpr int kStages = 2;
@@ -156,8 +181,10 @@ struct GradYShape {
     static constexpr unsigned kAcc = (kHigh + 1) * CT;  // columns of one set
 };
 
+constexpr int kGradYThreads = kConv + 64 + 128;
+
 template <int CT, int WP, bool VEC>
-__global__ void __launch_bounds__(448, 1)
+__global__ void __launch_bounds__(kGradYThreads, 1)
 pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap omap,
                    const float* __restrict__ grec, float* __restrict__ gy, PredBwdParams p) {
     using S = GradYShape<CT, WP>;
@@ -171,7 +198,7 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
 
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&full_g[s], 256);
+            mbar_init(&full_g[s], kConv / 32);
             mbar_init(&full_w[s], 1);
             mbar_init(&empty[s], 1);
             mbar_init(&acc_full[s], 1);
@@ -179,7 +206,7 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         }
         fence_barrier_init();
     }
-    if (warp == 8) tc::alloc(slot, 512u);
+    if (warp == 16) tc::alloc(slot, 512u);
     tc::fence_before();
     __syncthreads();  // every CTA holds its tensor memory before the next launch may start
     tc::fence_after();
@@ -193,36 +220,38 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     const long long steps = mine * p.chunks;
     bool ok = true;
 
-    if (warp < 8) {
+    if (warp < 16) {
         auto where = [&](long long it, long long& m0, int& s0) {
             const long long item = blockIdx.x + (it / p.chunks) * gridDim.x;
             m0 = item / p.slices * 128;
             s0 = static_cast<int>(it % p.chunks) * 64;
         };
-        GradPiece ra, rb;
-        long long m0;
-        int s0;
-        if (steps > 0) {
-            where(0, m0, s0);
-            load_grad<VEC>(ra, grec, m0, s0, tid, p);
-        }
-        auto step = [&](long long it, GradPiece& now, GradPiece& next) {
-            if (it + 1 < steps) {
-                where(it + 1, m0, s0);
-                load_grad<VEC>(next, grec, m0, s0, tid, p);
+        GradPiece r[3];
+        const ChunkWalk whole(64, tid), tail(p.NO - (p.chunks - 1) * 64, tid);
+        auto fetch = [&](long long it, GradPiece& to) {
+            long long m0;
+            int s0;
+            if (it < steps) {
+                where(it, m0, s0);
+                load_grad<VEC>(to, s0 + 64 < p.NO ? whole : tail, grec, m0, s0, p);
             }
+        };
+        fetch(0, r[0]);
+        fetch(1, r[1]);
+        auto step = [&](long long it, GradPiece& now, GradPiece& next) {
+            fetch(it + 2, next);
             const int s = static_cast<int>(it & 1);
             if (it >= 2) ok = mbar_wait_bounded(&empty[s], static_cast<unsigned>((it >> 1) - 1) & 1u, kCopyWaitLimitNs);
             if (!ok) return;
-            store_grad(sm + s * S::kStage, now, tid);
-            fence_proxy_async();
-            mbar_arrive(&full_g[s]);
+            store_grad(sm + s * S::kStage, static_cast<int>(it % p.chunks) + 1 < p.chunks ? whole : tail, now);
+            hand_over(&full_g[s], lane);
         };
-        for (long long it = 0; it < steps && ok; it += 2) {
-            step(it, ra, rb);
-            if (it + 1 < steps && ok) step(it + 1, rb, ra);
+        for (long long it = 0; it < steps && ok; it += 3) {
+            step(it, r[0], r[2]);
+            if (it + 1 < steps && ok) step(it + 1, r[1], r[0]);
+            if (it + 2 < steps && ok) step(it + 2, r[2], r[1]);
         }
-    } else if (warp == 8) {
+    } else if (warp == 16) {
         if (lane == 0) {
             for (long long it = 0; it < steps && ok; ++it) {
                 const int s = static_cast<int>(it & 1);
@@ -238,7 +267,7 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 mbar_arrive(&full_w[s]);
             }
         }
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         if (lane == 0) {
             constexpr uint32_t idesc = tc::idesc_f16(tc::kFmtBf16, CT, false, true);
             for (long long it = 0; it < steps && ok; ++it) {
@@ -252,19 +281,21 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 if (!ok) break;
                 tc::fence_after();
                 const uint32_t acc = tmem + b * S::kAcc, low = acc + S::kHigh * CT;
-                const unsigned a = smem_addr(sm + s * S::kStage), w = a + 3u * 16384u;
+                const unsigned base = smem_addr(sm + s * S::kStage);
+                const uint32_t a = tc::sw128(base), w = tc::sw128(base + 3u * 16384u, 8192u);
                 const int ksteps = (min(64, p.NO - chunk * 64) + 15) / 16;
-                for (int k = 0; k < ksteps; ++k) {
-                    const int n16 = chunk * 4 + k;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k >= ksteps) break;
 #pragma unroll
                     for (int i = 0; i < 3; ++i)
 #pragma unroll
                         for (int j = 0; j < WP; ++j) {
                             if (i + j > 2) continue;
-                            const uint64_t ad = tc::sw128_desc(a + i * 16384u + k * 32u);
-                            const uint64_t bd = tc::sw128_desc(w + j * (CT / 64) * 8192u + k * 2048u, 8192u);
-                            if (i + j == 0) tc::mma_f16(acc + (n16 % S::kHigh) * CT, ad, bd, idesc, n16 >= S::kHigh);
-                            else tc::mma_f16(low, ad, bd, idesc, n16 > 0 || !(i == (WP > 1 ? 0 : 1) && j == (WP > 1 ? 1 : 0)));
+                            const uint32_t ad = a + (i * 16384 + k * 32) / 16, bd = w + (j * (CT / 64) * 8192 + k * 2048) / 16;
+                            const bool first_low = k == 0 && i == (WP > 1 ? 0 : 1) && j == (WP > 1 ? 1 : 0);
+                            if (i + j == 0) tc::mma_f16(acc + (k % S::kHigh) * CT, ad, bd, idesc, chunk > 0 || k >= S::kHigh);
+                            else tc::mma_f16(low, ad, bd, idesc, chunk > 0 || !first_low);
                         }
                 }
                 tc::commit(&empty[s]);
@@ -272,7 +303,7 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             }
         }
     } else {
-        const int quarter = warp & 3, row = quarter * 32 + lane, et = tid - 320;
+        const int quarter = warp & 3, row = quarter * 32 + lane, et = tid - (kConv + 64);
         const int high = min(S::kHigh, (p.NO + 15) / 16);
         for (long long n = 0; n < mine; ++n) {
             const long long item = blockIdx.x + n * gridDim.x;
@@ -324,14 +355,14 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    if (warp == 8) tc::dealloc(tmem, 512u);
+    if (warp == 16) tc::dealloc(tmem, 512u);
 }
 
 // grad_weight and grad_bias, partial sums: 128 channels x 128 slots per CTA,
-// the pixels of every walkers-th tile. Warps 0..7 write the planes of y (the
+// the pixels of every walkers-th tile. Warps 0..15 write the planes of y (the
 // left operand) and, 64 slots at a time, of g (the right one), both with rows
 // that run along channels or slots: MN-major; the same threads sum g for the
-// bias. Warp 8 issues the products, warps 9..12 read the accumulators out to
+// bias. Warps 16..19 issue the products and read the accumulators out to
 // part [walkers][NO][C], lanes along the channels. A slice of at most 64
 // channels reads its one block of 64 for both halves of the M = 128 products.
 template <typename T>
@@ -363,8 +394,10 @@ __device__ __forceinline__ void load_y8(const T* __restrict__ y, long long m, in
     }
 }
 
+constexpr int kGradWThreads = kConv + 128;
+
 template <typename T, bool VEC, bool VECY>
-__global__ void __launch_bounds__(416, 1)
+__global__ void __launch_bounds__(kGradWThreads, 1)
 pred_grad_w_kernel(const float* __restrict__ grec, const T* __restrict__ y, float* __restrict__ part,
                    float* __restrict__ pbias, PredBwdParams p) {
     using S = GradWShape<T>;
@@ -373,23 +406,21 @@ pred_grad_w_kernel(const float* __restrict__ grec, const T* __restrict__ y, floa
     unsigned char* sm = pb_smem_raw + ((1024u - (smem_addr(pb_smem_raw) & 1023u)) & 1023u);
     unsigned char* gsm = sm + S::kYStages * S::kY;
     uint64_t* bars = reinterpret_cast<uint64_t*>(gsm + 2 * S::kG);
-    uint64_t *full_y = bars, *empty_y = bars + 2, *full_g = bars + 4, *empty_g = bars + 6, *acc_full = bars + 8,
-             *acc_empty = bars + 9;
+    uint64_t *full_y = bars, *empty_y = bars + 2, *full_g = bars + 4, *empty_g = bars + 6, *acc_full = bars + 8;
     uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 10);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&full_y[s], 256);
+            mbar_init(&full_y[s], kConv / 32);
             mbar_init(&empty_y[s], 1);
-            mbar_init(&full_g[s], 256);
+            mbar_init(&full_g[s], kConv / 32);
             mbar_init(&empty_g[s], 1);
         }
         mbar_init(acc_full, 1);
-        mbar_init(acc_empty, 128);
         fence_barrier_init();
     }
-    if (warp == 8) tc::alloc(slot, 512u);
+    if (warp == 16) tc::alloc(slot, 512u);
     tc::fence_before();
     __syncthreads();  // every CTA holds its tensor memory before the next launch may start
     tc::fence_after();
@@ -406,141 +437,162 @@ pred_grad_w_kernel(const float* __restrict__ grec, const T* __restrict__ y, floa
     const int mine = walker < p.tiles ? (p.tiles - walker + p.walkers - 1) / p.walkers : 0;
     bool ok = true;
 
-    if (warp < 8) {
+    if (warp < 16) {
         const bool sums = c0 == 0 && pbias != nullptr;
-        float bs[2][8] = {};
-        GradPiece ra;
-        const int npiece = wide ? 8 : 4;  // eight-channel pieces of y per thread
+        float bs[2][8] = {};              // [chunk][slot of this thread's group]
+        const int npiece = wide ? 4 : 2;  // eight-channel pieces of y per thread
         const int per_row = wide ? 16 : 8;
-        uint4 yr[4][kQ];
-        auto fetch_y = [&](long long m0, int q0) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int e = (q0 + q) * 256 + tid;
-                load_y8<T, VECY>(y, m0 + e / per_row, c0 + e % per_row * 8, p, yr[q]);
-            }
-        };
-        if (mine > 0) {
-            const long long m0 = static_cast<long long>(walker) * 128;
-            fetch_y(m0, 0);
-            load_grad<VEC>(ra, grec, m0, g0, tid, p);
-        }
-        for (int i = 0; i < mine && ok; ++i) {
+        const ChunkWalk walk0(p.NO - g0, tid), walk1(nch == 2 ? p.NO - g0 - 64 : 64, tid);
+        // pieces of y loaded ahead (the others, of fp32, when it is their turn)
+        constexpr int kYAhead = sizeof(T) == 4 ? 2 : 4;
+        uint4 yr[kYAhead][kQ];
+        auto fetch_y = [&](int i, int q0) {
+            if (i >= mine) return;
             const long long m0 = (static_cast<long long>(walker) + static_cast<long long>(i) * p.walkers) * 128;
-            const long long m1 = m0 + static_cast<long long>(p.walkers) * 128;  // the next tile
+#pragma unroll
+            for (int q = 0; q < kYAhead; ++q)
+                if (q0 + q < npiece) {
+                    const int e = (q0 + q) * kConv + tid;
+                    load_y8<T, VECY>(y, m0 + e / per_row, c0 + e % per_row * 8, p, yr[q]);
+                }
+        };
+        // chunk n of this CTA: chunk n % nch of its (n / nch)-th tile
+        auto fetch_g = [&](int n, GradPiece& to) {
+            const int i = nch == 2 ? n >> 1 : n, ch = nch == 2 ? n & 1 : 0;
+            if (i >= mine) return;
+            const long long m0 = (static_cast<long long>(walker) + static_cast<long long>(i) * p.walkers) * 128;
+            load_grad<VEC>(to, ch ? walk1 : walk0, grec, m0, g0 + ch * 64, p);
+        };
+        auto chunk = [&](int n, int ch, GradPiece& now) {
+            const int s = n & 1;
+            if (n >= 2) ok = mbar_wait_bounded(&empty_g[s], static_cast<unsigned>((n >> 1) - 1) & 1u, kCopyWaitLimitNs);
+            if (!ok) return;
+            store_grad(gsm + s * S::kG, ch ? walk1 : walk0, now);
+            hand_over(&full_g[s], lane);
+            if (sums) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    // rows past the tile hold zeros
+                    const float v[8] = {now.v[q][0].x, now.v[q][0].y, now.v[q][0].z, now.v[q][0].w,
+                                        now.v[q][1].x, now.v[q][1].y, now.v[q][1].z, now.v[q][1].w};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        if (ch == 0) bs[0][k] += v[k];
+                        else bs[1][k] += v[k];
+                    }
+                }
+            }
+            fetch_g(n + 2, now);  // two chunks ahead
+        };
+        GradPiece ga, gb2;
+        fetch_y(0, 0);
+        fetch_g(0, ga);
+        fetch_g(1, gb2);
+        for (int i = 0; i < mine && ok; ++i) {
             const int ys = i % S::kYStages, yn = i / S::kYStages;
             if (yn > 0) ok = mbar_wait_bounded(&empty_y[ys], static_cast<unsigned>(yn - 1) & 1u, kCopyWaitLimitNs);
             if (!ok) break;
-            for (int q0 = 0; q0 < npiece; q0 += 4) {
-                if (q0 > 0) fetch_y(m0, q0);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int e = (q0 + q) * 256 + tid, r = e / per_row, ch = e % per_row;
-                    float v[8];
-                    if constexpr (sizeof(T) == 4) {
+            for (int q4 = 0; q4 < 4; ++q4) {
+                if (q4 >= npiece) break;
+                const int q = q4 % kYAhead;
+                if (q4 > 0 && q == 0) fetch_y(i, q4);
+                const int e = q4 * kConv + tid, r = e / per_row, ch = e % per_row;
+                float v[8];
+                if constexpr (sizeof(T) == 4) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) v[k] = reinterpret_cast<const float*>(yr[q])[k];
-                    } else {
+                    for (int k = 0; k < 8; ++k) v[k] = reinterpret_cast<const float*>(yr[q])[k];
+                } else {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 f = unpack2(reinterpret_cast<const uint32_t*>(yr[q])[k], static_cast<T*>(nullptr));
-                            v[2 * k] = f.x;
-                            v[2 * k + 1] = f.y;
-                        }
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 f = unpack2(reinterpret_cast<const uint32_t*>(yr[q])[k], static_cast<T*>(nullptr));
+                        v[2 * k] = f.x;
+                        v[2 * k + 1] = f.y;
                     }
-                    store_split8<YP>(sm + ys * S::kY + (ch >> 3) * 16384, 32768u, r, ch & 7, v);
                 }
+                store_split8<YP>(sm + ys * S::kY + (ch >> 3) * 16384, 32768u, r, ch & 7, v);
             }
-            fence_proxy_async();
-            mbar_arrive(&full_y[ys]);
-            if (i + 1 < mine) fetch_y(m1, 0);
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-                if (ch >= nch) break;
-                const int gi = i * nch + ch, s = gi & 1;
-                if (gi >= 2) ok = mbar_wait_bounded(&empty_g[s], static_cast<unsigned>((gi >> 1) - 1) & 1u, kCopyWaitLimitNs);
-                if (!ok) break;
-                store_grad(gsm + s * S::kG, ra, tid);
-                fence_proxy_async();
-                mbar_arrive(&full_g[s]);
-                if (sums) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        bs[ch][0] += ra.v[q][0].x; bs[ch][1] += ra.v[q][0].y; bs[ch][2] += ra.v[q][0].z; bs[ch][3] += ra.v[q][0].w;
-                        bs[ch][4] += ra.v[q][1].x; bs[ch][5] += ra.v[q][1].y; bs[ch][6] += ra.v[q][1].z; bs[ch][7] += ra.v[q][1].w;
-                    }
-                }
-                if (ch + 1 < nch) load_grad<VEC>(ra, grec, m0, g0 + 64, tid, p);
-                else if (i + 1 < mine) load_grad<VEC>(ra, grec, m1, g0, tid, p);
+            hand_over(&full_y[ys], lane);
+            fetch_y(i + 1, 0);
+            if (nch == 2) {
+                chunk(2 * i, 0, ga);
+                if (ok) chunk(2 * i + 1, 1, gb2);
+            } else if (i & 1) {
+                chunk(i, 0, gb2);
+            } else {
+                chunk(i, 0, ga);
             }
         }
         if (sums) {
-            // the last products may still read the operand tiles: the sums go through shuffles and the first
-            // planes once those are done (every commit below orders them)
+            // once the last products have read the operand tiles (a commit covers all those before it), the
+            // threads' sums are added there, a slot's in the order of its rows' pieces
             const int last = mine * nch;
             if (ok && last > 0) {
                 const int s = (last - 1) & 1;
                 ok = mbar_wait_bounded(&empty_g[s], static_cast<unsigned>((last - 1) >> 1) & 1u, kCopyWaitLimitNs);
             }
-            float* red = reinterpret_cast<float*>(gsm);  // [8 warps][128 slots]
+            float* red = reinterpret_cast<float*>(gsm);  // [thread][8], one chunk at a time
 #pragma unroll
-            for (int ch = 0; ch < 2; ++ch)
+            for (int ch = 0; ch < 2; ++ch) {
+                if (ch >= nch) break;
+                const int ng = ch ? walk1.ng : walk0.ng, rows = ch ? walk1.rows : walk0.rows;
+                tc::bar_sync(2, kConv);
+                if (ok)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    float v = bs[ch][k];
-                    v += __shfl_xor_sync(0xffffffffu, v, 8);
-                    v += __shfl_xor_sync(0xffffffffu, v, 16);
-                    if (lane < 8 && ok) red[warp * 128 + ch * 64 + lane * 8 + k] = v;
-                }
-            tc::bar_sync(2, 256);
-            if (ok && tid < 128 && g0 + tid < p.NO) {
+                    for (int k = 0; k < 8; ++k) red[tid * 8 + k] = bs[ch][k];
+                tc::bar_sync(2, kConv);
+                // eight threads per slot, every eighth of the slot's threads each, then the eight
+                const int s = tid >> 3, part8 = tid & 7;
                 float v = 0.f;
-                for (int k = 0; k < 8; ++k) v += red[k * 128 + tid];
-                pbias[static_cast<size_t>(walker) * p.NO + g0 + tid] = v;
-            }
-        }
-    } else if (warp == 8) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = tc::idesc_f16(tc::kFmtBf16, 64, true, true);
-            const unsigned second = wide ? 16384u : 0u;
-            int flushed = 0;
-            for (int i = 0; i < mine && ok; ++i) {
-                const int ys = i % S::kYStages, t = i % kFlushTiles;
-                if (i > 0 && t == 0) ok = mbar_wait_bounded(acc_empty, static_cast<unsigned>(flushed++) & 1u, kCopyWaitLimitNs);
-                ok = ok && mbar_wait_bounded(&full_y[ys], static_cast<unsigned>(i / S::kYStages) & 1u, kCopyWaitLimitNs);
-                for (int ch = 0; ch < nch && ok; ++ch) {
-                    const int gi = i * nch + ch, s = gi & 1;
-                    ok = mbar_wait_bounded(&full_g[s], static_cast<unsigned>(gi >> 1) & 1u, kCopyWaitLimitNs);
-                    if (!ok) break;
-                    tc::fence_after();
-                    const unsigned a = smem_addr(sm + ys * S::kY), b = smem_addr(gsm + s * S::kG);
-                    for (int k = 0; k < 8; ++k) {
-                        const int n16 = t * 8 + k;
-#pragma unroll
-                        for (int gi3 = 0; gi3 < 3; ++gi3)
-#pragma unroll
-                            for (int j = 0; j < YP; ++j) {
-                                if (gi3 + j > 2) continue;
-                                const uint64_t ad = tc::sw128_desc(a + j * 32768u + k * 2048u, second);
-                                const uint64_t bd = tc::sw128_desc(b + gi3 * 16384u + k * 2048u);
-                                if (gi3 + j == 0) tc::mma_f16(tmem + (n16 % 3) * 128 + ch * 64, ad, bd, idesc, n16 >= 3);
-                                else tc::mma_f16(tmem + 384 + ch * 64, ad, bd, idesc,
-                                                 n16 > 0 || !(gi3 == (YP > 1 ? 0 : 1) && j == (YP > 1 ? 1 : 0)));
-                            }
-                    }
-                    tc::commit(&empty_g[s]);
-                }
-                if (!ok) break;
-                tc::commit(&empty_y[ys]);
-                if (t == kFlushTiles - 1 || i == mine - 1) tc::commit(acc_full);
+                if (s < ng * 8)
+                    for (int r = part8; r < rows; r += 8) v += red[(r * ng + (s >> 3)) * 8 + (s & 7)];
+                v += __shfl_xor_sync(0xffffffffu, v, 1);
+                v += __shfl_xor_sync(0xffffffffu, v, 2);
+                v += __shfl_xor_sync(0xffffffffu, v, 4);
+                if (ok && part8 == 0 && s < ng * 8 && g0 + ch * 64 + s < p.NO)
+                    pbias[static_cast<size_t>(walker) * p.NO + g0 + ch * 64 + s] = v;
             }
         }
     } else {
+        // warp 16's first lane issues the products of up to kFlushTiles tiles; then all four read the sums out
+        constexpr uint32_t idesc = tc::idesc_f16(tc::kFmtBf16, 64, true, true);
+        const unsigned second = wide ? 16384u : 0u;
         const int quarter = warp & 3, row = quarter * 32 + lane, c = c0 + row;
-        const int flushes = (mine + kFlushTiles - 1) / kFlushTiles;
         const bool on = c < p.C && (wide || row < 64);
-        for (int f = 0; f < flushes; ++f) {
-            ok = tc::bar_and(1, 128, mbar_wait_bounded(acc_full, static_cast<unsigned>(f) & 1u, kCopyWaitLimitNs));
+        for (int f = 0; f * kFlushTiles < mine; ++f) {
+            if (warp == 16 && lane == 0) {
+                tc::fence_after();
+                const int last = min(mine, (f + 1) * kFlushTiles);
+                for (int i = f * kFlushTiles; i < last && ok; ++i) {
+                    const int ys = i % S::kYStages, t = i - f * kFlushTiles;
+                    ok = mbar_wait_bounded(&full_y[ys], static_cast<unsigned>(i / S::kYStages) & 1u, kCopyWaitLimitNs);
+                    for (int ch = 0; ch < nch && ok; ++ch) {
+                        const int n = i * nch + ch, s = n & 1;
+                        ok = mbar_wait_bounded(&full_g[s], static_cast<unsigned>(n >> 1) & 1u, kCopyWaitLimitNs);
+                        if (!ok) break;
+                        tc::fence_after();
+                        const uint32_t a = tc::sw128(smem_addr(sm + ys * S::kY), second), b = tc::sw128(smem_addr(gsm + s * S::kG));
+                        const uint32_t acc = tmem + ch * 64;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+#pragma unroll
+                            for (int gi = 0; gi < 3; ++gi)
+#pragma unroll
+                                for (int j = 0; j < YP; ++j) {
+                                    if (gi + j > 2) continue;
+                                    const uint32_t ad = a + (j * 32768 + k * 2048) / 16, bd = b + (gi * 16384 + k * 2048) / 16;
+                                    const bool first_low = k == 0 && gi == (YP > 1 ? 0 : 1) && j == (YP > 1 ? 1 : 0);
+                                    if (gi + j == 0) tc::mma_f16(acc + (k % 3) * 128, ad, bd, idesc, t > 0 || k >= 3);
+                                    else tc::mma_f16(acc + 384, ad, bd, idesc, t > 0 || !first_low);
+                                }
+                        tc::commit(&empty_g[s]);
+                    }
+                    if (ok) tc::commit(&empty_y[ys]);
+                }
+                if (ok) tc::commit(acc_full);
+            }
+            __syncwarp();
+            ok = tc::bar_and(1, 128, ok && mbar_wait_bounded(acc_full, static_cast<unsigned>(f) & 1u, kFlushWaitLimitNs));
             if (!ok) break;
             tc::fence_after();
             const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -564,23 +616,23 @@ pred_grad_w_kernel(const float* __restrict__ grec, const T* __restrict__ y, floa
                     }
             }
             tc::fence_before();
-            mbar_arrive(acc_empty);
+            tc::bar_sync(1, 128);
         }
     }
     if (!ok) atomicOr(p.status, kStatusCopyTimeout);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    if (warp == 8) tc::dealloc(tmem, 512u);
+    if (warp == 16) tc::dealloc(tmem, 512u);
 }
 
-// The walkers' partial sums added in a fixed order (eight strided runs of
-// walkers, then the eight), rows moved from record order to the projection's
+// The walkers' partial sums added in a fixed order (sixteen strided runs of
+// walkers, then the sixteen), rows moved from record order to the projection's
 // channel order: 32 entries per CTA.
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(512)
 pred_grad_w_join_kernel(const float* __restrict__ part, const float* __restrict__ pbias, float* __restrict__ gw,
                         float* __restrict__ gb, PredBwdParams p) {
-    __shared__ float red[8][32];
+    __shared__ float red[16][32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const long long n = static_cast<long long>(p.NO) * p.C, total = n + (gb ? p.NO : 0);
@@ -592,12 +644,12 @@ pred_grad_w_join_kernel(const float* __restrict__ part, const float* __restrict_
             const float* src = i < n ? part + i : pbias + (i - n);
             const long long step = i < n ? n : p.NO;
 #pragma unroll 8
-            for (int k = run; k < p.walkers; k += 8) a += __ldg(src + k * step);
+            for (int k = run; k < p.walkers; k += 16) a += __ldg(src + k * step);
         }
         red[run][lane] = a;
         __syncthreads();
         if (run == 0 && i < total) {
-            for (int k = 1; k < 8; ++k) a += red[k][lane];
+            for (int k = 1; k < 16; ++k) a += red[k][lane];
             if (i < n) {
                 const int s = static_cast<int>(i / p.C), c = static_cast<int>(i - static_cast<long long>(s) * p.C);
                 gw[static_cast<size_t>(channel_of_slot(s, p.G, p.P)) * p.C + c] = a;
