@@ -65,56 +65,64 @@ bool tile_map(CUtensorMap* map, CUtensorMapDataType type, int e, void* base, lon
 }
 
 template <int CT, int WP>
-int launch_grad_y(const CUtensorMap& wmap, const CUtensorMap& omap, const float* grec, float* gy,
-                  dcnv4::PredBwdParams p, int nsm, bool vec, cudaStream_t s) {
+int launch_grad_y(const CUtensorMap& wmap, const CUtensorMap& gmap, const CUtensorMap& omap, const float* grec, float* gy,
+                  dcnv4::PredBwdParams p, int nsm, bool raw, cudaStream_t s) {
     constexpr unsigned smem = dcnv4::GradYShape<CT, WP>::kSmem;
     static_assert(smem <= kTileSmemLimit, "the stages do not fit");
-    auto kern = vec ? dcnv4::pred_grad_y_kernel<CT, WP, true> : dcnv4::pred_grad_y_kernel<CT, WP, false>;
+    auto kern = raw ? dcnv4::pred_grad_y_kernel<CT, WP, true> : dcnv4::pred_grad_y_kernel<CT, WP, false>;
     if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess)
         return DCNV4_ERR_LAUNCH;
     p.slices = (p.C + CT - 1) / CT;
     const long long items = static_cast<long long>(p.tiles) * p.slices;
-    return launch_chained(kern, dim3(static_cast<unsigned>(std::min<long long>(items, nsm))), dcnv4::kGradYThreads, smem, s, wmap, omap,
-                          grec, gy, p);
+    return launch_chained(kern, dim3(static_cast<unsigned>(std::min<long long>(items, nsm))), dcnv4::kGradYThreads, smem, s,
+                          wmap, gmap, omap, grec, gy, p);
+}
+
+template <typename T, bool RAW>
+int launch_grad_w(const CUtensorMap& gmap, const CUtensorMap& ymap, const float* grec, const T* y, float* part,
+                  float* pbias, dcnv4::PredBwdParams p, cudaStream_t s) {
+    constexpr unsigned smem = dcnv4::GradWShape<T, RAW>::kSmem;
+    static_assert(smem <= kTileSmemLimit, "the stages do not fit");
+    auto kern = dcnv4::pred_grad_w_kernel<T, RAW>;
+    if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess) return DCNV4_ERR_LAUNCH;
+    p.slices = (p.C + 127) / 128;
+    return launch_chained(kern, dim3(static_cast<unsigned>(p.walkers) * p.slices * p.groups), dcnv4::kGradWThreads, smem, s,
+                          gmap, ymap, grec, y, part, pbias, p);
 }
 
 template <typename T>
 int launch(const void* y, const void* w, const float* grec, float* gy, float* gw, float* gb, unsigned char* ws,
            dcnv4::PredBwdParams p, int dtype, cudaStream_t s) {
-    constexpr int WP = dcnv4::split_planes<T>();
+    constexpr int WP = dcnv4::split_planes<T>(), E = sizeof(T);
     const int nsm = sm_count();
     if (nsm <= 0) return DCNV4_ERR_CUDA;
     const Layout l = layout(p, dtype);
     __nv_bfloat16* planes = reinterpret_cast<__nv_bfloat16*>(ws);
     float *part = reinterpret_cast<float*>(ws + l.part), *pbias = gb ? reinterpret_cast<float*>(ws + l.pbias) : nullptr;
-    CUtensorMap wmap, omap;
-    if (!tile_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, planes, p.wpitch, p.wrows, WP, 64, 64)) return DCNV4_ERR_CUDA;
-    omap = wmap;
+    // TMA wants rows of whole 16-byte units on 16-byte boundaries
+    const bool raw_g = p.NO % 4 == 0 && aligned(grec, 16), raw_w = raw_g && p.C * E % 16 == 0 && aligned(y, 16);
     p.tma_out = p.C % 4 == 0 && aligned(gy, 16) ? 1 : 0;
-    if (p.tma_out && !tile_map(&omap, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, gy, p.C, p.M, 1, 32, 128)) return DCNV4_ERR_CUDA;
+    CUtensorMap wmap{}, gmap{}, ymap{}, omap{};
+    if (!tile_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, planes, p.wpitch, p.wrows, WP, 64, 64) ||
+        (raw_g && !tile_map(&gmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<float*>(grec), p.NO, p.M, 1, 32, 128)) ||
+        (raw_w && !tile_map(&ymap, tma_dtype<T>(), E, const_cast<void*>(y), p.C, p.M, 1, 128 / E, 128)) ||
+        (p.tma_out && !tile_map(&omap, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, gy, p.C, p.M, 1, 32, 128)))
+        return DCNV4_ERR_CUDA;
     const long long pairs = static_cast<long long>(p.wrows) * p.wpitch / 2;
     int rc = launch_chained(dcnv4::pred_split_weight_kernel<T>, dim3(static_cast<unsigned>(std::min<long long>((pairs + 255) / 256, 148 * 8))),
                             256, 0, s, static_cast<const T*>(w), planes, p);
     if (rc) return rc;
-    const bool vec = p.NO % 4 == 0 && aligned(grec, 16);
     // 128 channels per tile halve the readings of g; with many slots (long chains of truncated additions) or three
     // weight planes (shared memory) 64 channels leave room for three accumulators of order 0
     if constexpr (WP <= 2) {
-        if (p.C > 64 && p.NO <= 256) rc = launch_grad_y<128, WP>(wmap, omap, grec, gy, p, nsm, vec, s);
-        else rc = launch_grad_y<64, WP>(wmap, omap, grec, gy, p, nsm, vec, s);
+        if (p.C > 64 && p.NO <= 256) rc = launch_grad_y<128, WP>(wmap, gmap, omap, grec, gy, p, nsm, raw_g, s);
+        else rc = launch_grad_y<64, WP>(wmap, gmap, omap, grec, gy, p, nsm, raw_g, s);
     } else {
-        rc = launch_grad_y<64, WP>(wmap, omap, grec, gy, p, nsm, vec, s);
+        rc = launch_grad_y<64, WP>(wmap, gmap, omap, grec, gy, p, nsm, raw_g, s);
     }
     if (rc) return rc;
-    const bool vecy = p.C % 8 == 0 && aligned(y, 16);
-    auto kern = vec ? (vecy ? dcnv4::pred_grad_w_kernel<T, true, true> : dcnv4::pred_grad_w_kernel<T, true, false>)
-                    : (vecy ? dcnv4::pred_grad_w_kernel<T, false, true> : dcnv4::pred_grad_w_kernel<T, false, false>);
-    constexpr unsigned smem = dcnv4::GradWShape<T>::kSmem;
-    static_assert(smem <= kTileSmemLimit, "the stages do not fit");
-    if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess) return DCNV4_ERR_LAUNCH;
-    p.slices = (p.C + 127) / 128;
-    rc = launch_chained(kern, dim3(static_cast<unsigned>(p.walkers) * p.slices * p.groups), dcnv4::kGradWThreads, smem, s, grec,
-                        static_cast<const T*>(y), part, pbias, p);
+    rc = raw_w ? launch_grad_w<T, true>(gmap, ymap, grec, static_cast<const T*>(y), part, pbias, p, s)
+               : launch_grad_w<T, false>(gmap, ymap, grec, static_cast<const T*>(y), part, pbias, p, s);
     if (rc) return rc;
     const long long n = (static_cast<long long>(p.NO) * p.C + (gb ? p.NO : 0) + 31) / 32;
     return launch_chained(dcnv4::pred_grad_w_join_kernel, dim3(static_cast<unsigned>(std::min<long long>(n, 148 * 4))), 512, 0, s,

@@ -105,58 +105,79 @@ pred_split_weight_kernel(const T* __restrict__ w, __nv_bfloat16* __restrict__ pl
     }
 }
 
-// The records' gradients of 128 pixels x one chunk of up to 64 slots, spread
-// over kConv threads in pieces of eight slots: only the groups of eight below
-// the chunk's last 16-slot step are touched (a chunk's other columns are never
-// read, or only into sums that nobody reads). A thread has two pieces at most,
-// of one group and rows `rows` apart.
+// Columns of a row-major matrix (record slots of g, channels of y) are turned
+// into operand planes 64 at a time, 128 pixels each, by kConv threads in pieces
+// of eight columns: only the groups of eight below the last 16 valid columns
+// are touched (a chunk's other columns are never read, or only into sums that
+// nobody reads). A thread has two pieces at most, of one group and rows `rows`
+// apart. By TMA the values come through a ring of raw tiles (blocks of 128
+// bytes of columns x 128 rows, 128-byte swizzle, zeros past the matrix): reads
+// through L1 would have no room there, since the operand tiles take most of
+// an SM's memory, and so few of them in flight that DRAM idles (measured: 31 %
+// of its rate). Matrices whose rows TMA cannot take are read directly.
 constexpr int kConv = 512;
-struct GradPiece {
-    float4 v[2][2];
-};
+constexpr unsigned kRaw = 32768u;  // 128 rows x 64 fp32
 struct ChunkWalk {
-    int ng, row, grp, rows;  // groups of eight slots; this thread's first row, its group, rows per round
-    __device__ __forceinline__ ChunkWalk(int slots, int tid) {
-        ng = min(8, (slots + 15) / 16 * 2);
+    int ng, row, grp, rows;  // groups of eight columns; this thread's first row, its group, rows per round
+    __device__ __forceinline__ ChunkWalk(int columns, int tid) {
+        ng = min(8, (columns + 15) / 16 * 2);
         rows = kConv / ng;
         row = tid / ng;
         grp = tid - row * ng;
         if (row >= rows) row = 128;  // the threads left over
     }
 };
-template <bool VEC>
-__device__ __forceinline__ void load_grad(GradPiece& r, const ChunkWalk& walk, const float* __restrict__ g, long long m0,
-                                          int s0, const PredBwdParams& p) {
-    const int s = s0 + walk.grp * 8;
+template <typename T>
+struct Piece {
+    float v[2][8];
+    // from a raw tile: column c of row r is in block c / (128 / sizeof(T)), 16-byte chunk k at k ^ (r mod 8)
+    __device__ __forceinline__ void from_raw(const unsigned char* raw, const ChunkWalk& walk) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int row = walk.row + q * walk.rows;
-        const bool on = row < 128 && m0 + row < p.M;
-        const float* src = g + (m0 + row) * p.NO + s;
+        for (int q = 0; q < 2; ++q) {
+            const int row = walk.row + q * walk.rows;
+            if (row >= 128) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if constexpr (VEC) {
-                r.v[q][h] = on && s + 4 * h < p.NO ? __ldg(reinterpret_cast<const float4*>(src + 4 * h))
-                                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = 0; k < 8; ++k) v[q][k] = 0.f;
+                continue;
+            }
+            if constexpr (sizeof(T) == 4) {
+                const unsigned char* at = raw + (walk.grp >> 2) * 16384 + row * 128;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    *reinterpret_cast<float4*>(&v[q][4 * h]) =
+                        *reinterpret_cast<const float4*>(at + ((((walk.grp & 3) * 2 + h) ^ (row & 7)) << 4));
             } else {
-                float e[4];
+                const uint4 w = *reinterpret_cast<const uint4*>(raw + row * 128 + ((walk.grp ^ (row & 7)) << 4));
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) e[k] = on && s + 4 * h + k < p.NO ? __ldg(src + 4 * h + k) : 0.f;
-                r.v[q][h] = make_float4(e[0], e[1], e[2], e[3]);
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = unpack2(u[k], static_cast<T*>(nullptr));
+                    v[q][2 * k] = f.x;
+                    v[q][2 * k + 1] = f.y;
+                }
             }
         }
     }
-}
-__device__ __forceinline__ void store_grad(unsigned char* stage, const ChunkWalk& walk, const GradPiece& r) {
+    // from memory: rows m0.. of M, columns c0.. of C
+    __device__ __forceinline__ void from_global(const T* __restrict__ x, const ChunkWalk& walk, long long m0, int M, int c0, int C) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int row = walk.row + q * walk.rows;
-        if (row >= 128) continue;
-        const float v[8] = {r.v[q][0].x, r.v[q][0].y, r.v[q][0].z, r.v[q][0].w,
-                            r.v[q][1].x, r.v[q][1].y, r.v[q][1].z, r.v[q][1].w};
-        store_split8<3>(stage, 16384u, row, walk.grp, v);
+        for (int q = 0; q < 2; ++q) {
+            const int row = walk.row + q * walk.rows;
+            const T* src = x + (m0 + row) * C + c0 + walk.grp * 8;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[q][k] = row < 128 && m0 + row < M && c0 + walk.grp * 8 + k < C ? ElemTraits<T>::to_float(__ldg(src + k)) : 0.f;
+        }
     }
-}
+    template <int PLANES>
+    __device__ __forceinline__ void store(unsigned char* tile, unsigned step, const ChunkWalk& walk) const {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int row = walk.row + q * walk.rows;
+            if (row < 128) store_split8<PLANES>(tile, step, row, walk.grp, v[q]);
+        }
+    }
+};
 // the operand tiles this warp's threads wrote, handed over (one arrival per warp)
 __device__ __forceinline__ void hand_over(uint64_t* bar, int lane) {
     fence_proxy_async();
@@ -164,36 +185,39 @@ __device__ __forceinline__ void hand_over(uint64_t* bar, int lane) {
     if (lane == 0) mbar_arrive(bar);
 }
 
-// grad_y: tiles of 128 pixels x CT channels. Warps 0..15 read g 64 slots at a
-// time (three chunks ahead, in registers) and write its planes as the left
-// operand (K-major); warp 16 loads the same slots' rows of W's planes by TMA
-// as the right one (its rows run along the channels: MN-major); warp 17 issues
-// the products; warps 18..21 read the accumulators (two sets, in turn) and
-// write the tile through shared memory and TMA.
+// grad_y: tiles of 128 pixels x CT channels. Warps 0..15 write the planes of g
+// as the left operand (K-major), 64 slots at a time; warp 16 loads g's raw
+// tiles and the same slots' rows of W's planes by TMA, these as the right
+// operand (their rows run along the channels: MN-major); warp 17 issues the
+// products; warps 18..21 read the accumulators (two sets, in turn) and write
+// the tile through shared memory and TMA, 64 channels at a time.
 template <int CT, int WP>
 struct GradYShape {
     static constexpr int kStages = 2;
     static constexpr int kHigh = CT == 64 ? 3 : 1;  // accumulators of order 0
     static constexpr unsigned kWBytes = WP * (CT / 64) * 8192u;
     static constexpr unsigned kStage = 3u * 16384u + kWBytes;
-    static constexpr unsigned kOut = (CT / 32) * 16384u;
-    static constexpr unsigned kSmem = 1024u + kStages * kStage + kOut + 256u;
+    static constexpr unsigned kOut = 32768u;
+    static constexpr int kRaws = kStages * kStage + kOut + 2 * kRaw <= 224u * 1024u ? 2 : 1;  // raw tiles
+    static constexpr unsigned kSmem = 1024u + kStages * kStage + kOut + kRaws * kRaw + 256u;
     static constexpr unsigned kAcc = (kHigh + 1) * CT;  // columns of one set
 };
-
 constexpr int kGradYThreads = kConv + 64 + 128;
 
-template <int CT, int WP, bool VEC>
+template <int CT, int WP, bool RAW>
 __global__ void __launch_bounds__(kGradYThreads, 1)
-pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap omap,
-                   const float* __restrict__ grec, float* __restrict__ gy, PredBwdParams p) {
+pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap gmap,
+                   const __grid_constant__ CUtensorMap omap, const float* __restrict__ grec, float* __restrict__ gy,
+                   PredBwdParams p) {
     using S = GradYShape<CT, WP>;
     extern __shared__ unsigned char pb_smem_raw[];
     unsigned char* sm = pb_smem_raw + ((1024u - (smem_addr(pb_smem_raw) & 1023u)) & 1023u);
     unsigned char* outs = sm + S::kStages * S::kStage;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(outs + S::kOut);
-    uint64_t *full_g = bars, *full_w = bars + 2, *empty = bars + 4, *acc_full = bars + 6, *acc_empty = bars + 8;
-    uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 10);
+    unsigned char* raws = outs + S::kOut;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(raws + S::kRaws * kRaw);
+    uint64_t *full_g = bars, *full_w = bars + 2, *empty = bars + 4, *acc_full = bars + 6, *acc_empty = bars + 8,
+             *raw_full = bars + 10, *raw_empty = bars + 12;
+    uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 14);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
@@ -203,6 +227,8 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             mbar_init(&empty[s], 1);
             mbar_init(&acc_full[s], 1);
             mbar_init(&acc_empty[s], 128);
+            mbar_init(&raw_full[s], 1);
+            mbar_init(&raw_empty[s], kConv / 32);
         }
         fence_barrier_init();
     }
@@ -221,50 +247,67 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     bool ok = true;
 
     if (warp < 16) {
-        auto where = [&](long long it, long long& m0, int& s0) {
-            const long long item = blockIdx.x + (it / p.chunks) * gridDim.x;
-            m0 = item / p.slices * 128;
-            s0 = static_cast<int>(it % p.chunks) * 64;
-        };
-        GradPiece r[3];
         const ChunkWalk whole(64, tid), tail(p.NO - (p.chunks - 1) * 64, tid);
-        auto fetch = [&](long long it, GradPiece& to) {
-            long long m0;
-            int s0;
-            if (it < steps) {
-                where(it, m0, s0);
-                load_grad<VEC>(to, s0 + 64 < p.NO ? whole : tail, grec, m0, s0, p);
+        Piece<float> piece;
+        int chunk = 0;
+        long long n = 0;  // the item
+        for (long long it = 0; it < steps && ok; ++it) {
+            const int s = static_cast<int>(it & 1), r = static_cast<int>(it % S::kRaws);
+            const ChunkWalk& walk = chunk + 1 < p.chunks ? whole : tail;
+            if constexpr (RAW) {
+                ok = mbar_wait_bounded(&raw_full[r], static_cast<unsigned>(it / S::kRaws) & 1u, kCopyWaitLimitNs);
+                if (!ok) break;
+                piece.from_raw(raws + r * kRaw, walk);
+            } else {
+                const long long item = blockIdx.x + n * gridDim.x;
+                piece.from_global(grec, walk, item / p.slices * 128, p.M, chunk * 64, p.NO);
             }
-        };
-        fetch(0, r[0]);
-        fetch(1, r[1]);
-        auto step = [&](long long it, GradPiece& now, GradPiece& next) {
-            fetch(it + 2, next);
-            const int s = static_cast<int>(it & 1);
             if (it >= 2) ok = mbar_wait_bounded(&empty[s], static_cast<unsigned>((it >> 1) - 1) & 1u, kCopyWaitLimitNs);
-            if (!ok) return;
-            store_grad(sm + s * S::kStage, static_cast<int>(it % p.chunks) + 1 < p.chunks ? whole : tail, now);
+            if (!ok) break;
+            piece.template store<3>(sm + s * S::kStage, 16384u, walk);
             hand_over(&full_g[s], lane);
-        };
-        for (long long it = 0; it < steps && ok; it += 3) {
-            step(it, r[0], r[2]);
-            if (it + 1 < steps && ok) step(it + 1, r[1], r[0]);
-            if (it + 2 < steps && ok) step(it + 2, r[2], r[1]);
+            if (RAW && lane == 0) mbar_arrive(&raw_empty[r]);
+            if (++chunk == p.chunks) {
+                chunk = 0;
+                ++n;
+            }
         }
     } else if (warp == 16) {
         if (lane == 0) {
+            // raw tiles run ahead of the operand stages by as many as the ring holds
+            auto where = [&](long long it, int& m0, int& c0, int& s0) {
+                const long long item = blockIdx.x + (it / p.chunks) * gridDim.x;
+                m0 = static_cast<int>(item / p.slices) * 128;
+                c0 = static_cast<int>(item % p.slices) * CT;
+                s0 = static_cast<int>(it % p.chunks) * 64;
+            };
+            auto load_raw = [&](long long it) {
+                if (!RAW || it >= steps) return;
+                const int r = static_cast<int>(it % S::kRaws);
+                if (it >= S::kRaws)
+                    ok = mbar_wait_bounded(&raw_empty[r], static_cast<unsigned>(it / S::kRaws - 1) & 1u, kCopyWaitLimitNs);
+                if (!ok) return;
+                int m0, c0, s0;
+                where(it, m0, c0, s0);
+                const int halves = s0 + 32 < p.NO ? 2 : 1;
+                mbar_expect_tx(&raw_full[r], halves * 16384u);
+                for (int h = 0; h < halves; ++h) tc::tma_load_3d(raws + r * kRaw + h * 16384, &gmap, s0 + h * 32, m0, 0, &raw_full[r]);
+                mbar_arrive(&raw_full[r]);
+            };
+            for (int k = 0; k < S::kRaws; ++k) load_raw(k);
             for (long long it = 0; it < steps && ok; ++it) {
                 const int s = static_cast<int>(it & 1);
                 if (it >= 2) ok = mbar_wait_bounded(&empty[s], static_cast<unsigned>((it >> 1) - 1) & 1u, kCopyWaitLimitNs);
                 if (!ok) break;
-                const long long item = blockIdx.x + (it / p.chunks) * gridDim.x;
-                const int c0 = static_cast<int>(item % p.slices) * CT, s0 = static_cast<int>(it % p.chunks) * 64;
+                int m0, c0, s0;
+                where(it, m0, c0, s0);
                 unsigned char* w = sm + s * S::kStage + 3 * 16384;
                 mbar_expect_tx(&full_w[s], S::kWBytes);
                 for (int pl = 0; pl < WP; ++pl)
                     for (int b = 0; b < CT / 64; ++b)
                         tc::tma_load_3d(w + (pl * (CT / 64) + b) * 8192, &wmap, c0 + b * 64, s0, pl, &full_w[s]);
                 mbar_arrive(&full_w[s]);
+                load_raw(it + S::kRaws);
             }
         }
     } else if (warp == 17) {
@@ -309,45 +352,50 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             const long long item = blockIdx.x + n * gridDim.x;
             const long long m0 = item / p.slices * 128;
             const int c0 = static_cast<int>(item % p.slices) * CT, b = static_cast<int>(n & 1);
-            if (et == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             ok = tc::bar_and(1, 128, mbar_wait_bounded(&acc_full[b], static_cast<unsigned>(n >> 1) & 1u, kCopyWaitLimitNs));
             if (!ok) break;
             tc::fence_after();
             const uint32_t acc = tmem + b * S::kAcc + (static_cast<uint32_t>(quarter * 32) << 16);
-            for (int cc = 0; cc < CT / 16; ++cc) {
-                float v[16], w[16];
-                tc::ld16(acc + S::kHigh * CT + cc * 16, v);
-                for (int q = 0; q < high; ++q) {
-                    tc::ld16(acc + q * CT + cc * 16, w);
-                    tc::wait_ld();
+            for (int h = 0; h < CT / 64; ++h) {
+                if (h > 0 && c0 + h * 64 >= p.C) continue;
+                // the stores that read the staging tile have done so
+                if (et == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                tc::bar_sync(1, 128);
+                for (int cc = 0; cc < 4; ++cc) {
+                    float v[16], w[16];
+                    tc::ld16(acc + S::kHigh * CT + h * 64 + cc * 16, v);
+                    for (int q = 0; q < high; ++q) {
+                        tc::ld16(acc + q * CT + h * 64 + cc * 16, w);
+                        tc::wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] += w[e];
+                        for (int e = 0; e < 16; ++e) v[e] += w[e];
+                    }
+                    // 32 channels (128 bytes) per block of the staging tile
+                    unsigned char* o = outs + (cc >> 1) * 16384 + row * 128;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<float4*>(o + ((((cc & 1) * 4 + q) ^ (row & 7)) << 4)) =
+                            make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
                 }
-                // 32 channels (128 bytes) per block of the staging tile
-                unsigned char* o = outs + (cc >> 1) * 16384 + row * 128;
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    *reinterpret_cast<float4*>(o + ((((cc & 1) * 4 + q) ^ (row & 7)) << 4)) =
-                        make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                if (p.tma_out) fence_proxy_async();
+                tc::bar_sync(1, 128);
+                if (p.tma_out) {
+                    if (et == 0) {
+                        for (int q = 0; q < 2; ++q)
+                            if (c0 + h * 64 + q * 32 < p.C)
+                                tc::tma_store_3d(&omap, c0 + h * 64 + q * 32, static_cast<int>(m0), 0, outs + q * 16384);
+                        tc::bulk_commit();
+                    }
+                } else {
+                    const int rows = static_cast<int>(min(128LL, p.M - m0)), cols = min(64, p.C - c0 - h * 64);
+                    for (int r = quarter; r < rows; r += 4)
+                        for (int c = lane; c < cols; c += 32)
+                            gy[(m0 + r) * p.C + c0 + h * 64 + c] = *reinterpret_cast<const float*>(
+                                outs + (c >> 5) * 16384 + r * 128 + ((((c & 31) >> 2) ^ (r & 7)) << 4) + (c & 3) * 4);
+                }
             }
             tc::fence_before();
             mbar_arrive(&acc_empty[b]);
-            if (p.tma_out) fence_proxy_async();
-            tc::bar_sync(1, 128);
-            if (p.tma_out) {
-                if (et == 0) {
-                    for (int q = 0; q < CT / 32; ++q)
-                        if (c0 + q * 32 < p.C) tc::tma_store_3d(&omap, c0 + q * 32, static_cast<int>(m0), 0, outs + q * 16384);
-                    tc::bulk_commit();
-                }
-            } else {
-                const int rows = static_cast<int>(min(128LL, p.M - m0)), cols = min(CT, p.C - c0);
-                for (int r = quarter; r < rows; r += 4)
-                    for (int c = lane; c < cols; c += 32)
-                        gy[(m0 + r) * p.C + c0 + c] = *reinterpret_cast<const float*>(
-                            outs + (c >> 5) * 16384 + r * 128 + ((((c & 31) >> 2) ^ (r & 7)) << 4) + (c & 3) * 4);
-                tc::bar_sync(1, 128);
-            }
         }
         if (et == 0) tc::bulk_wait_all();
     }
@@ -362,60 +410,58 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
 // the pixels of every walkers-th tile. Warps 0..15 write the planes of y (the
 // left operand) and, 64 slots at a time, of g (the right one), both with rows
 // that run along channels or slots: MN-major; the same threads sum g for the
-// bias. Warps 16..19 issue the products and read the accumulators out to
-// part [walkers][NO][C], lanes along the channels. A slice of at most 64
-// channels reads its one block of 64 for both halves of the M = 128 products.
-template <typename T>
+// bias. y in bf16 is its own plane and comes straight by TMA. Of warps 16..19,
+// one lane issues the products and another the TMA loads; every kFlushTiles
+// tiles all four read the accumulators out to part [walkers][NO][C], lanes
+// along the channels. A slice of at most 64 channels reads its one block of 64
+// for both halves of the M = 128 products.
+template <typename T, bool RAW>
 struct GradWShape {
     static constexpr int YP = split_planes<T>();
-    static constexpr int kYStages = YP <= 2 ? 2 : 1;
+    static constexpr bool kDirectY = RAW && YP == 1;  // y's plane by TMA
+    static constexpr int kYStages = YP == 1 ? 2 : 1;
     static constexpr unsigned kY = YP * 32768u;
     static constexpr unsigned kG = 3u * 16384u;
-    static constexpr unsigned kSmem = 1024u + kYStages * kY + 2u * kG + 256u;
+    static constexpr int kRaws = !RAW ? 0 : YP == 3 ? 1 : 2;
+    static constexpr unsigned kSmem = 1024u + kYStages * kY + 2u * kG + kRaws * kRaw + 256u;
 };
-
-// Eight channels of y at (m, c), zeros outside.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_y8(const T* __restrict__ y, long long m, int c, const PredBwdParams& p, uint4 (&w)[sizeof(T) / 2]) {
-    const T* src = y + m * p.C + c;
-    if constexpr (VEC) {
-        const bool on = m < p.M && c < p.C;
-#pragma unroll
-        for (int q = 0; q < static_cast<int>(sizeof(T) / 2); ++q)
-            w[q] = on ? __ldg(reinterpret_cast<const uint4*>(src) + q) : make_uint4(0, 0, 0, 0);
-    } else {
-        T* d = reinterpret_cast<T*>(w);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            if (m < p.M && c + q < p.C) d[q] = __ldg(src + q);
-            else if constexpr (sizeof(T) == 4) d[q] = 0.f;
-            else reinterpret_cast<uint16_t*>(w)[q] = 0;
-        }
-    }
-}
-
 constexpr int kGradWThreads = kConv + 128;
 
-template <typename T, bool VEC, bool VECY>
+template <typename T, bool RAW>
 __global__ void __launch_bounds__(kGradWThreads, 1)
-pred_grad_w_kernel(const float* __restrict__ grec, const T* __restrict__ y, float* __restrict__ part,
+pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CUtensorMap ymap,
+                   const float* __restrict__ grec, const T* __restrict__ y, float* __restrict__ part,
                    float* __restrict__ pbias, PredBwdParams p) {
-    using S = GradWShape<T>;
-    constexpr int YP = S::YP, kQ = sizeof(T) / 2;
+    using S = GradWShape<T, RAW>;
+    constexpr int YP = S::YP;
     extern __shared__ unsigned char pb_smem_raw[];
     unsigned char* sm = pb_smem_raw + ((1024u - (smem_addr(pb_smem_raw) & 1023u)) & 1023u);
     unsigned char* gsm = sm + S::kYStages * S::kY;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(gsm + 2 * S::kG);
-    uint64_t *full_y = bars, *empty_y = bars + 2, *full_g = bars + 4, *empty_g = bars + 6, *acc_full = bars + 8;
-    uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 10);
+    unsigned char* raws = gsm + 2 * S::kG;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(raws + S::kRaws * kRaw);
+    uint64_t *full_y = bars, *empty_y = bars + 2, *full_g = bars + 4, *empty_g = bars + 6, *acc_full = bars + 8,
+             *raw_full = bars + 9, *raw_empty = bars + 11;
+    uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 13);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // CTA -> walker, (slice, group); the slices and groups of one walker side by side
+    const int per = p.slices * p.groups;
+    const int walker = static_cast<int>(blockIdx.x) / per, which = static_cast<int>(blockIdx.x) % per;
+    const int c0 = which % p.slices * 128, g0 = which / p.slices * 128;
+    const int nch = (min(128, p.NO - g0) + 63) / 64;    // chunks of this group
+    const bool wide = p.C - c0 > 64;
+    const int ny = wide ? 2 : 1;                        // blocks of 64 channels of this slice
+    const int mine = walker < p.tiles ? (p.tiles - walker + p.walkers - 1) / p.walkers : 0;
+    auto pixel = [&](int i) { return (static_cast<long long>(walker) + static_cast<long long>(i) * p.walkers) * 128; };
 
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&full_y[s], kConv / 32);
+            mbar_init(&full_y[s], S::kDirectY ? 1 : kConv / 32 * ny);
             mbar_init(&empty_y[s], 1);
             mbar_init(&full_g[s], kConv / 32);
             mbar_init(&empty_g[s], 1);
+            mbar_init(&raw_full[s], 1);
+            mbar_init(&raw_empty[s], kConv / 32);
         }
         mbar_init(acc_full, 1);
         fence_barrier_init();
@@ -427,100 +473,60 @@ pred_grad_w_kernel(const float* __restrict__ grec, const T* __restrict__ y, floa
     const uint32_t tmem = *slot;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-    // CTA -> walker, (slice, group); the slices and groups of one walker side by side
-    const int per = p.slices * p.groups;
-    const int walker = static_cast<int>(blockIdx.x) / per, which = static_cast<int>(blockIdx.x) % per;
-    const int c0 = which % p.slices * 128, g0 = which / p.slices * 128;
-    const int nch = (min(128, p.NO - g0) + 63) / 64;    // chunks of this group
-    const bool wide = p.C - c0 > 64;
-    const int mine = walker < p.tiles ? (p.tiles - walker + p.walkers - 1) / p.walkers : 0;
     bool ok = true;
 
     if (warp < 16) {
         const bool sums = c0 == 0 && pbias != nullptr;
         float bs[2][8] = {};              // [chunk][slot of this thread's group]
-        const int npiece = wide ? 4 : 2;  // eight-channel pieces of y per thread
-        const int per_row = wide ? 16 : 8;
         const ChunkWalk walk0(p.NO - g0, tid), walk1(nch == 2 ? p.NO - g0 - 64 : 64, tid);
-        // pieces of y loaded ahead (the others, of fp32, when it is their turn)
-        constexpr int kYAhead = sizeof(T) == 4 ? 2 : 4;
-        uint4 yr[kYAhead][kQ];
-        auto fetch_y = [&](int i, int q0) {
-            if (i >= mine) return;
-            const long long m0 = (static_cast<long long>(walker) + static_cast<long long>(i) * p.walkers) * 128;
-#pragma unroll
-            for (int q = 0; q < kYAhead; ++q)
-                if (q0 + q < npiece) {
-                    const int e = (q0 + q) * kConv + tid;
-                    load_y8<T, VECY>(y, m0 + e / per_row, c0 + e % per_row * 8, p, yr[q]);
-                }
-        };
-        // chunk n of this CTA: chunk n % nch of its (n / nch)-th tile
-        auto fetch_g = [&](int n, GradPiece& to) {
-            const int i = nch == 2 ? n >> 1 : n, ch = nch == 2 ? n & 1 : 0;
-            if (i >= mine) return;
-            const long long m0 = (static_cast<long long>(walker) + static_cast<long long>(i) * p.walkers) * 128;
-            load_grad<VEC>(to, ch ? walk1 : walk0, grec, m0, g0 + ch * 64, p);
-        };
-        auto chunk = [&](int n, int ch, GradPiece& now) {
-            const int s = n & 1;
-            if (n >= 2) ok = mbar_wait_bounded(&empty_g[s], static_cast<unsigned>((n >> 1) - 1) & 1u, kCopyWaitLimitNs);
+        const ChunkWalk ywalk0(p.C - c0, tid), ywalk1(wide ? p.C - c0 - 64 : 64, tid);
+        int raw_n = 0;  // raw tiles so far
+        auto take = [&](auto& piece, const ChunkWalk& walk) {
+            const int r = raw_n % max(1, S::kRaws);
+            ok = mbar_wait_bounded(&raw_full[r], static_cast<unsigned>(raw_n / max(1, S::kRaws)) & 1u, kCopyWaitLimitNs);
             if (!ok) return;
-            store_grad(gsm + s * S::kG, ch ? walk1 : walk0, now);
-            hand_over(&full_g[s], lane);
-            if (sums) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    // rows past the tile hold zeros
-                    const float v[8] = {now.v[q][0].x, now.v[q][0].y, now.v[q][0].z, now.v[q][0].w,
-                                        now.v[q][1].x, now.v[q][1].y, now.v[q][1].z, now.v[q][1].w};
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        if (ch == 0) bs[0][k] += v[k];
-                        else bs[1][k] += v[k];
-                    }
-                }
-            }
-            fetch_g(n + 2, now);  // two chunks ahead
+            piece.from_raw(raws + r * kRaw, walk);
         };
-        GradPiece ga, gb2;
-        fetch_y(0, 0);
-        fetch_g(0, ga);
-        fetch_g(1, gb2);
-        for (int i = 0; i < mine && ok; ++i) {
-            const int ys = i % S::kYStages, yn = i / S::kYStages;
-            if (yn > 0) ok = mbar_wait_bounded(&empty_y[ys], static_cast<unsigned>(yn - 1) & 1u, kCopyWaitLimitNs);
-            if (!ok) break;
-#pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-                if (q4 >= npiece) break;
-                const int q = q4 % kYAhead;
-                if (q4 > 0 && q == 0) fetch_y(i, q4);
-                const int e = q4 * kConv + tid, r = e / per_row, ch = e % per_row;
-                float v[8];
-                if constexpr (sizeof(T) == 4) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = reinterpret_cast<const float*>(yr[q])[k];
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 f = unpack2(reinterpret_cast<const uint32_t*>(yr[q])[k], static_cast<T*>(nullptr));
-                        v[2 * k] = f.x;
-                        v[2 * k + 1] = f.y;
-                    }
-                }
-                store_split8<YP>(sm + ys * S::kY + (ch >> 3) * 16384, 32768u, r, ch & 7, v);
+        auto give_back = [&] {
+            if (RAW) {
+                if (lane == 0) mbar_arrive(&raw_empty[raw_n % max(1, S::kRaws)]);
+                ++raw_n;
             }
-            hand_over(&full_y[ys], lane);
-            fetch_y(i + 1, 0);
-            if (nch == 2) {
-                chunk(2 * i, 0, ga);
-                if (ok) chunk(2 * i + 1, 1, gb2);
-            } else if (i & 1) {
-                chunk(i, 0, gb2);
-            } else {
-                chunk(i, 0, ga);
+        };
+        for (int i = 0; i < mine && ok; ++i) {
+            if constexpr (!S::kDirectY) {
+                const int ys = i % S::kYStages, yn = i / S::kYStages;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    if (b >= ny || !ok) break;
+                    const ChunkWalk& walk = b ? ywalk1 : ywalk0;
+                    Piece<T> piece;
+                    if constexpr (RAW) take(piece, walk);
+                    else piece.from_global(y, walk, pixel(i), p.M, c0 + b * 64, p.C);
+                    if (b == 0 && yn > 0)
+                        ok = ok && mbar_wait_bounded(&empty_y[ys], static_cast<unsigned>(yn - 1) & 1u, kCopyWaitLimitNs);
+                    if (!ok) break;
+                    piece.template store<YP>(sm + ys * S::kY + b * 16384, 32768u, walk);
+                    hand_over(&full_y[ys], lane);
+                    give_back();
+                }
+            }
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {
+                if (ch >= nch || !ok) break;
+                const ChunkWalk& walk = ch ? walk1 : walk0;
+                const int n = i * nch + ch, s = n & 1;
+                Piece<float> piece;
+                if constexpr (RAW) take(piece, walk);
+                else piece.from_global(grec, walk, pixel(i), p.M, g0 + ch * 64, p.NO);
+                if (n >= 2) ok = ok && mbar_wait_bounded(&empty_g[s], static_cast<unsigned>((n >> 1) - 1) & 1u, kCopyWaitLimitNs);
+                if (!ok) break;
+                piece.template store<3>(gsm + s * S::kG, 16384u, walk);
+                hand_over(&full_g[s], lane);
+                give_back();
+                if (sums)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) bs[ch][k] += piece.v[0][k] + piece.v[1][k];  // rows past the tile: zeros
             }
         }
         if (sums) {
@@ -554,17 +560,53 @@ pred_grad_w_kernel(const float* __restrict__ grec, const T* __restrict__ y, floa
             }
         }
     } else {
-        // warp 16's first lane issues the products of up to kFlushTiles tiles; then all four read the sums out
+        // Up to kFlushTiles tiles: warp 16's first lane issues the products, warp 17's first lane the loads; then
+        // all four warps read the sums out.
         constexpr uint32_t idesc = tc::idesc_f16(tc::kFmtBf16, 64, true, true);
         const unsigned second = wide ? 16384u : 0u;
         const int quarter = warp & 3, row = quarter * 32 + lane, c = c0 + row;
         const bool on = c < p.C && (wide || row < 64);
+        int raw_n = 0;
+        auto load_raw = [&](const CUtensorMap* map, int col, int step, int blocks, long long m0) {
+            const int r = raw_n % max(1, S::kRaws);
+            if (raw_n >= S::kRaws)
+                ok = mbar_wait_bounded(&raw_empty[r], static_cast<unsigned>(raw_n / max(1, S::kRaws) - 1) & 1u, kCopyWaitLimitNs);
+            if (!ok) return;
+            mbar_expect_tx(&raw_full[r], blocks * 16384u);
+            for (int b = 0; b < blocks; ++b)
+                tc::tma_load_3d(raws + r * kRaw + b * 16384, map, col + b * step, static_cast<int>(m0), 0, &raw_full[r]);
+            mbar_arrive(&raw_full[r]);
+            ++raw_n;
+        };
         for (int f = 0; f * kFlushTiles < mine; ++f) {
+            const int begin = f * kFlushTiles, end = min(mine, begin + kFlushTiles);
+            if (RAW && warp == 17 && lane == 0) {
+                for (int i = begin; i < end && ok; ++i) {
+                    const long long m0 = pixel(i);
+                    if constexpr (S::kDirectY) {
+                        const int ys = i % S::kYStages, yn = i / S::kYStages;
+                        if (yn > 0) ok = mbar_wait_bounded(&empty_y[ys], static_cast<unsigned>(yn - 1) & 1u, kCopyWaitLimitNs);
+                        if (!ok) break;
+                        mbar_expect_tx(&full_y[ys], ny * 16384u);
+                        for (int b = 0; b < ny; ++b)
+                            tc::tma_load_3d(sm + ys * S::kY + b * 16384, &ymap, c0 + b * 64, static_cast<int>(m0), 0, &full_y[ys]);
+                        mbar_arrive(&full_y[ys]);
+                    } else {
+                        for (int b = 0; b < ny && ok; ++b) {
+                            const int col = c0 + b * 64;
+                            load_raw(&ymap, col, 32, sizeof(T) == 4 && col + 32 < p.C ? 2 : 1, m0);
+                        }
+                    }
+                    for (int ch = 0; ch < nch && ok; ++ch) {
+                        const int col = g0 + ch * 64;
+                        load_raw(&gmap, col, 32, col + 32 < p.NO ? 2 : 1, m0);
+                    }
+                }
+            }
             if (warp == 16 && lane == 0) {
                 tc::fence_after();
-                const int last = min(mine, (f + 1) * kFlushTiles);
-                for (int i = f * kFlushTiles; i < last && ok; ++i) {
-                    const int ys = i % S::kYStages, t = i - f * kFlushTiles;
+                for (int i = begin; i < end && ok; ++i) {
+                    const int ys = i % S::kYStages, t = i - begin;
                     ok = mbar_wait_bounded(&full_y[ys], static_cast<unsigned>(i / S::kYStages) & 1u, kCopyWaitLimitNs);
                     for (int ch = 0; ch < nch && ok; ++ch) {
                         const int n = i * nch + ch, s = n & 1;
