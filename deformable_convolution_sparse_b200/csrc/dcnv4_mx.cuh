@@ -254,13 +254,15 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(int n, uint32_t sf) {
     return (sf << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) | (1u << 27) |
            (sf << 29);
 }
+// (called by a whole warp, as mma_f16)
 __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                         bool accumulate) {
+                                         bool accumulate, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate ? 1u : 0u)
+        "setp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate ? 1u : 0u), "r"(lead)
         : "memory");
 }
 // 32 rows of 16 bytes (row r at r * 16) into 4 tensor-memory columns, the same
@@ -309,7 +311,7 @@ predictor_mx_kernel(const __grid_constant__ CUtensorMap rmap, const T* __restric
     uint64_t* done = reinterpret_cast<uint64_t*>(sm + p.smem_bars);
     uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
     constexpr int E = sizeof(T);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = static_cast<int>(tc::uniform(threadIdx.x >> 5)), lane = tid & 31;
     const int cta = static_cast<int>(blockIdx.x) % p.walkers, walkers = p.walkers;
     const int s0 = static_cast<int>(blockIdx.x) / p.walkers * p.NT, width = min(p.NT, p.NO - s0), np = (width + 15) / 16 * 16;
 
@@ -324,7 +326,7 @@ predictor_mx_kernel(const __grid_constant__ CUtensorMap rmap, const T* __restric
     tc::fence_before();
     __syncthreads();  // every CTA holds its tensor memory before the next launch may start
     tc::fence_after();
-    const uint32_t tmem = *slot;
+    const uint32_t tmem = tc::uniform(*slot);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -433,17 +435,20 @@ predictor_mx_kernel(const __grid_constant__ CUtensorMap rmap, const T* __restric
         if (warp == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         tc::fence_before();
         __syncthreads();
-        if (tid == 0) {
+        if (warp == 0) {
             tc::fence_after();
-            if (it == 0)
-                for (int i = 0; i < p.kc * p.groups; ++i) tc::copy_scales(tmem + p.sfb_col + i * 4, smem_addr(sfb + i * 512));
-            for (int i = 0; i < p.kc; ++i) tc::copy_scales(tmem + p.sfa_col + i * 4, smem_addr(sfa + i * 512));
+            const uint32_t lead = tc::lead_lane();
+            if (lead) {
+                if (it == 0)
+                    for (int i = 0; i < p.kc * p.groups; ++i) tc::copy_scales(tmem + p.sfb_col + i * 4, smem_addr(sfb + i * 512));
+                for (int i = 0; i < p.kc; ++i) tc::copy_scales(tmem + p.sfa_col + i * 4, smem_addr(sfa + i * 512));
+            }
+            __syncwarp();
+            const uint64_t a = tc::smem_desc(smem_addr(asm_), 2048u, 128u, 0u), b = tc::smem_desc(smem_addr(bsm), 16u * p.NT, 128u, 0u);
             for (int k = 0; k < p.k64; ++k)
-                tc::mma_mxf4(tmem, tc::smem_desc(smem_addr(asm_) + k * 4096u, 2048u, 128u, 0u),
-                             tc::smem_desc(smem_addr(bsm) + k * 32u * p.NT, 16u * p.NT, 128u, 0u),
-                             tc::idesc_mxf4(np, (k & 1) * 2u), tmem + p.sfa_col + (k >> 1) * 4,
-                             tmem + p.sfb_col + (k >> 1) * 4 * p.groups, k > 0);
-            tc::commit(done);
+                tc::mma_mxf4(tmem, a + k * 256u, b + static_cast<unsigned>(k) * 2u * p.NT, tc::idesc_mxf4(np, (k & 1) * 2u),
+                             tmem + p.sfa_col + (k >> 1) * 4, tmem + p.sfb_col + (k >> 1) * 4 * p.groups, k > 0, lead);
+            if (lead) tc::commit(done);
         }
         ok = __syncthreads_and(mbar_wait_bounded(done, static_cast<unsigned>(it) & 1u, kCopyWaitLimitNs)) != 0;
         if (!ok) break;

@@ -198,8 +198,8 @@ __device__ __forceinline__ uint4 ortho_load(const __half* p) {
 //                               columns: an MN-major operand)
 //   kLast:  kApply with the result rounded to T and written to `out`
 // Warp 0 (one lane) loads 64 k at a time by TMA: 128 rows x 64 k of the left
-// planes, 64 x 64 of the right ones, in a ring of STAGES; warp 1 (one
-// lane) issues the products; warps 2..9 read the accumulators, form the result
+// planes, 64 x 64 of the right ones, in a ring of STAGES; warp 1 issues the
+// products; warps 2..9 read the accumulators, form the result
 // and write it as planes through shared memory (the idle ring) and TMA. A
 // product's time is mostly latency (per tile: first load 0.7 us, products 0.4
 // us per 64 k, epilogue 0.5, store 0.6; the launch about 2 us more), so the
@@ -229,7 +229,7 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + STAGES * kOrthoStageBytes);
     uint64_t *full = bars, *empty = bars + STAGES, *done = bars + 2 * STAGES;
     uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = static_cast<int>(tc::uniform(threadIdx.x >> 5)), lane = tid & 31;
     const unsigned per = static_cast<unsigned>(g.tiles_i) * g.tiles_j;
     const int mat = static_cast<int>(blockIdx.x / per);
     const unsigned t = blockIdx.x - static_cast<unsigned>(mat) * per;
@@ -250,7 +250,7 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
     tc::fence_before();
     __syncthreads();  // every CTA holds its tensor memory before the next launch may start
     tc::fence_after();
-    const uint32_t tmem = *slot;
+    const uint32_t tmem = tc::uniform(*slot);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     bool ok = true;
@@ -275,27 +275,26 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr bool mn = MODE >= kApply;
-            constexpr uint32_t idesc = tc::idesc_f16(tc::kFmtF16, 64, false, mn);
-            for (int kb = 0; kb < g.kblocks; ++kb) {
-                const int s = kb % STAGES;
-                ok = mbar_wait_bounded(&full[s], static_cast<unsigned>(kb / STAGES) & 1u, kCopyWaitLimitNs);
-                if (!ok) break;
-                tc::fence_after();
-                const unsigned base = smem_addr(sm + s * kOrthoStageBytes);
-                const uint32_t a = tc::sw128(base), b = tc::sw128(base + 32768u);
+        constexpr bool mn = MODE >= kApply;
+        constexpr uint32_t idesc = tc::idesc_f16(tc::kFmtF16, 64, false, mn);
+        const uint32_t lead = tc::lead_lane();
+        for (int kb = 0; kb < g.kblocks; ++kb) {
+            const int s = kb % STAGES;
+            ok = tc::warp_wait(&full[s], static_cast<unsigned>(kb / STAGES) & 1u, kCopyWaitLimitNs);
+            if (!ok) break;
+            tc::fence_after();
+            const unsigned base = smem_addr(sm + s * kOrthoStageBytes);
+            const uint32_t a = tc::sw128(base), b = tc::sw128(base + 32768u);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t ah = a + k * 2, al = ah + 1024, bh = b + (mn ? k * 128 : k * 2), bl = bh + 512;
-                    tc::mma_f16(tmem + 192u, ah, bl, idesc, kb > 0 || k > 0);
-                    tc::mma_f16(tmem + 192u, al, bh, idesc, true);
-                    tc::mma_f16(tmem + (k % 3) * 64u, ah, bh, idesc, kb > 0 || k >= 3);
-                }
-                tc::commit(&empty[s]);
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t ah = a + k * 2, al = ah + 1024, bh = b + k * (mn ? 128 : 2), bl = bh + 512;
+                tc::mma_f16(tmem + 192u, ah, bl, idesc, kb > 0 || k > 0, lead);
+                tc::mma_f16(tmem + 192u, al, bh, idesc, true, lead);
+                tc::mma_f16(tmem + (k % 3) * 64u, ah, bh, idesc, kb > 0 || k >= 3, lead);
             }
-            if (ok) tc::commit(done);
+            if (lead) tc::commit(&empty[s]);
         }
+        if (ok && lead) tc::commit(done);
     } else {
         const int quarter = warp & 3, row = quarter * 32 + lane, et = tid - 64, half = (warp - 2) >> 2;
         const int i = i0 + row, lift = p.lift[mat];
@@ -398,7 +397,7 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
 // bytes each, 128-byte swizzle; rows and columns past the matrix are zero. X's
 // blocks serve as both operands of the Gram product (K-major) and as the right
 // one of the application (MN-major), A's as both of the polynomial, which
-// overwrites them with P. One thread issues a product's instructions, then all
+// overwrites them with P. One warp issues a product's instructions, then all
 // warps turn the accumulators into the next operand. What bounds it is the
 // chain of 3 * steps dependent products, each a few hundred cycles of tensor
 // work between two barriers.
@@ -431,7 +430,7 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
     __shared__ uint32_t slot;
     unsigned char* xs = ortho_smem_raw + ((1024u - (smem_addr(ortho_smem_raw) & 1023u)) & 1023u);
     unsigned char* as = xs + g.xb * kOrthoBlock;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = static_cast<int>(tc::uniform(threadIdx.x >> 5)), lane = tid & 31;
     const int quarter = warp & 3, row = quarter * 32 + lane, part = warp >> 2;
     if (tid == 0) {
         mbar_init(&done_bar, 1);
@@ -443,7 +442,7 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
     tc::fence_before();
     __syncthreads();  // every CTA holds its tensor memory before the next launch may start
     tc::fence_after();
-    const uint32_t tmem = slot, lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t tmem = tc::uniform(slot), lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -463,34 +462,35 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
 
     unsigned phase = 0;
     bool ok = true;
-    // hands the operands over to the tensor cores, lets thread 0 issue, and waits for the products
+    // hands the operands over to the tensor cores, lets warp 0 issue, and waits for the products
     auto product = [&](auto issue) {
         fence_proxy_async();
         tc::fence_before();
         __syncthreads();
-        if (tid == 0) {
+        if (warp == 0) {
             tc::fence_after();
-            issue();
-            tc::commit(&done_bar);
+            const uint32_t lead = tc::lead_lane();
+            issue(lead);
+            if (lead) tc::commit(&done_bar);
         }
         ok = __syncthreads_and(mbar_wait_bounded(&done_bar, phase & 1u, kCopyWaitLimitNs)) != 0;
         ++phase;
         tc::fence_after();
     };
     // square products: n columns, four accumulators n16 columns apart; K-major operands with ksteps of 16 k
-    auto square = [&](unsigned base, int ksteps) {
+    auto square = [&](unsigned base, int ksteps, uint32_t lead) {
         const uint32_t idesc = tc::idesc_f16(tc::kFmtF16, g.n16, false, false);
         const uint32_t cross = tmem + 3 * g.n16;
-        uint32_t h = tc::sw128(base);
-        for (int k0 = 0; k0 < ksteps; k0 += 4, h += kOrthoBlock / 16)  // a block of 64 k
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (k0 + k >= ksteps) break;
-                const uint32_t hk = h + k * 2, lk = hk + 1024;
-                tc::mma_f16(cross, hk, lk, idesc, k0 > 0 || k > 0);
-                tc::mma_f16(cross, lk, hk, idesc, true);
-                tc::mma_f16(tmem + (k % 3) * g.n16, hk, hk, idesc, k0 > 0 || k >= 3);
-            }
+        uint32_t h = tc::sw128(base), high = tmem;
+#pragma unroll 1
+        for (int k = 0; k < ksteps; ++k) {
+            const uint32_t l = h + 1024;
+            tc::mma_f16(cross, h, l, idesc, k > 0, lead);
+            tc::mma_f16(cross, l, h, idesc, true, lead);
+            tc::mma_f16(high, h, h, idesc, k >= 3, lead);
+            high = high == tmem + 2 * g.n16 ? tmem : high + g.n16;
+            h += (k & 3) == 3 ? kOrthoBlock / 16 - 6 : 2;  // 16 k further, or the next block of 64
+        }
     };
     const int nchunks = g.n16 / 16;
     for (int s = 0; s < g.steps && ok; ++s) {
@@ -519,7 +519,7 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
             at[1024] = *reinterpret_cast<const uint4*>(lo);
         };
         // A = X X^T
-        product([&] { square(smem_addr(xs), g.m16 / 16); });
+        product([&](uint32_t lead) { square(smem_addr(xs), g.m16 / 16, lead); });
         if (!ok) break;
         for (int cc = part; cc < nchunks; cc += 4) {
             float v[16];
@@ -533,7 +533,7 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
             }
         }
         // P = a I + b A + c A A, over A
-        product([&] { square(smem_addr(as), nchunks); });
+        product([&](uint32_t lead) { square(smem_addr(as), nchunks, lead); });
         if (!ok) break;
         const float ub = scalbnf(p.b, -2 * now), uc = scalbnf(p.c, -4 * now) * (kOrthoSP / (kOrthoSA * kOrthoSA));
         for (int cc = part; cc < nchunks; cc += 4) {
@@ -558,18 +558,17 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
         const bool last = s + 1 == g.steps;
         for (int j0 = 0; j0 < g.m16 && ok; j0 += 256) {
             const int width = min(256, g.m16 - j0);
-            product([&] {
+            product([&](uint32_t lead) {
                 const uint32_t idesc = tc::idesc_f16(tc::kFmtF16, width, false, true);
-                uint32_t a = tc::sw128(smem_addr(as)), b = tc::sw128(smem_addr(xs) + (j0 >> 6) * kOrthoBlock, kOrthoBlock);
-                for (int k0 = 0; k0 < nchunks; k0 += 4, a += kOrthoBlock / 16, b += 4 * 128)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (k0 + k >= nchunks) break;
-                        const uint32_t ah = a + k * 2, al = ah + 1024, bh = b + k * 128, bl = bh + 1024;
-                        tc::mma_f16(tmem + width, ah, bl, idesc, k0 > 0 || k > 0);
-                        tc::mma_f16(tmem + width, al, bh, idesc, true);
-                        tc::mma_f16(tmem, ah, bh, idesc, k0 > 0 || k > 0);
-                    }
+                uint32_t ah = tc::sw128(smem_addr(as)), bh = tc::sw128(smem_addr(xs) + (j0 >> 6) * kOrthoBlock, kOrthoBlock);
+#pragma unroll 1
+                for (int k = 0; k < nchunks; ++k, bh += 128) {
+                    const uint32_t al = ah + 1024, bl = bh + 1024;
+                    tc::mma_f16(tmem + width, ah, bl, idesc, k > 0, lead);
+                    tc::mma_f16(tmem + width, al, bh, idesc, true, lead);
+                    tc::mma_f16(tmem, ah, bh, idesc, k > 0, lead);
+                    ah += (k & 3) == 3 ? kOrthoBlock / 16 - 6 : 2;
+                }
             });
             if (!ok) break;
             const float ux = scalbnf(1.f, (last ? 0 : next) - now) / (last ? kOrthoSP * kOrthoSX : kOrthoSP);

@@ -218,7 +218,7 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     uint64_t *full_g = bars, *full_w = bars + 2, *empty = bars + 4, *acc_full = bars + 6, *acc_empty = bars + 8,
              *raw_full = bars + 10, *raw_empty = bars + 12;
     uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 14);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = static_cast<int>(tc::uniform(threadIdx.x >> 5)), lane = tid & 31;
 
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
@@ -236,7 +236,7 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     tc::fence_before();
     __syncthreads();  // every CTA holds its tensor memory before the next launch may start
     tc::fence_after();
-    const uint32_t tmem = *slot;
+    const uint32_t tmem = tc::uniform(*slot);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -311,38 +311,44 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             }
         }
     } else if (warp == 17) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = tc::idesc_f16(tc::kFmtBf16, CT, false, true);
-            for (long long it = 0; it < steps && ok; ++it) {
-                const int s = static_cast<int>(it & 1), chunk = static_cast<int>(it % p.chunks);
-                const long long n = it / p.chunks;
-                const int b = static_cast<int>(n & 1);
-                if (chunk == 0 && n >= 2)
-                    ok = mbar_wait_bounded(&acc_empty[b], static_cast<unsigned>((n >> 1) - 1) & 1u, kCopyWaitLimitNs);
-                ok = ok && mbar_wait_bounded(&full_g[s], static_cast<unsigned>(it >> 1) & 1u, kCopyWaitLimitNs) &&
-                     mbar_wait_bounded(&full_w[s], static_cast<unsigned>(it >> 1) & 1u, kCopyWaitLimitNs);
-                if (!ok) break;
-                tc::fence_after();
-                const uint32_t acc = tmem + b * S::kAcc, low = acc + S::kHigh * CT;
-                const unsigned base = smem_addr(sm + s * S::kStage);
-                const uint32_t a = tc::sw128(base), w = tc::sw128(base + 3u * 16384u, 8192u);
-                const int ksteps = (min(64, p.NO - chunk * 64) + 15) / 16;
+        constexpr uint32_t idesc = tc::idesc_f16(tc::kFmtBf16, CT, false, true);
+        const uint32_t lead = tc::lead_lane();
+        int chunk = 0, b = 0;
+        long long n = 0;  // the item
+        for (long long it = 0; it < steps && ok; ++it) {
+            const int s = static_cast<int>(it & 1);
+            if (chunk == 0 && n >= 2)
+                ok = tc::warp_wait(&acc_empty[b], static_cast<unsigned>((n >> 1) - 1) & 1u, kCopyWaitLimitNs);
+            ok = ok && tc::warp_wait(&full_g[s], static_cast<unsigned>(it >> 1) & 1u, kCopyWaitLimitNs) &&
+                 tc::warp_wait(&full_w[s], static_cast<unsigned>(it >> 1) & 1u, kCopyWaitLimitNs);
+            if (!ok) break;
+            tc::fence_after();
+            const uint32_t acc = tmem + b * S::kAcc, low = acc + S::kHigh * CT;
+            const unsigned base = smem_addr(sm + s * S::kStage);
+            const uint32_t a = tc::sw128(base), w = tc::sw128(base + 3u * 16384u, 8192u);
+            const int ksteps = (min(64, p.NO - chunk * 64) + 15) / 16;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (k >= ksteps) break;
+            for (int k = 0; k < 4; ++k) {
+                if (k >= ksteps) break;
 #pragma unroll
-                    for (int i = 0; i < 3; ++i)
+                for (int i = 0; i < 3; ++i)
 #pragma unroll
-                        for (int j = 0; j < WP; ++j) {
-                            if (i + j > 2) continue;
-                            const uint32_t ad = a + (i * 16384 + k * 32) / 16, bd = w + (j * (CT / 64) * 8192 + k * 2048) / 16;
-                            const bool first_low = k == 0 && i == (WP > 1 ? 0 : 1) && j == (WP > 1 ? 1 : 0);
-                            if (i + j == 0) tc::mma_f16(acc + (k % S::kHigh) * CT, ad, bd, idesc, chunk > 0 || k >= S::kHigh);
-                            else tc::mma_f16(low, ad, bd, idesc, chunk > 0 || !first_low);
-                        }
-                }
+                    for (int j = 0; j < WP; ++j) {
+                        if (i + j > 2) continue;
+                        const uint32_t ad = a + i * 1024 + k * 2, bd = w + j * (CT / 64) * 512 + k * 128;
+                        const bool first_low = k == 0 && i == (WP > 1 ? 0 : 1) && j == (WP > 1 ? 1 : 0);
+                        if (i + j == 0) tc::mma_f16(acc + (k % S::kHigh) * CT, ad, bd, idesc, chunk > 0 || k >= S::kHigh, lead);
+                        else tc::mma_f16(low, ad, bd, idesc, chunk > 0 || !first_low, lead);
+                    }
+            }
+            if (lead) {
                 tc::commit(&empty[s]);
                 if (chunk == p.chunks - 1) tc::commit(&acc_full[b]);
+            }
+            if (++chunk == p.chunks) {
+                chunk = 0;
+                b ^= 1;
+                ++n;
             }
         }
     } else {
@@ -411,7 +417,7 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
 // left operand) and, 64 slots at a time, of g (the right one), both with rows
 // that run along channels or slots: MN-major; the same threads sum g for the
 // bias. y in bf16 is its own plane and comes straight by TMA. Of warps 16..19,
-// one lane issues the products and another the TMA loads; every kFlushTiles
+// one issues the products and a lane of another the TMA loads; every kFlushTiles
 // tiles all four read the accumulators out to part [walkers][NO][C], lanes
 // along the channels. A slice of at most 64 channels reads its one block of 64
 // for both halves of the M = 128 products.
@@ -442,7 +448,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
     uint64_t *full_y = bars, *empty_y = bars + 2, *full_g = bars + 4, *empty_g = bars + 6, *acc_full = bars + 8,
              *raw_full = bars + 9, *raw_empty = bars + 11;
     uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 13);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = static_cast<int>(tc::uniform(threadIdx.x >> 5)), lane = tid & 31;
 
     // CTA -> walker, (slice, group); the slices and groups of one walker side by side
     const int per = p.slices * p.groups;
@@ -470,7 +476,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
     tc::fence_before();
     __syncthreads();  // every CTA holds its tensor memory before the next launch may start
     tc::fence_after();
-    const uint32_t tmem = *slot;
+    const uint32_t tmem = tc::uniform(*slot);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     bool ok = true;
@@ -560,7 +566,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
             }
         }
     } else {
-        // Up to kFlushTiles tiles: warp 16's first lane issues the products, warp 17's first lane the loads; then
+        // Up to kFlushTiles tiles: warp 16 issues the products, a lane of warp 17 the loads; then
         // all four warps read the sums out.
         constexpr uint32_t idesc = tc::idesc_f16(tc::kFmtBf16, 64, true, true);
         const unsigned second = wide ? 16384u : 0u;
@@ -603,35 +609,39 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
                     }
                 }
             }
-            if (warp == 16 && lane == 0) {
+            if (warp == 16) {
                 tc::fence_after();
+                const uint32_t lead = tc::lead_lane();
                 for (int i = begin; i < end && ok; ++i) {
                     const int ys = i % S::kYStages, t = i - begin;
-                    ok = mbar_wait_bounded(&full_y[ys], static_cast<unsigned>(i / S::kYStages) & 1u, kCopyWaitLimitNs);
+                    ok = tc::warp_wait(&full_y[ys], static_cast<unsigned>(i / S::kYStages) & 1u, kCopyWaitLimitNs);
                     for (int ch = 0; ch < nch && ok; ++ch) {
                         const int n = i * nch + ch, s = n & 1;
-                        ok = mbar_wait_bounded(&full_g[s], static_cast<unsigned>(n >> 1) & 1u, kCopyWaitLimitNs);
+                        ok = tc::warp_wait(&full_g[s], static_cast<unsigned>(n >> 1) & 1u, kCopyWaitLimitNs);
                         if (!ok) break;
                         tc::fence_after();
                         const uint32_t a = tc::sw128(smem_addr(sm + ys * S::kY), second), b = tc::sw128(smem_addr(gsm + s * S::kG));
                         const uint32_t acc = tmem + ch * 64;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
+                        uint32_t high = acc;
+#pragma unroll 1
+                        for (int k = 0; k < 8; ++k) {
 #pragma unroll
                             for (int gi = 0; gi < 3; ++gi)
 #pragma unroll
                                 for (int j = 0; j < YP; ++j) {
                                     if (gi + j > 2) continue;
-                                    const uint32_t ad = a + (j * 32768 + k * 2048) / 16, bd = b + (gi * 16384 + k * 2048) / 16;
-                                    const bool first_low = k == 0 && gi == (YP > 1 ? 0 : 1) && j == (YP > 1 ? 1 : 0);
-                                    if (gi + j == 0) tc::mma_f16(acc + (k % 3) * 128, ad, bd, idesc, t > 0 || k >= 3);
-                                    else tc::mma_f16(acc + 384, ad, bd, idesc, t > 0 || !first_low);
+                                    const uint32_t ad = a + j * 2048 + k * 128, bd = b + gi * 1024 + k * 128;
+                                    const bool first_low = gi == (YP > 1 ? 0 : 1) && j == (YP > 1 ? 1 : 0);
+                                    if (gi + j == 0) tc::mma_f16(high, ad, bd, idesc, t > 0 || k >= 3, lead);
+                                    else tc::mma_f16(acc + 384, ad, bd, idesc, t > 0 || k > 0 || !first_low, lead);
                                 }
-                        tc::commit(&empty_g[s]);
+                            high = high == acc + 256 ? acc : high + 128;
+                        }
+                        if (lead) tc::commit(&empty_g[s]);
                     }
-                    if (ok) tc::commit(&empty_y[ys]);
+                    if (ok && lead) tc::commit(&empty_y[ys]);
                 }
-                if (ok) tc::commit(acc_full);
+                if (ok && lead) tc::commit(acc_full);
             }
             __syncwarp();
             ok = tc::bar_and(1, 128, ok && mbar_wait_bounded(acc_full, static_cast<unsigned>(f) & 1u, kFlushWaitLimitNs));

@@ -26,9 +26,7 @@ __device__ __forceinline__ uint64_t smem_desc(unsigned saddr, unsigned lead, uns
 // two atoms, +2048 bytes). Such an operand is its descriptor's low word: start
 // address and, in the upper half, the step to the next 64 M/N indexes of an
 // MN-major operand (K-major: unused); `bytes` further on it is the word plus
-// bytes / 16. The high word is the same for all of them. (The issuing thread's
-// own instructions bound a product's rate when every descriptor is built from
-// its parts: 75 cycles per 128 x 64 x 16 product, against 20 with this form.)
+// bytes / 16. The high word is the same for all of them.
 __device__ __forceinline__ uint32_t sw128(unsigned saddr, unsigned lead = 16u) {
     return ((saddr >> 4) & 0x3FFFu) | ((lead >> 4) << 16);
 }
@@ -41,16 +39,35 @@ __host__ __device__ constexpr uint32_t idesc_f16(uint32_t fmt, int n, bool a_mn_
            (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 }
 
-// a, b: operands as sw128() gives them
-__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+// A whole converged warp makes the call, with the same values in every lane
+// (warp index, tensor-memory address and the like taken from uniform()); its
+// one lane with `lead` set (lead_lane()) issues. What a product needs then
+// stays in uniform registers: in a branch of one lane, whose values the
+// compiler has to move there for every product, the issue of a 128 x 64 x 16
+// product took 86 cycles, in this form 49 (what its operands' shared-memory
+// reads take); a 128 x 128 x 16 one takes 65. a, b: operands as sw128() gives
+// them.
+__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
         "mov.b64 da, {%1, %5};\n\t"
         "mov.b64 db, {%2, %5};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(kSw128High)
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(kSw128High), "r"(lead)
         : "memory");
+}
+// 1 in one lane of the (converged) warp, 0 in the others
+__device__ __forceinline__ uint32_t lead_lane() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+// a bounded wait of a whole warp, with one answer
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit_ns)) != 0;
 }
 // arrives on `bar` once every tcgen05 operation this thread issued so far has completed
 __device__ __forceinline__ void commit(uint64_t* bar) {
