@@ -158,6 +158,16 @@ struct Piece {
             }
         }
     }
+    // All lanes of the warp: returns once every lane's values have arrived. The vote needs them all, and
+    // instructions issue in order; the branch it decides does nothing of use.
+    __device__ __forceinline__ void landed() const {
+        uint32_t u = 0u;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u |= __float_as_uint(v[q][k]);
+        if (__any_sync(0xffffffffu, u == 0x80000001u)) __nanosleep(1);
+    }
     // from memory: rows m0.. of M, columns c0.. of C
     __device__ __forceinline__ void from_global(const T* __restrict__ x, const ChunkWalk& walk, long long m0, int M, int c0, int C) {
 #pragma unroll
@@ -258,6 +268,8 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 ok = mbar_wait_bounded(&raw_full[r], static_cast<unsigned>(it / S::kRaws) & 1u, kCopyWaitLimitNs);
                 if (!ok) break;
                 piece.from_raw(raws + r * kRaw, walk);
+                piece.landed();
+                if (lane == 0) mbar_arrive(&raw_empty[r]);
             } else {
                 const long long item = blockIdx.x + n * gridDim.x;
                 piece.from_global(grec, walk, item / p.slices * 128, p.M, chunk * 64, p.NO);
@@ -266,7 +278,6 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             if (!ok) break;
             piece.template store<3>(sm + s * S::kStage, 16384u, walk);
             hand_over(&full_g[s], lane);
-            if (RAW && lane == 0) mbar_arrive(&raw_empty[r]);
             if (++chunk == p.chunks) {
                 chunk = 0;
                 ++n;
@@ -492,12 +503,9 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
             ok = mbar_wait_bounded(&raw_full[r], static_cast<unsigned>(raw_n / max(1, S::kRaws)) & 1u, kCopyWaitLimitNs);
             if (!ok) return;
             piece.from_raw(raws + r * kRaw, walk);
-        };
-        auto give_back = [&] {
-            if (RAW) {
-                if (lane == 0) mbar_arrive(&raw_empty[raw_n % max(1, S::kRaws)]);
-                ++raw_n;
-            }
+            piece.landed();
+            if (lane == 0) mbar_arrive(&raw_empty[r]);
+            ++raw_n;
         };
         for (int i = 0; i < mine && ok; ++i) {
             if constexpr (!S::kDirectY) {
@@ -514,7 +522,6 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
                     if (!ok) break;
                     piece.template store<YP>(sm + ys * S::kY + b * 16384, 32768u, walk);
                     hand_over(&full_y[ys], lane);
-                    give_back();
                 }
             }
 #pragma unroll
@@ -529,7 +536,6 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
                 if (!ok) break;
                 piece.template store<3>(gsm + s * S::kG, 16384u, walk);
                 hand_over(&full_g[s], lane);
-                give_back();
                 if (sums)
 #pragma unroll
                     for (int k = 0; k < 8; ++k) bs[ch][k] += piece.v[0][k] + piece.v[1][k];  // rows past the tile: zeros

@@ -266,6 +266,26 @@ def test_predictor_backward(case, dtype, cuda_device):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,C,G", [(20000, 128, 8), (30000, 64, 4), (5000, 320, 8)])
+def test_predictor_backward_is_the_same_in_every_run(M, C, G, dtype, cuda_device):
+    """Many tiles per SM, so that every ring goes round: equal bits, and integers that every sum holds exactly."""
+    g = torch.Generator(device=cuda_device).manual_seed(M)
+    y = torch.randint(-2, 3, (M, C), generator=g, device=cuda_device).to(TD[dtype])
+    w = torch.randint(-2, 3, (27 * G, C), generator=g, device=cuda_device).to(TD[dtype])
+    gr = torch.randint(-8, 9, (M, G, 27), generator=g, device=cuda_device).float()
+    first = dcn.predictor_backward(y, w, gr, G=G, K=3)
+    sl = torch.tensor(ow.slots(G, 9), device=cuda_device)
+    gp = gr.double().view(M, -1)[:, sl]
+    # |sums| <= M * 16 < 2^24
+    assert torch.equal(first[0].double(), gp @ w.double())
+    assert torch.equal(first[1].double(), gp.t() @ y.double())
+    assert torch.equal(first[2].double(), gp.sum(dim=0))
+    for _ in range(10):
+        for a, b in zip(dcn.predictor_backward(y, w, gr, G=G, K=3), first):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 def test_predictor_backward_far_apart_magnitudes_and_misaligned_rows(dtype, cuda_device):
     """Gradients from 1e-30 to 1e30 in one call: every sum keeps fp32 precision relative to its own terms."""
     M, C, G, K = 300, 40, 3, 3
