@@ -141,11 +141,14 @@ struct Piece {
                 continue;
             }
             if constexpr (sizeof(T) == 4) {
+                // groups 0..3 and 4..7 of a row lie in two blocks at the same banks: the latter read their second
+                // half first
                 const unsigned char* at = raw + (walk.grp >> 2) * 16384 + row * 128;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    *reinterpret_cast<float4*>(&v[q][4 * h]) =
-                        *reinterpret_cast<const float4*>(at + ((((walk.grp & 3) * 2 + h) ^ (row & 7)) << 4));
+                const int late = walk.grp >> 2;
+                const float4 a = *reinterpret_cast<const float4*>(at + ((((walk.grp & 3) * 2 + late) ^ (row & 7)) << 4));
+                const float4 b = *reinterpret_cast<const float4*>(at + ((((walk.grp & 3) * 2 + 1 - late) ^ (row & 7)) << 4));
+                v[q][0] = late ? b.x : a.x; v[q][1] = late ? b.y : a.y; v[q][2] = late ? b.z : a.z; v[q][3] = late ? b.w : a.w;
+                v[q][4] = late ? a.x : b.x; v[q][5] = late ? a.y : b.y; v[q][6] = late ? a.z : b.z; v[q][7] = late ? a.w : b.w;
             } else {
                 const uint4 w = *reinterpret_cast<const uint4*>(raw + row * 128 + ((walk.grp ^ (row & 7)) << 4));
                 const uint32_t u[4] = {w.x, w.y, w.z, w.w};
