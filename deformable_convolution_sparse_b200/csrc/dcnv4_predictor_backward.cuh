@@ -106,34 +106,40 @@ pred_split_weight_kernel(const T* __restrict__ w, __nv_bfloat16* __restrict__ pl
 }
 
 // Columns of a row-major matrix (record slots of g, channels of y) are turned
-// into operand planes 64 at a time, 128 pixels each, by kConv threads in pieces
-// of eight columns: only the groups of eight below the last 16 valid columns
-// are touched (a chunk's other columns are never read, or only into sums that
-// nobody reads). A thread has two pieces at most, of one group and rows `rows`
-// apart. By TMA the values come through a ring of raw tiles (blocks of 128
-// bytes of columns x 128 rows, 128-byte swizzle, zeros past the matrix): reads
-// through L1 would have no room there, since the operand tiles take most of
-// an SM's memory, and so few of them in flight that DRAM idles (measured: 31 %
-// of its rate). Matrices whose rows TMA cannot take are read directly.
-constexpr int kConv = 512;
+// into operand planes 64 at a time, 128 pixels each. Two groups of kGroup
+// threads take the chunks in turn, so that one's waits fall into the other's
+// work, in pieces of eight columns: only the groups of eight columns below the
+// last 16 valid ones are touched (a chunk's other columns are never read, or
+// only into sums that nobody reads). A thread has at most four pieces, of the
+// same columns and rows `rows` apart. By TMA the values come through a ring of
+// raw tiles (blocks of 128 bytes of columns x 128 rows, 128-byte swizzle, zeros
+// past the matrix): reads through L1 would have no room there, since the
+// operand tiles take most of an SM's memory, and so few of them in flight that
+// DRAM idles (measured: 31 % of its rate). A raw tile is given back as soon as
+// its values are in registers, so that the ring is nearly always in flight;
+// landed() is what makes sure of that, since an arrival after the reads in
+// program order can overtake those still on their way (the next tile then
+// showed up in them). Matrices whose rows TMA cannot take are read directly.
+constexpr int kConv = 512, kGroup = 256, kPieces = 4;
 constexpr unsigned kRaw = 32768u;  // 128 rows x 64 fp32
 struct ChunkWalk {
-    int ng, row, grp, rows;  // groups of eight columns; this thread's first row, its group, rows per round
+    int ng, row, grp, rows;  // groups of eight columns; this thread's first row, its columns, rows per round
     __device__ __forceinline__ ChunkWalk(int columns, int tid) {
+        const int t = tid % kGroup;
         ng = min(8, (columns + 15) / 16 * 2);
-        rows = kConv / ng;
-        row = tid / ng;
-        grp = tid - row * ng;
+        rows = kGroup / ng;
+        row = t / ng;
+        grp = t - row * ng;
         if (row >= rows) row = 128;  // the threads left over
     }
 };
 template <typename T>
 struct Piece {
-    float v[2][8];
+    float v[kPieces][8];
     // from a raw tile: column c of row r is in block c / (128 / sizeof(T)), 16-byte chunk k at k ^ (r mod 8)
     __device__ __forceinline__ void from_raw(const unsigned char* raw, const ChunkWalk& walk) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < kPieces; ++q) {
             const int row = walk.row + q * walk.rows;
             if (row >= 128) {
 #pragma unroll
@@ -166,7 +172,7 @@ struct Piece {
     __device__ __forceinline__ void landed() const {
         uint32_t u = 0u;
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+        for (int q = 0; q < kPieces; ++q)
 #pragma unroll
             for (int k = 0; k < 8; ++k) u |= __float_as_uint(v[q][k]);
         if (__any_sync(0xffffffffu, u == 0x80000001u)) __nanosleep(1);
@@ -174,7 +180,7 @@ struct Piece {
     // from memory: rows m0.. of M, columns c0.. of C
     __device__ __forceinline__ void from_global(const T* __restrict__ x, const ChunkWalk& walk, long long m0, int M, int c0, int C) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < kPieces; ++q) {
             const int row = walk.row + q * walk.rows;
             const T* src = x + (m0 + row) * C + c0 + walk.grp * 8;
 #pragma unroll
@@ -185,7 +191,7 @@ struct Piece {
     template <int PLANES>
     __device__ __forceinline__ void store(unsigned char* tile, unsigned step, const ChunkWalk& walk) const {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < kPieces; ++q) {
             const int row = walk.row + q * walk.rows;
             if (row < 128) store_split8<PLANES>(tile, step, row, walk.grp, v[q]);
         }
@@ -235,13 +241,13 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
 
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&full_g[s], kConv / 32);
+            mbar_init(&full_g[s], kGroup / 32);
             mbar_init(&full_w[s], 1);
             mbar_init(&empty[s], 1);
             mbar_init(&acc_full[s], 1);
             mbar_init(&acc_empty[s], 128);
             mbar_init(&raw_full[s], 1);
-            mbar_init(&raw_empty[s], kConv / 32);
+            mbar_init(&raw_empty[s], kGroup / 32);
         }
         fence_barrier_init();
     }
@@ -262,17 +268,21 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     if (warp < 16) {
         const ChunkWalk whole(64, tid), tail(p.NO - (p.chunks - 1) * 64, tid);
         Piece<float> piece;
-        int chunk = 0;
-        long long n = 0;  // the item
-        for (long long it = 0; it < steps && ok; ++it) {
-            const int s = static_cast<int>(it & 1), r = static_cast<int>(it % S::kRaws);
+        const int s = warp >> 3;  // this group's operand stage, and the parity of its steps
+        int chunk = s;
+        long long n = 0;          // the item
+        for (long long it = s; it < steps && ok; it += 2, chunk += 2) {
+            while (chunk >= p.chunks) {
+                chunk -= p.chunks;
+                ++n;
+            }
             const ChunkWalk& walk = chunk + 1 < p.chunks ? whole : tail;
             if constexpr (RAW) {
-                ok = mbar_wait_bounded(&raw_full[r], static_cast<unsigned>(it / S::kRaws) & 1u, kCopyWaitLimitNs);
+                ok = mbar_wait_bounded(&raw_full[s], static_cast<unsigned>(it >> 1) & 1u, kCopyWaitLimitNs);
                 if (!ok) break;
-                piece.from_raw(raws + r * kRaw, walk);
+                piece.from_raw(raws + (it % S::kRaws) * kRaw, walk);
                 piece.landed();
-                if (lane == 0) mbar_arrive(&raw_empty[r]);
+                if (lane == 0) mbar_arrive(&raw_empty[s]);
             } else {
                 const long long item = blockIdx.x + n * gridDim.x;
                 piece.from_global(grec, walk, item / p.slices * 128, p.M, chunk * 64, p.NO);
@@ -281,10 +291,6 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             if (!ok) break;
             piece.template store<3>(sm + s * S::kStage, 16384u, walk);
             hand_over(&full_g[s], lane);
-            if (++chunk == p.chunks) {
-                chunk = 0;
-                ++n;
-            }
         }
     } else if (warp == 16) {
         if (lane == 0) {
@@ -297,16 +303,18 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             };
             auto load_raw = [&](long long it) {
                 if (!RAW || it >= steps) return;
-                const int r = static_cast<int>(it % S::kRaws);
-                if (it >= S::kRaws)
-                    ok = mbar_wait_bounded(&raw_empty[r], static_cast<unsigned>(it / S::kRaws - 1) & 1u, kCopyWaitLimitNs);
+                // the tile's place is free once step it - kRaws has given it back; each group has barriers of its own
+                const int r = static_cast<int>(it % S::kRaws), f = static_cast<int>(it & 1);
+                const long long before = it - S::kRaws;
+                if (before >= 0)
+                    ok = mbar_wait_bounded(&raw_empty[before & 1], static_cast<unsigned>(before >> 1) & 1u, kCopyWaitLimitNs);
                 if (!ok) return;
                 int m0, c0, s0;
                 where(it, m0, c0, s0);
                 const int halves = s0 + 32 < p.NO ? 2 : 1;
-                mbar_expect_tx(&raw_full[r], halves * 16384u);
-                for (int h = 0; h < halves; ++h) tc::tma_load_3d(raws + r * kRaw + h * 16384, &gmap, s0 + h * 32, m0, 0, &raw_full[r]);
-                mbar_arrive(&raw_full[r]);
+                mbar_expect_tx(&raw_full[f], halves * 16384u);
+                for (int h = 0; h < halves; ++h) tc::tma_load_3d(raws + r * kRaw + h * 16384, &gmap, s0 + h * 32, m0, 0, &raw_full[f]);
+                mbar_arrive(&raw_full[f]);
             };
             for (int k = 0; k < S::kRaws; ++k) load_raw(k);
             for (long long it = 0; it < steps && ok; ++it) {
@@ -476,12 +484,12 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
 
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&full_y[s], S::kDirectY ? 1 : kConv / 32 * ny);
+            mbar_init(&full_y[s], S::kDirectY ? 1 : kGroup / 32 * ny);
             mbar_init(&empty_y[s], 1);
-            mbar_init(&full_g[s], kConv / 32);
+            mbar_init(&full_g[s], kGroup / 32);
             mbar_init(&empty_g[s], 1);
             mbar_init(&raw_full[s], 1);
-            mbar_init(&raw_empty[s], kConv / 32);
+            mbar_init(&raw_empty[s], kGroup / 32);
         }
         mbar_init(acc_full, 1);
         fence_barrier_init();
@@ -500,15 +508,14 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
         float bs[2][8] = {};              // [chunk][slot of this thread's group]
         const ChunkWalk walk0(p.NO - g0, tid), walk1(nch == 2 ? p.NO - g0 - 64 : 64, tid);
         const ChunkWalk ywalk0(p.C - c0, tid), ywalk1(wide ? p.C - c0 - 64 : 64, tid);
-        int raw_n = 0;  // raw tiles so far
+        const int group = warp >> 3;
+        int k = 0;  // chunks (of y, then of g, tile by tile) so far; this group takes those of its parity
         auto take = [&](auto& piece, const ChunkWalk& walk) {
-            const int r = raw_n % max(1, S::kRaws);
-            ok = mbar_wait_bounded(&raw_full[r], static_cast<unsigned>(raw_n / max(1, S::kRaws)) & 1u, kCopyWaitLimitNs);
+            ok = mbar_wait_bounded(&raw_full[group], static_cast<unsigned>(k >> 1) & 1u, kCopyWaitLimitNs);
             if (!ok) return;
-            piece.from_raw(raws + r * kRaw, walk);
+            piece.from_raw(raws + k % max(1, S::kRaws) * kRaw, walk);
             piece.landed();
-            if (lane == 0) mbar_arrive(&raw_empty[r]);
-            ++raw_n;
+            if (lane == 0) mbar_arrive(&raw_empty[group]);
         };
         for (int i = 0; i < mine && ok; ++i) {
             if constexpr (!S::kDirectY) {
@@ -516,32 +523,38 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     if (b >= ny || !ok) break;
-                    const ChunkWalk& walk = b ? ywalk1 : ywalk0;
-                    Piece<T> piece;
-                    if constexpr (RAW) take(piece, walk);
-                    else piece.from_global(y, walk, pixel(i), p.M, c0 + b * 64, p.C);
-                    if (b == 0 && yn > 0)
-                        ok = ok && mbar_wait_bounded(&empty_y[ys], static_cast<unsigned>(yn - 1) & 1u, kCopyWaitLimitNs);
-                    if (!ok) break;
-                    piece.template store<YP>(sm + ys * S::kY + b * 16384, 32768u, walk);
-                    hand_over(&full_y[ys], lane);
+                    if ((k & 1) == group) {
+                        const ChunkWalk& walk = b ? ywalk1 : ywalk0;
+                        Piece<T> piece;
+                        if constexpr (RAW) take(piece, walk);
+                        else piece.from_global(y, walk, pixel(i), p.M, c0 + b * 64, p.C);
+                        if (yn > 0) ok = ok && mbar_wait_bounded(&empty_y[ys], static_cast<unsigned>(yn - 1) & 1u, kCopyWaitLimitNs);
+                        if (!ok) break;
+                        piece.template store<YP>(sm + ys * S::kY + b * 16384, 32768u, walk);
+                        hand_over(&full_y[ys], lane);
+                    }
+                    ++k;
                 }
             }
 #pragma unroll
             for (int ch = 0; ch < 2; ++ch) {
                 if (ch >= nch || !ok) break;
-                const ChunkWalk& walk = ch ? walk1 : walk0;
-                const int n = i * nch + ch, s = n & 1;
-                Piece<float> piece;
-                if constexpr (RAW) take(piece, walk);
-                else piece.from_global(grec, walk, pixel(i), p.M, g0 + ch * 64, p.NO);
-                if (n >= 2) ok = ok && mbar_wait_bounded(&empty_g[s], static_cast<unsigned>((n >> 1) - 1) & 1u, kCopyWaitLimitNs);
-                if (!ok) break;
-                piece.template store<3>(gsm + s * S::kG, 16384u, walk);
-                hand_over(&full_g[s], lane);
-                if (sums)
+                if ((k & 1) == group) {
+                    const ChunkWalk& walk = ch ? walk1 : walk0;
+                    const int n = i * nch + ch, s = n & 1;
+                    Piece<float> piece;
+                    if constexpr (RAW) take(piece, walk);
+                    else piece.from_global(grec, walk, pixel(i), p.M, g0 + ch * 64, p.NO);
+                    if (n >= 2) ok = ok && mbar_wait_bounded(&empty_g[s], static_cast<unsigned>((n >> 1) - 1) & 1u, kCopyWaitLimitNs);
+                    if (!ok) break;
+                    piece.template store<3>(gsm + s * S::kG, 16384u, walk);
+                    hand_over(&full_g[s], lane);
+                    if (sums)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) bs[ch][k] += piece.v[0][k] + piece.v[1][k];  // rows past the tile: zeros
+                        for (int e = 0; e < 8; ++e)  // rows past the tile hold zeros
+                            bs[ch][e] += (piece.v[0][e] + piece.v[1][e]) + (piece.v[2][e] + piece.v[3][e]);
+                }
+                ++k;
             }
         }
         if (sums) {
@@ -562,11 +575,14 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
 #pragma unroll
                     for (int k = 0; k < 8; ++k) red[tid * 8 + k] = bs[ch][k];
                 tc::bar_sync(2, kConv);
-                // eight threads per slot, every eighth of the slot's threads each, then the eight
+                // eight threads per slot, every eighth of the slot's threads of both groups each, then the eight
                 const int s = tid >> 3, part8 = tid & 7;
                 float v = 0.f;
                 if (s < ng * 8)
-                    for (int r = part8; r < rows; r += 8) v += red[(r * ng + (s >> 3)) * 8 + (s & 7)];
+                    for (int r = part8; r < rows; r += 8) {
+                        const float* at = red + (r * ng + (s >> 3)) * 8 + (s & 7);
+                        v += at[0] + at[kGroup * 8];
+                    }
                 v += __shfl_xor_sync(0xffffffffu, v, 1);
                 v += __shfl_xor_sync(0xffffffffu, v, 2);
                 v += __shfl_xor_sync(0xffffffffu, v, 4);
@@ -583,14 +599,14 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
         const bool on = c < p.C && (wide || row < 64);
         int raw_n = 0;
         auto load_raw = [&](const CUtensorMap* map, int col, int step, int blocks, long long m0) {
-            const int r = raw_n % max(1, S::kRaws);
-            if (raw_n >= S::kRaws)
-                ok = mbar_wait_bounded(&raw_empty[r], static_cast<unsigned>(raw_n / max(1, S::kRaws) - 1) & 1u, kCopyWaitLimitNs);
+            const int r = raw_n % max(1, S::kRaws), f = raw_n & 1, before = raw_n - S::kRaws;
+            if (before >= 0)
+                ok = mbar_wait_bounded(&raw_empty[before & 1], static_cast<unsigned>(before >> 1) & 1u, kCopyWaitLimitNs);
             if (!ok) return;
-            mbar_expect_tx(&raw_full[r], blocks * 16384u);
+            mbar_expect_tx(&raw_full[f], blocks * 16384u);
             for (int b = 0; b < blocks; ++b)
-                tc::tma_load_3d(raws + r * kRaw + b * 16384, map, col + b * step, static_cast<int>(m0), 0, &raw_full[r]);
-            mbar_arrive(&raw_full[r]);
+                tc::tma_load_3d(raws + r * kRaw + b * 16384, map, col + b * step, static_cast<int>(m0), 0, &raw_full[f]);
+            mbar_arrive(&raw_full[f]);
             ++raw_n;
         };
         for (int f = 0; f * kFlushTiles < mine; ++f) {
@@ -669,12 +685,15 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
                 }
                 const int s = g0 + q * 16;
                 float* o = part + (static_cast<size_t>(walker) * p.NO + s) * p.C + c;
+                if (f > 0) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = on && s + e < p.NO ? o[static_cast<size_t>(e) * p.C] : 0.f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] += w[e];
+                }
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    if (on && s + e < p.NO) {
-                        float* at = o + static_cast<size_t>(e) * p.C;
-                        *at = f == 0 ? v[e] : *at + v[e];
-                    }
+                    if (on && s + e < p.NO) o[static_cast<size_t>(e) * p.C] = v[e];
             }
             tc::fence_before();
             tc::bar_sync(1, 128);
