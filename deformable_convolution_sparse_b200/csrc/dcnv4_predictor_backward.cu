@@ -81,10 +81,15 @@ int launch_grad_y(const CUtensorMap& wmap, const CUtensorMap& gmap, const CUtens
 template <typename T, bool RAW>
 int launch_grad_w(const CUtensorMap& gmap, const CUtensorMap& ymap, const float* grec, const T* y, float* part,
                   float* pbias, dcnv4::PredBwdParams p, cudaStream_t s) {
-    constexpr unsigned smem = dcnv4::GradWShape<T, RAW>::kSmem;
-    static_assert(smem <= kTileSmemLimit, "the stages do not fit");
+    using S = dcnv4::GradWShape<T, RAW>;
+    static_assert(S::smem(16384u) <= kTileSmemLimit && S::smem(32768u) <= kTileSmemLimit, "the stages do not fit");
+    p.ystep = p.C > 64 ? 32768u : 16384u;
+    p.raws = S::raws(p.ystep);
+    const unsigned smem = S::smem(p.ystep);
     auto kern = dcnv4::pred_grad_w_kernel<T, RAW>;
-    if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess) return DCNV4_ERR_LAUNCH;
+    if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(std::max(S::smem(16384u), S::smem(32768u)))) !=
+        cudaSuccess)
+        return DCNV4_ERR_LAUNCH;
     p.slices = (p.C + 127) / 128;
     return launch_chained(kern, dim3(static_cast<unsigned>(p.walkers) * p.slices * p.groups), dcnv4::kGradWThreads, smem, s,
                           gmap, ymap, grec, y, part, pbias, p);

@@ -37,6 +37,8 @@ struct PredBwdParams {
     int groups;          // groups of 128 slots (grad_weight)
     int walkers;         // CTAs that share the pixel tiles of a (slice, group), each with partial sums of its own
     int tma_out;         // grad_y by TMA
+    int raws;            // grad_weight: raw tiles (0: direct reads)
+    unsigned ystep;      // grad_weight: bytes between y's planes, 16 KB per block of 64 channels of a slice
     unsigned* status;
 };
 
@@ -209,15 +211,18 @@ __device__ __forceinline__ void hand_over(uint64_t* bar, int lane) {
 // tiles and the same slots' rows of W's planes by TMA, these as the right
 // operand (their rows run along the channels: MN-major); warp 17 issues the
 // products; warps 18..21 read the accumulators (two sets, in turn) and write
-// the tile through shared memory and TMA, 64 channels at a time.
+// the tile through shared memory and TMA, 32 channels at a time.
 template <int CT, int WP>
 struct GradYShape {
     static constexpr int kStages = 2;
     static constexpr int kHigh = CT == 64 ? 3 : 1;  // accumulators of order 0
     static constexpr unsigned kWBytes = WP * (CT / 64) * 8192u;
     static constexpr unsigned kStage = 3u * 16384u + kWBytes;
-    static constexpr unsigned kOut = 32768u;
-    static constexpr int kRaws = kStages * kStage + kOut + 2 * kRaw <= 224u * 1024u ? 2 : 1;  // raw tiles
+    static constexpr unsigned kOut = 16384u;
+    // raw tiles: as many as fit, up to three (each takes about 2 us to come from a busy DRAM)
+    static constexpr int kRaws = kStages * kStage + kOut + 3 * kRaw <= 224u * 1024u   ? 3
+                                 : kStages * kStage + kOut + 2 * kRaw <= 224u * 1024u ? 2
+                                                                                      : 1;
     static constexpr unsigned kSmem = 1024u + kStages * kStage + kOut + kRaws * kRaw + 256u;
     static constexpr unsigned kAcc = (kHigh + 1) * CT;  // columns of one set
 };
@@ -235,8 +240,8 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     unsigned char* raws = outs + S::kOut;
     uint64_t* bars = reinterpret_cast<uint64_t*>(raws + S::kRaws * kRaw);
     uint64_t *full_g = bars, *full_w = bars + 2, *empty = bars + 4, *acc_full = bars + 6, *acc_empty = bars + 8,
-             *raw_full = bars + 10, *raw_empty = bars + 12;
-    uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 14);
+             *raw_full = bars + 10, *raw_empty = bars + 14;  // of step it: the (it mod 4)-th
+    uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 18);
     const int tid = threadIdx.x, warp = static_cast<int>(tc::uniform(threadIdx.x >> 5)), lane = tid & 31;
 
     if (tid == 0) {
@@ -246,6 +251,8 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             mbar_init(&empty[s], 1);
             mbar_init(&acc_full[s], 1);
             mbar_init(&acc_empty[s], 128);
+        }
+        for (int s = 0; s < 4; ++s) {
             mbar_init(&raw_full[s], 1);
             mbar_init(&raw_empty[s], kGroup / 32);
         }
@@ -278,11 +285,11 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             }
             const ChunkWalk& walk = chunk + 1 < p.chunks ? whole : tail;
             if constexpr (RAW) {
-                ok = mbar_wait_bounded(&raw_full[s], static_cast<unsigned>(it >> 1) & 1u, kCopyWaitLimitNs);
+                ok = mbar_wait_bounded(&raw_full[it & 3], static_cast<unsigned>(it >> 2) & 1u, kCopyWaitLimitNs);
                 if (!ok) break;
                 piece.from_raw(raws + (it % S::kRaws) * kRaw, walk);
                 piece.landed();
-                if (lane == 0) mbar_arrive(&raw_empty[s]);
+                if (lane == 0) mbar_arrive(&raw_empty[it & 3]);
             } else {
                 const long long item = blockIdx.x + n * gridDim.x;
                 piece.from_global(grec, walk, item / p.slices * 128, p.M, chunk * 64, p.NO);
@@ -303,11 +310,12 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             };
             auto load_raw = [&](long long it) {
                 if (!RAW || it >= steps) return;
-                // the tile's place is free once step it - kRaws has given it back; each group has barriers of its own
-                const int r = static_cast<int>(it % S::kRaws), f = static_cast<int>(it & 1);
+                // the tile's place is free once step it - kRaws has given it back. A group waits for every fourth
+                // step's barrier after its own use of it four steps before, whatever the ring's length.
+                const int r = static_cast<int>(it % S::kRaws), f = static_cast<int>(it & 3);
                 const long long before = it - S::kRaws;
                 if (before >= 0)
-                    ok = mbar_wait_bounded(&raw_empty[before & 1], static_cast<unsigned>(before >> 1) & 1u, kCopyWaitLimitNs);
+                    ok = mbar_wait_bounded(&raw_empty[before & 3], static_cast<unsigned>(before >> 2) & 1u, kCopyWaitLimitNs);
                 if (!ok) return;
                 int m0, c0, s0;
                 where(it, m0, c0, s0);
@@ -384,42 +392,39 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             if (!ok) break;
             tc::fence_after();
             const uint32_t acc = tmem + b * S::kAcc + (static_cast<uint32_t>(quarter * 32) << 16);
-            for (int h = 0; h < CT / 64; ++h) {
-                if (h > 0 && c0 + h * 64 >= p.C) continue;
-                // the stores that read the staging tile have done so
+            for (int h = 0; h < CT / 32; ++h) {
+                const int ch = c0 + h * 32;
+                if (ch >= p.C) break;
+                // the store that read the staging tile has done so
                 if (et == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 tc::bar_sync(1, 128);
-                for (int cc = 0; cc < 4; ++cc) {
+                for (int cc = 0; cc < 2; ++cc) {
                     float v[16], w[16];
-                    tc::ld16(acc + S::kHigh * CT + h * 64 + cc * 16, v);
+                    tc::ld16(acc + S::kHigh * CT + h * 32 + cc * 16, v);
                     for (int q = 0; q < high; ++q) {
-                        tc::ld16(acc + q * CT + h * 64 + cc * 16, w);
+                        tc::ld16(acc + q * CT + h * 32 + cc * 16, w);
                         tc::wait_ld();
 #pragma unroll
                         for (int e = 0; e < 16; ++e) v[e] += w[e];
                     }
-                    // 32 channels (128 bytes) per block of the staging tile
-                    unsigned char* o = outs + (cc >> 1) * 16384 + row * 128;
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        *reinterpret_cast<float4*>(o + ((((cc & 1) * 4 + q) ^ (row & 7)) << 4)) =
+                        *reinterpret_cast<float4*>(outs + row * 128 + (((cc * 4 + q) ^ (row & 7)) << 4)) =
                             make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
                 }
                 if (p.tma_out) fence_proxy_async();
                 tc::bar_sync(1, 128);
                 if (p.tma_out) {
                     if (et == 0) {
-                        for (int q = 0; q < 2; ++q)
-                            if (c0 + h * 64 + q * 32 < p.C)
-                                tc::tma_store_3d(&omap, c0 + h * 64 + q * 32, static_cast<int>(m0), 0, outs + q * 16384);
+                        tc::tma_store_3d(&omap, ch, static_cast<int>(m0), 0, outs);
                         tc::bulk_commit();
                     }
                 } else {
-                    const int rows = static_cast<int>(min(128LL, p.M - m0)), cols = min(64, p.C - c0 - h * 64);
-                    for (int r = quarter; r < rows; r += 4)
-                        for (int c = lane; c < cols; c += 32)
-                            gy[(m0 + r) * p.C + c0 + h * 64 + c] = *reinterpret_cast<const float*>(
-                                outs + (c >> 5) * 16384 + r * 128 + ((((c & 31) >> 2) ^ (r & 7)) << 4) + (c & 3) * 4);
+                    const int rows = static_cast<int>(min(128LL, p.M - m0));
+                    if (ch + lane < p.C)
+                        for (int r = quarter; r < rows; r += 4)
+                            gy[(m0 + r) * p.C + ch + lane] = *reinterpret_cast<const float*>(
+                                outs + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
                 }
             }
             tc::fence_before();
@@ -448,10 +453,13 @@ struct GradWShape {
     static constexpr int YP = split_planes<T>();
     static constexpr bool kDirectY = RAW && YP == 1;  // y's plane by TMA
     static constexpr int kYStages = YP == 1 ? 2 : 1;
-    static constexpr unsigned kY = YP * 32768u;
     static constexpr unsigned kG = 3u * 16384u;
-    static constexpr int kRaws = !RAW ? 0 : YP == 3 ? 1 : 2;
-    static constexpr unsigned kSmem = 1024u + kYStages * kY + 2u * kG + kRaws * kRaw + 256u;
+    static constexpr unsigned fixed(unsigned ystep) { return kYStages * YP * ystep + 2u * kG; }
+    // as many raw tiles as fit, up to three
+    static constexpr int raws(unsigned ystep) {
+        return !RAW ? 0 : fixed(ystep) + 3 * kRaw <= 224u * 1024u ? 3 : fixed(ystep) + 2 * kRaw <= 224u * 1024u ? 2 : 1;
+    }
+    static constexpr unsigned smem(unsigned ystep) { return 1024u + fixed(ystep) + raws(ystep) * kRaw + 256u; }
 };
 constexpr int kGradWThreads = kConv + 128;
 
@@ -464,12 +472,13 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
     constexpr int YP = S::YP;
     extern __shared__ unsigned char pb_smem_raw[];
     unsigned char* sm = pb_smem_raw + ((1024u - (smem_addr(pb_smem_raw) & 1023u)) & 1023u);
-    unsigned char* gsm = sm + S::kYStages * S::kY;
+    const unsigned ystage = YP * p.ystep;
+    unsigned char* gsm = sm + S::kYStages * ystage;
     unsigned char* raws = gsm + 2 * S::kG;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(raws + S::kRaws * kRaw);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(raws + p.raws * kRaw);
     uint64_t *full_y = bars, *empty_y = bars + 2, *full_g = bars + 4, *empty_g = bars + 6, *acc_full = bars + 8,
-             *raw_full = bars + 9, *raw_empty = bars + 11;
-    uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 13);
+             *raw_full = bars + 9, *raw_empty = bars + 13;  // of raw tile k: the (k mod 4)-th
+    uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 17);
     const int tid = threadIdx.x, warp = static_cast<int>(tc::uniform(threadIdx.x >> 5)), lane = tid & 31;
 
     // CTA -> walker, (slice, group); the slices and groups of one walker side by side
@@ -488,6 +497,8 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
             mbar_init(&empty_y[s], 1);
             mbar_init(&full_g[s], kGroup / 32);
             mbar_init(&empty_g[s], 1);
+        }
+        for (int s = 0; s < 4; ++s) {
             mbar_init(&raw_full[s], 1);
             mbar_init(&raw_empty[s], kGroup / 32);
         }
@@ -509,13 +520,20 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
         const ChunkWalk walk0(p.NO - g0, tid), walk1(nch == 2 ? p.NO - g0 - 64 : 64, tid);
         const ChunkWalk ywalk0(p.C - c0, tid), ywalk1(wide ? p.C - c0 - 64 : 64, tid);
         const int group = warp >> 3;
-        int k = 0;  // chunks (of y, then of g, tile by tile) so far; this group takes those of its parity
+        // chunks (of y, then of g, tile by tile) so far, and their place in the ring; this group takes those of its
+        // parity
+        int k = 0;
+        unsigned char* place = raws;
+        auto next = [&] {
+            ++k;
+            place = place == raws + (p.raws - 1) * kRaw ? raws : place + kRaw;
+        };
         auto take = [&](auto& piece, const ChunkWalk& walk) {
-            ok = mbar_wait_bounded(&raw_full[group], static_cast<unsigned>(k >> 1) & 1u, kCopyWaitLimitNs);
+            ok = mbar_wait_bounded(&raw_full[k & 3], static_cast<unsigned>(k >> 2) & 1u, kCopyWaitLimitNs);
             if (!ok) return;
-            piece.from_raw(raws + k % max(1, S::kRaws) * kRaw, walk);
+            piece.from_raw(place, walk);
             piece.landed();
-            if (lane == 0) mbar_arrive(&raw_empty[group]);
+            if (lane == 0) mbar_arrive(&raw_empty[k & 3]);
         };
         for (int i = 0; i < mine && ok; ++i) {
             if constexpr (!S::kDirectY) {
@@ -530,10 +548,10 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
                         else piece.from_global(y, walk, pixel(i), p.M, c0 + b * 64, p.C);
                         if (yn > 0) ok = ok && mbar_wait_bounded(&empty_y[ys], static_cast<unsigned>(yn - 1) & 1u, kCopyWaitLimitNs);
                         if (!ok) break;
-                        piece.template store<YP>(sm + ys * S::kY + b * 16384, 32768u, walk);
+                        piece.template store<YP>(sm + ys * ystage + b * 16384, p.ystep, walk);
                         hand_over(&full_y[ys], lane);
                     }
-                    ++k;
+                    next();
                 }
             }
 #pragma unroll
@@ -554,7 +572,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
                         for (int e = 0; e < 8; ++e)  // rows past the tile hold zeros
                             bs[ch][e] += (piece.v[0][e] + piece.v[1][e]) + (piece.v[2][e] + piece.v[3][e]);
                 }
-                ++k;
+                next();
             }
         }
         if (sums) {
@@ -597,17 +615,18 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
         const unsigned second = wide ? 16384u : 0u;
         const int quarter = warp & 3, row = quarter * 32 + lane, c = c0 + row;
         const bool on = c < p.C && (wide || row < 64);
-        int raw_n = 0;
+        int raw_n = 0, r = 0;
         auto load_raw = [&](const CUtensorMap* map, int col, int step, int blocks, long long m0) {
-            const int r = raw_n % max(1, S::kRaws), f = raw_n & 1, before = raw_n - S::kRaws;
+            const int f = raw_n & 3, before = raw_n - p.raws;
             if (before >= 0)
-                ok = mbar_wait_bounded(&raw_empty[before & 1], static_cast<unsigned>(before >> 1) & 1u, kCopyWaitLimitNs);
+                ok = mbar_wait_bounded(&raw_empty[before & 3], static_cast<unsigned>(before >> 2) & 1u, kCopyWaitLimitNs);
             if (!ok) return;
             mbar_expect_tx(&raw_full[f], blocks * 16384u);
             for (int b = 0; b < blocks; ++b)
                 tc::tma_load_3d(raws + r * kRaw + b * 16384, map, col + b * step, static_cast<int>(m0), 0, &raw_full[f]);
             mbar_arrive(&raw_full[f]);
             ++raw_n;
+            r = r + 1 == p.raws ? 0 : r + 1;
         };
         for (int f = 0; f * kFlushTiles < mine; ++f) {
             const int begin = f * kFlushTiles, end = min(mine, begin + kFlushTiles);
@@ -620,7 +639,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
                         if (!ok) break;
                         mbar_expect_tx(&full_y[ys], ny * 16384u);
                         for (int b = 0; b < ny; ++b)
-                            tc::tma_load_3d(sm + ys * S::kY + b * 16384, &ymap, c0 + b * 64, static_cast<int>(m0), 0, &full_y[ys]);
+                            tc::tma_load_3d(sm + ys * ystage + b * 16384, &ymap, c0 + b * 64, static_cast<int>(m0), 0, &full_y[ys]);
                         mbar_arrive(&full_y[ys]);
                     } else {
                         for (int b = 0; b < ny && ok; ++b) {
@@ -645,7 +664,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
                         ok = tc::warp_wait(&full_g[s], static_cast<unsigned>(n >> 1) & 1u, kCopyWaitLimitNs);
                         if (!ok) break;
                         tc::fence_after();
-                        const uint32_t a = tc::sw128(smem_addr(sm + ys * S::kY), second), b = tc::sw128(smem_addr(gsm + s * S::kG));
+                        const uint32_t a = tc::sw128(smem_addr(sm + ys * ystage), second), b = tc::sw128(smem_addr(gsm + s * S::kG));
                         const uint32_t acc = tmem + ch * 64;
                         uint32_t high = acc;
 #pragma unroll 1
@@ -655,7 +674,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
 #pragma unroll
                                 for (int j = 0; j < YP; ++j) {
                                     if (gi + j > 2) continue;
-                                    const uint32_t ad = a + j * 2048 + k * 128, bd = b + gi * 1024 + k * 128;
+                                    const uint32_t ad = a + j * (p.ystep / 16) + k * 128, bd = b + gi * 1024 + k * 128;
                                     const bool first_low = gi == (YP > 1 ? 0 : 1) && j == (YP > 1 ? 1 : 0);
                                     if (gi + j == 0) tc::mma_f16(high, ad, bd, idesc, t > 0 || k >= 3, lead);
                                     else tc::mma_f16(acc + 384, ad, bd, idesc, t > 0 || k > 0 || !first_low, lead);
