@@ -388,7 +388,7 @@ def _output(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype,
     """``t`` checked against shape, dtype and device, or a new tensor of them."""
     if t is None:
         return torch.empty(*shape, dtype=dtype, device=device)
-    if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device \
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype or t.device != device \
             or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
@@ -461,10 +461,10 @@ MX_BLOCK = 32  # channels that share a scale
 
 def _check_mx(codes: torch.Tensor, scales: torch.Tensor, lead: tuple, C: int, names=("codes", "scales")):
     nb = (C + MX_BLOCK - 1) // MX_BLOCK
-    for t, name, shape in ((codes, names[0], lead + (nb * 16,)), (scales, names[1], lead + (nb,))):
+    for t, name, shape in ((codes, names[0], (*lead, nb * 16)), (scales, names[1], (*lead, nb))):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if t.device.type != "cuda" or t.dtype != torch.uint8 or not t.is_contiguous() or tuple(t.shape) != shape:
+        if t.shape != shape or t.dtype is not torch.uint8 or not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor of shape {shape}")
     if codes.device != scales.device:
         raise ValueError(f"{names[0]} and {names[1]} must be on one device")
@@ -532,7 +532,7 @@ def predictor_mx(y: torch.Tensor, weight_codes: torch.Tensor, weight_scales: tor
     bp = 0
     if bias is not None:
         _check_tensor(bias, "bias")
-        if bias.dtype != torch.float32 or tuple(bias.shape) != (NO,) or bias.device != y.device:
+        if bias.dtype != torch.float32 or bias.shape != (NO,) or bias.device != y.device:
             raise ValueError(f"bias must be fp32 [{NO}] on y's device")
         bp = bias.data_ptr()
     with _launching_on(y.device, stream):
