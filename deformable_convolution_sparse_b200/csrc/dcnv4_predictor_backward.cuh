@@ -510,7 +510,9 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
     __syncthreads();  // every CTA holds its tensor memory before the next launch may start
     tc::fence_after();
     const uint32_t tmem = tc::uniform(*slot);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // No wait for the launch before, which is grad_y's: this kernel reads nothing of it, and it starts once all of
+    // that one's CTAs have let it, after their own wait, so that everything before them is complete. It does wait at
+    // its end, so that whatever waits for this kernel has grad_y as well.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     bool ok = true;
 
@@ -723,6 +725,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
     __syncthreads();
     tc::fence_after();
     if (warp == 16) tc::dealloc(tmem, 512u);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // The walkers' partial sums added in a fixed order (sixteen strided runs of

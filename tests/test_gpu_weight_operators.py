@@ -515,6 +515,38 @@ def test_on_another_stream_and_two_at_once(cuda_device):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("M", [130, 20000])
+def test_gradients_are_complete_for_the_next_launch(M, cuda_device):
+    """The next kernel on the stream reads every gradient at once, eagerly and in a graph: kernels that start
+    before the one in front of them has finished must still leave everything complete."""
+    g = torch.Generator(device=cuda_device).manual_seed(M)
+    y = torch.randn(M, 128, generator=g, device=cuda_device).bfloat16()
+    w = torch.randn(216, 128, generator=g, device=cuda_device).bfloat16()
+    gr = torch.randn(M, 8, 27, generator=g, device=cuda_device)
+    outs = [torch.empty(M, 128, device=cuda_device), torch.empty(216, 128, device=cuda_device),
+            torch.empty(216, device=cuda_device)]
+
+    def run():
+        for t in outs:
+            t.fill_(float("nan"))
+        dcn.predictor_backward(y, w, gr, G=8, K=3, grad_y=outs[0], grad_weight=outs[1], grad_bias=outs[2])
+        return [dcn.mx_quantize(t) for t in outs]
+
+    first = run()
+    torch.cuda.synchronize()
+    want = [dcn.mx_quantize(t) for t in outs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = run()
+    for _ in range(20):
+        for got in (run(), captured):
+            graph.replay()
+            for a, b in zip(got, want):
+                assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    for a, b in zip(first, want):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_stream_argument(cuda_device):
     x = torch.randn(2, 80, 50, device=cuda_device)
     want = dcn.orthogonalize(x)
