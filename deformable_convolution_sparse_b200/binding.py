@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -209,8 +210,10 @@ def validate(x_ptr: int, om_ptr: int, out_ptr: int, N: int, H: int, W: int, C: i
 
 def _stream_handle(stream) -> int:
     if stream is None:
-        # the current stream of the current device, without making a Stream object of it
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        if torch.cuda.is_initialized():
+            # the current stream of the current device, without making a Stream object of it
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        stream = torch.cuda.current_stream()
     return int(stream.cuda_stream)
 
 
@@ -414,6 +417,16 @@ def _pixels(lead) -> int:
     return m
 
 
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(entry: str, *args: int) -> int:
+    """Bytes that ``entry`` (a _workspace function of the library) asks for: a function of its arguments alone."""
+    size = ctypes.c_size_t(0)
+    rc = getattr(load_library(), entry)(*args, ctypes.byref(size))
+    if rc != DCNV4_OK:
+        raise DCNv4Error(rc, entry)
+    return size.value
+
+
 def predictor_backward(y: torch.Tensor, weight: torch.Tensor, grad_offset_mask: torch.Tensor, G: int, K: int,
                        remove_center: bool = False, with_bias: bool = True, grad_y: torch.Tensor | None = None,
                        grad_weight: torch.Tensor | None = None, grad_bias: torch.Tensor | None = None, stream=None):
@@ -427,6 +440,8 @@ def predictor_backward(y: torch.Tensor, weight: torch.Tensor, grad_offset_mask: 
     """
     for t, name in ((y, "y"), (weight, "weight"), (grad_offset_mask, "grad_offset_mask")):
         _check_tensor(t, name)
+    if y.dim() < 1:
+        raise ValueError("y must be [..., C]")
     P = K * K - (1 if remove_center else 0)
     C, lead, NO = y.shape[-1], tuple(y.shape[:-1]), 3 * G * P
     if weight.dtype != y.dtype or weight.device != y.device or tuple(weight.shape) != (NO, C):
@@ -437,20 +452,16 @@ def predictor_backward(y: torch.Tensor, weight: torch.Tensor, grad_offset_mask: 
     if not with_bias and grad_bias is not None:
         raise ValueError("grad_bias is given but with_bias is False")
     M, flags, dt = _pixels(lead), FLAG_REMOVE_CENTER if remove_center else 0, TORCH_DTYPE[y.dtype]
-    lib = load_library()
-    size = ctypes.c_size_t(0)
-    rc = lib.dcnv4_predictor_backward_workspace(M, C, G, K, flags, dt, ctypes.byref(size))
-    if rc != DCNV4_OK:
-        raise DCNv4Error(rc, "dcnv4_predictor_backward_workspace")
+    size = _workspace_bytes("dcnv4_predictor_backward_workspace", M, C, G, K, flags, dt)
     f32, dev = torch.float32, y.device
     with _launching_on(dev, stream):
         gy = _output(grad_y, "grad_y", tuple(y.shape), f32, dev)
         gw = _output(grad_weight, "grad_weight", (NO, C), f32, dev)
         gb = _output(grad_bias, "grad_bias", (NO,), f32, dev) if with_bias else None
-        ws = torch.empty(size.value, dtype=torch.uint8, device=dev)
-        rc = lib.dcnv4_predictor_backward(y.data_ptr(), weight.data_ptr(), grad_offset_mask.data_ptr(),
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        rc = load_library().dcnv4_predictor_backward(y.data_ptr(), weight.data_ptr(), grad_offset_mask.data_ptr(),
                                           gy.data_ptr(), gw.data_ptr(), 0 if gb is None else gb.data_ptr(),
-                                          ws.data_ptr(), size.value, M, C, G, K, flags, dt, _stream_handle(stream))
+                                          ws.data_ptr(), size, M, C, G, K, flags, dt, _stream_handle(stream))
     if rc != DCNV4_OK:
         raise DCNv4Error(rc, "dcnv4_predictor_backward")
     return gy, gw, gb
@@ -524,6 +535,8 @@ def predictor_mx(y: torch.Tensor, weight_codes: torch.Tensor, weight_scales: tor
     [3*G*P] or None. Returns offset_mask [..., G, 3*P] in y's dtype.
     """
     _check_tensor(y, "y")
+    if y.dim() < 1:
+        raise ValueError("y must be [..., C]")
     P = K * K - (1 if remove_center else 0)
     C, lead, NO = y.shape[-1], tuple(y.shape[:-1]), 3 * G * P
     _check_mx(weight_codes, weight_scales, (NO,), C, ("weight_codes", "weight_scales"))
@@ -564,15 +577,11 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients: tuple = (3.4445
     a, b, c = (float(v) for v in coefficients)
     R, C = x.shape[-2:]
     B, dt = _pixels(x.shape[:-2]), TORCH_DTYPE[x.dtype]
-    lib = load_library()
-    size = ctypes.c_size_t(0)
-    rc = lib.dcnv4_orthogonalize_workspace(B, R, C, dt, ctypes.byref(size))
-    if rc != DCNV4_OK:
-        raise DCNv4Error(rc, "dcnv4_orthogonalize_workspace")
+    size = _workspace_bytes("dcnv4_orthogonalize_workspace", B, R, C, dt)
     with _launching_on(x.device, stream):
         out = _output(out, "out", tuple(x.shape), x.dtype, x.device)
-        ws = torch.empty(size.value, dtype=torch.uint8, device=x.device)
-        rc = lib.dcnv4_orthogonalize(x.data_ptr(), out.data_ptr(), ws.data_ptr(), size.value, B, R, C, int(steps),
+        ws = torch.empty(size, dtype=torch.uint8, device=x.device)
+        rc = load_library().dcnv4_orthogonalize(x.data_ptr(), out.data_ptr(), ws.data_ptr(), size, B, R, C, int(steps),
                                      a, b, c, float(eps), dt, _stream_handle(stream))
     if rc != DCNV4_OK:
         raise DCNv4Error(rc, "dcnv4_orthogonalize")

@@ -19,12 +19,12 @@
 
 #include "dcnv4_async.cuh"
 #include "dcnv4_kernels.cuh"
+#include "dcnv4_records.cuh"
 #include "dcnv4_tcgen05.cuh"
 
 namespace dcnv4 {
 
-constexpr int kMxBlock = 32;       // channels that share a scale
-constexpr int kMxBlockBytes = 16;  // their codes
+constexpr int kMxBlock = 32;  // channels that share a scale (16 bytes of codes)
 
 // Eight fp32 values as e2m1 codes, value 2i in the low half of byte i.
 __device__ __forceinline__ uint32_t e2m1_pack8(const float* q) {
@@ -209,18 +209,6 @@ mx_dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restri
                 if (c0 + i < C) o[i] = mx_from_float<T>(v[i]);
         }
     }
-}
-
-// Slot of projection channel o in its record (offsets (g, comp, j) -> g*3P +
-// comp*P + j, masks (g, j) -> g*3P + 2P + j) and the channel of a slot.
-__host__ __device__ __forceinline__ int record_slot(int o, int G, int P) {
-    if (o < 2 * G * P) return (o / (2 * P)) * 3 * P + o % (2 * P);
-    const int q = o - 2 * G * P;
-    return (q / P) * 3 * P + 2 * P + q % P;
-}
-__host__ __device__ __forceinline__ int slot_channel(int s, int G, int P) {
-    const int g = s / (3 * P), r = s - g * 3 * P;
-    return r < 2 * P ? g * 2 * P + r : 2 * G * P + g * P + (r - 2 * P);
 }
 
 struct MxProjParams {
@@ -450,7 +438,8 @@ predictor_mx_kernel(const __grid_constant__ CUtensorMap rmap, const T* __restric
                              tmem + p.sfa_col + (k >> 1) * 4, tmem + p.sfb_col + (k >> 1) * 4 * p.groups, k > 0, lead);
             if (lead) tc::commit(done);
         }
-        ok = __syncthreads_and(mbar_wait_bounded(done, static_cast<unsigned>(it) & 1u, kCopyWaitLimitNs)) != 0;
+        // one warp polls; the others wait at the barrier, where they take no issue slots
+        ok = __syncthreads_and(warp != 0 || mbar_wait_bounded(done, static_cast<unsigned>(it) & 1u, kCopyWaitLimitNs)) != 0;
         if (!ok) break;
         tc::fence_after();
 

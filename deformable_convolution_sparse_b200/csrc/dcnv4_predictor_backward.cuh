@@ -24,6 +24,7 @@
 
 #include "dcnv4_async.cuh"
 #include "dcnv4_kernels.cuh"
+#include "dcnv4_records.cuh"
 #include "dcnv4_tcgen05.cuh"
 
 namespace dcnv4 {
@@ -45,12 +46,6 @@ struct PredBwdParams {
 constexpr int kFlushTiles = 16;
 // the wait for a run of kFlushTiles tiles: every copy of it has its own limit, one after the other at worst
 constexpr uint64_t kFlushWaitLimitNs = 2 * kCopyWaitLimitNs;
-
-// projection channel of a record slot
-__host__ __device__ __forceinline__ int channel_of_slot(int s, int G, int P) {
-    const int g = s / (3 * P), r = s - g * 3 * P;
-    return r < 2 * P ? g * 2 * P + r : 2 * G * P + g * P + (r - 2 * P);
-}
 
 template <typename T>
 constexpr int split_planes() {
@@ -96,7 +91,7 @@ pred_split_weight_kernel(const T* __restrict__ w, __nv_bfloat16* __restrict__ pl
         const int s = static_cast<int>(2 * i / p.wpitch), c = static_cast<int>(2 * i - static_cast<long long>(s) * p.wpitch);
         float a = 0.f, b = 0.f;
         if (s < p.NO) {
-            const T* row = w + static_cast<size_t>(channel_of_slot(s, p.G, p.P)) * p.C;
+            const T* row = w + static_cast<size_t>(slot_channel(s, p.G, p.P)) * p.C;
             if (c < p.C) a = ElemTraits<T>::to_float(__ldg(row + c));
             if (c + 1 < p.C) b = ElemTraits<T>::to_float(__ldg(row + c + 1));
         }
@@ -754,9 +749,9 @@ pred_grad_w_join_kernel(const float* __restrict__ part, const float* __restrict_
             for (int k = 1; k < 16; ++k) a += red[k][lane];
             if (i < n) {
                 const int s = static_cast<int>(i / p.C), c = static_cast<int>(i - static_cast<long long>(s) * p.C);
-                gw[static_cast<size_t>(channel_of_slot(s, p.G, p.P)) * p.C + c] = a;
+                gw[static_cast<size_t>(slot_channel(s, p.G, p.P)) * p.C + c] = a;
             } else {
-                gb[channel_of_slot(static_cast<int>(i - n), p.G, p.P)] = a;
+                gb[slot_channel(static_cast<int>(i - n), p.G, p.P)] = a;
             }
         }
         __syncthreads();

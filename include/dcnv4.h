@@ -255,7 +255,9 @@ DCNV4_API int dcnv4_predictor(const void *y, const void *weight, const float *bi
  * device fp32 [NO], or NULL when it is not wanted. All three are fully
  * overwritten (M == 0: the weight's and the bias's with zeros). flags as
  * dcnv4_predictor. Sums are fp32 and their order is fixed by the sizes: the
- * same bits in every run. workspace: device, 256-byte aligned, at least
+ * same bits in every run. A NaN or an infinity in y, weight or
+ * grad_offset_mask (or an fp32 magnitude above 3.38e38) makes the sums it
+ * enters NaN or infinite, no others. workspace: device, 256-byte aligned, at least
  * dcnv4_predictor_backward_workspace's bytes; its contents before and after
  * do not matter, and calls whose work overlaps on the GPU need one each.
  * Errors: those of dcnv4_predictor, DCNV4_ERR_WORKSPACE, and DCNV4_ERR_ALIAS

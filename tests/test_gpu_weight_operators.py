@@ -134,6 +134,10 @@ MX_CASES = [
     (200, 33, 3, 3, False, True),      # one channel in the last block, odd rows
     (131, 100, 5, 3, False, False),    # 135 channels
     (90, 1056, 2, 3, False, True),     # 33 blocks
+    (500, 96, 8, 3, False, True),      # 3 blocks, 512-thread CTAs: the last round of pieces is half empty
+    (300, 72, 8, 3, False, False),     # the same, a quarter of the last block
+    (1300, 160, 8, 3, False, True),
+    (40, 4000, 1, 1, False, True),     # rows too long for the tensor-core kernel
     (20000, 64, 4, 3, False, True),    # several tiles per SM
 ]
 
@@ -237,6 +241,7 @@ BWD_CASES = [
     (131, 100, 5, 3, False, True),
     (513, 9, 2, 5, False, True),
     (4999, 64, 4, 3, False, True),
+    (12000, 512, 32, 3, False, True),  # more than one run of tiles per CTA between two readings of the sums
 ]
 
 
@@ -354,6 +359,27 @@ def test_predictor_backward_against_differences(cuda_device):
             # each record is rounded C + 2 times from terms below 10 in size; 54 * M of them, weighted by |g|
             tol = (C + 2) * U * 10 * C * gr.abs().sum().item() / step
             assert abs(diff - grad.view(-1)[i].item()) <= tol
+
+
+def test_offsets_past_32_bits(cuda_device):
+    """Records of 2^31 - 1 elements at most, more than 2^32 bytes: the last rows equal a call on them alone."""
+    if torch.cuda.get_device_properties(cuda_device).total_memory < 60e9:
+        pytest.skip("needs 30 GB")
+    M, C, G, tail = 9_900_000, 8, 8, 700
+    codes, scales, _ = _mx_weight(216, C, 1, cuda_device)
+    g = torch.Generator(device=cuda_device).manual_seed(3)
+    y = torch.randn(M, C, generator=g, device=cuda_device).half()
+    rec = dcn.predictor_mx(y, codes, scales, None, G=G, K=3)
+    assert torch.equal(rec[-tail:], dcn.predictor_mx(y[-tail:].contiguous(), codes, scales, None, G=G, K=3))
+    del rec
+    w = torch.randn(216, C, generator=g, device=cuda_device).half()
+    gr = torch.zeros(M, G, 27, device=cuda_device)
+    gr[-tail:] = torch.randn(tail, G, 27, generator=g, device=cuda_device)
+    gy, gw, gb = dcn.predictor_backward(y, w, gr, G=G, K=3)
+    ty, tw, tb = dcn.predictor_backward(y[-tail:].contiguous(), w, gr[-tail:].contiguous(), G=G, K=3)
+    assert torch.equal(gy[-tail:], ty) and not gy[:-tail].any()
+    for a, b in ((gw, tw), (gb, tb)):   # the pixels are shared out differently: rounding only
+        assert bool(((a - b).abs() <= 1e-4 * b.abs().max()).all())
 
 
 # ------------------------------------------------------ orthogonalised update ---
