@@ -201,13 +201,14 @@ __device__ __forceinline__ uint4 ortho_load(const __half* p) {
 // planes, 64 x 64 of the right ones, in a ring of STAGES; warp 1 issues the
 // products; warps 2..9 read the accumulators, form the result
 // and write it as planes through shared memory (the idle ring) and TMA. A
-// product's time is mostly latency (per tile: first load 0.7 us, products 0.4
+// product's time is mostly latency (per tile: first load 0.8 us, products 0.3
 // us per 64 k, epilogue 0.5, store 0.6; the launch about 2 us more), so the
 // ring is deep, four stages, while the tiles fit the SMs once; when there are
 // more tiles than SMs, two stages leave room for two CTAs per SM (256 columns
-// of tensor memory each) whose latencies overlap. Whole iteration, 432 x 256:
-// 18 matrices 147 us with four stages against 157 with two, 40 matrices 328
-// against 248.
+// of tensor memory each) whose latencies overlap. Whole iteration in fp32, 432
+// x 256: 18 matrices (144 and 252 tiles) 120 us, all products with four stages
+// 132, with two 149; 40 matrices 243 with two, 289 with four. 4 of 864 x 512
+// in bf16: 149 us.
 constexpr int kGram = 0, kPoly = 1, kApply = 2, kLast = 3;
 constexpr int kOrthoEpi = 256, kOrthoThreads = 64 + kOrthoEpi;
 constexpr unsigned kOrthoStageBytes = 2u * 16384u + 2u * 8192u;
@@ -400,7 +401,8 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
 // overwrites them with P. One warp issues a product's instructions, then all
 // warps turn the accumulators into the next operand. What bounds it is the
 // chain of 3 * steps dependent products, each a few hundred cycles of tensor
-// work between two barriers.
+// work between two barriers: 4 matrices of 108 x 64 take 28 us (67 through the
+// kernels above), 18 of 216 x 128 64 us (85), 300 of 108 x 64 83 us (161).
 constexpr int kOrthoSmallThreads = 512, kOrthoSmallBlocks = 7;
 constexpr unsigned kOrthoBlock = 2u * 16384u;
 constexpr int kOrthoMaxSteps = 64;

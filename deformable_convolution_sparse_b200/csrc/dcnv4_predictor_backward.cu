@@ -117,8 +117,9 @@ int launch(const void* y, const void* w, const float* grec, float* gy, float* gw
     int rc = launch_chained(dcnv4::pred_split_weight_kernel<T>, dim3(static_cast<unsigned>(std::min<long long>((pairs + 255) / 256, 148 * 8))),
                             256, 0, s, static_cast<const T*>(w), planes, p);
     if (rc) return rc;
-    // 128 channels per tile halve the readings of g; with many slots (long chains of truncated additions) or three
-    // weight planes (shared memory) 64 channels leave room for three accumulators of order 0
+    // 128 channels per tile halve the readings of g (129,032 pixels x 128 channels x 216 slots: bf16 92.7 us against
+    // 117.3, fp16 139 against 152); with many slots (long chains of truncated additions) or three weight planes
+    // (shared memory) 64 channels leave room for three accumulators of order 0
     if constexpr (WP <= 2) {
         if (p.C > 64 && p.NO <= 256) rc = launch_grad_y<128, WP>(wmap, gmap, omap, grec, gy, p, nsm, raw_g, s);
         else rc = launch_grad_y<64, WP>(wmap, gmap, omap, grec, gy, p, nsm, raw_g, s);

@@ -17,6 +17,15 @@
 // three accumulators in turn, the small others to one of their own, and these
 // are added with rounding when they are read; the weight's gradient is read
 // out every kFlushTiles tiles of pixels.
+//
+// Memory bounds the formulas: g is read by two kernels (one would need more
+// tensor memory than there is, dL/dW's sums beside dL/dy's, for more than 128
+// slots). What bounds the kernels: DRAM latency against the 64 to 96 KB of raw
+// tiles a CTA can keep in flight beside its operand planes (such a ring alone,
+// without any work, reads g at 3.0 to 3.5 TB/s), and for three planes of y the
+// products themselves. Measured on B200, everything together: 200,704 pixels x
+// 64 bf16 channels x 108 slots 76 us (grad_y 34, grad_weight 36), 26,047 x 320
+// fp32 x 192 slots 100 us, 196 x 256 fp16 x 432 slots 24 us.
 #pragma once
 
 #include <cuda_bf16.h>
