@@ -47,6 +47,8 @@
  *     host-memory entry points, three streams per device and whether a
  *     geometry's bands of output rows take the whole image's plan); each
  *     cache is guarded by its own lock.
+ *   - Scratch memory, where an operator needs any, is the caller's: its _workspace
+ *     call gives the bytes for the sizes.
  *   - Compute calls are asynchronous on `stream` (a cudaStream_t; NULL is the
  *     legacy default stream) and never synchronise. Arguments are checked on
  *     the host before anything is launched; on a non-zero return nothing was
