@@ -205,6 +205,10 @@ predictor_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_const
     // Launched with programmatic stream serialisation: wait for the previous
     // kernel on the stream (complete, its writes visible) before the first
     // global access, then let the next launch start its set-up as SMs free up.
+    // By then every CTA holds its tensor memory (the barrier): a CTA still
+    // waiting for columns that another stream's kernel has could see the next
+    // launch take them and wait for this one in turn.
+    __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (int o = tid; o < p.NO; o += blockDim.x) {

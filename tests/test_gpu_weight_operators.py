@@ -541,6 +541,36 @@ def test_on_another_stream_and_two_at_once(cuda_device):
             assert torch.equal(a, b)
 
 
+def test_tensor_memory_shared_between_streams(cuda_device):
+    """Projections that want all of an SM's tensor memory, each followed by one that wants little, beside a second
+    stream whose small kernels hold columns nearly all the time: everything finishes, with the same results."""
+    g = torch.Generator(device=cuda_device).manual_seed(4)
+    y = torch.randn(60000, 64, generator=g, device=cuda_device).half()
+    w = (torch.randn(216, 64, generator=g, device=cuda_device) / 8).half()
+    codes, scales = dcn.mx_quantize(w)
+    small = dcn.mx_quantize((torch.randn(27, 64, generator=g, device=cuda_device) / 8).half())
+    torch.cuda.synchronize()
+
+    def main():
+        return dcn.predictor(y, w, None, G=8, K=3), dcn.predictor_mx(y[:9000], codes, scales, None, G=8, K=3)
+
+    def side():
+        return (dcn.predictor_mx(y, *small, None, G=1, K=3),)
+    want_main, want_side = main(), side()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(10):
+        for s, call, want in zip(streams, (main, side), (want_main, want_side)):
+            with torch.cuda.stream(s):
+                got.append((call(), want))
+    torch.cuda.synchronize()
+    for r, want in got:
+        for a, b in zip(r, want):
+            assert torch.equal(a, b)
+    assert binding.device_status() == 0
+
+
 @pytest.mark.parametrize("M", [130, 20000])
 def test_gradients_are_complete_for_the_next_launch(M, cuda_device):
     """The next kernel on the stream reads every gradient at once, eagerly and in a graph: kernels that start

@@ -2,6 +2,9 @@
 error class is reported before any CUDA call, empty calls touch nothing, and the
 workspaces' sizes depend on the arguments alone."""
 import ctypes
+import glob
+import os
+import re
 
 import pytest
 
@@ -162,3 +165,21 @@ def test_bindings_refuse_cpu_tensors_and_wrong_arguments():
         B.predictor_backward(x, torch.zeros(27, 64), torch.zeros(4, 1, 27), G=1, K=3)
     with pytest.raises(ValueError, match="CUDA"):
         B.orthogonalize(x)
+
+
+def test_tensor_memory_is_held_before_the_next_launch_may_start():
+    """Every kernel that allocates tensor memory passes a CTA barrier between that and letting the next launch
+    start; else a CTA still waiting for columns (another stream's kernel has them) could see the next launch's CTA
+    take them and wait for this kernel in turn, for good."""
+    csrc = os.path.join(os.path.dirname(B.__file__), "csrc")
+    seen = 0
+    for path in sorted(glob.glob(os.path.join(csrc, "*.cuh"))):
+        with open(path) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        for kernel in text.split("__global__")[1:]:
+            alloc = re.search(r"tc::alloc\(|tcgen05\.alloc", kernel)
+            trigger = kernel.find("griddepcontrol.launch_dependents")
+            if alloc and trigger >= 0:
+                seen += 1
+                assert "__syncthreads();" in kernel[alloc.start():trigger], (os.path.basename(path), kernel[:120])
+    assert seen >= 6
