@@ -41,16 +41,16 @@ int check_mx(const void* x, const void* codes, const void* scales, int M, int C,
     return DCNV4_OK;
 }
 
-unsigned mx_grid(long long blocks) {
-    // 64 or 128 blocks (256 threads) per CTA and round, at most 16 CTAs per SM
-    return static_cast<unsigned>(std::min<long long>((blocks + 63) / 64, 148LL * 16));
+// 256 threads per CTA, at most 16 CTAs per SM
+unsigned mx_grid(long long blocks, int lanes) {
+    return static_cast<unsigned>(std::min<long long>((blocks * lanes + 255) / 256, 148LL * 16));
 }
 
 template <typename T>
 int launch_quantize(const void* x, uint8_t* codes, uint8_t* scales, int C, long long blocks, cudaStream_t s) {
     const bool vec = C % 8 == 0 && aligned(x, 16);
     auto kern = vec ? dcnv4::mx_quantize_kernel<T, true> : dcnv4::mx_quantize_kernel<T, false>;
-    return launch_chained(kern, dim3(mx_grid((blocks + 1) / 2)), 256, 0, s, static_cast<const T*>(x),
+    return launch_chained(kern, dim3(mx_grid(blocks, 2)), 256, 0, s, static_cast<const T*>(x),
                           reinterpret_cast<uint2*>(codes), scales, static_cast<unsigned>(blocks),
                           dcnv4::make_fastdiv(static_cast<unsigned>((C + 31) / 32)), C);
 }
@@ -59,7 +59,7 @@ template <typename T>
 int launch_dequantize(const uint8_t* codes, const uint8_t* scales, void* x, int C, long long blocks, cudaStream_t s) {
     const bool vec = C % 8 == 0 && aligned(x, 16);
     auto kern = vec ? dcnv4::mx_dequantize_kernel<T, true> : dcnv4::mx_dequantize_kernel<T, false>;
-    return launch_chained(kern, dim3(mx_grid(blocks)), 256, 0, s, reinterpret_cast<const uint32_t*>(codes), scales,
+    return launch_chained(kern, dim3(mx_grid(blocks, dcnv4::mx_lanes<T>())), 256, 0, s, codes, scales,
                           static_cast<T*>(x), static_cast<unsigned>(blocks),
                           dcnv4::make_fastdiv(static_cast<unsigned>((C + 31) / 32)), C);
 }
