@@ -542,6 +542,16 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
             if (lane == 0) mbar_arrive(&raw_empty[k & 3]);
         };
         for (int i = 0; i < mine && ok; ++i) {
+            // With one stage of y, both groups wait for its release once a tile, before their first store. A group
+            // that writes y (or a stage of g) in every other tile only would otherwise miss a phase of the barrier
+            // and take the one before for the one it needs.
+            bool freed = i == 0;
+            auto y_freed = [&] {
+                if constexpr (!S::kDirectY && S::kYStages == 1) {
+                    if (!freed) ok = ok && mbar_wait_bounded(&empty_y[0], static_cast<unsigned>(i - 1) & 1u, kCopyWaitLimitNs);
+                    freed = true;
+                }
+            };
             if constexpr (!S::kDirectY) {
                 const int ys = i % S::kYStages, yn = i / S::kYStages;
 #pragma unroll
@@ -552,7 +562,9 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
                         Piece<T> piece;
                         if constexpr (RAW) take(piece, walk);
                         else piece.from_global(y, walk, pixel(i), p.M, c0 + b * 64, p.C);
-                        if (yn > 0) ok = ok && mbar_wait_bounded(&empty_y[ys], static_cast<unsigned>(yn - 1) & 1u, kCopyWaitLimitNs);
+                        y_freed();
+                        if (S::kYStages > 1 && yn > 0)
+                            ok = ok && mbar_wait_bounded(&empty_y[ys], static_cast<unsigned>(yn - 1) & 1u, kCopyWaitLimitNs);
                         if (!ok) break;
                         piece.template store<YP>(sm + ys * ystage + b * 16384, p.ystep, walk);
                         hand_over(&full_y[ys], lane);
@@ -569,6 +581,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
                     Piece<float> piece;
                     if constexpr (RAW) take(piece, walk);
                     else piece.from_global(grec, walk, pixel(i), p.M, g0 + ch * 64, p.NO);
+                    y_freed();
                     if (n >= 2) ok = ok && mbar_wait_bounded(&empty_g[s], static_cast<unsigned>((n >> 1) - 1) & 1u, kCopyWaitLimitNs);
                     if (!ok) break;
                     piece.template store<3>(gsm + s * S::kG, 16384u, walk);

@@ -242,6 +242,15 @@ BWD_CASES = [
     (513, 9, 2, 5, False, True),
     (4999, 64, 4, 3, False, True),
     (12000, 512, 32, 3, False, True),  # more than one run of tiles per CTA between two readings of the sums
+    # at most 64 channels and 128 slots: one or two chunks of slots, channels that end inside a half, several runs
+    (1, 8, 4, 1, False, True),
+    (300, 24, 4, 3, False, True),
+    (257, 56, 8, 2, False, False),
+    (20001, 40, 8, 2, False, True),
+    (19000, 64, 10, 2, False, True),
+    (305000, 16, 5, 2, False, True),
+    (304001, 64, 4, 3, False, True),
+    (610000, 33, 4, 3, False, True),   # (rows that TMA cannot take)
 ]
 
 
