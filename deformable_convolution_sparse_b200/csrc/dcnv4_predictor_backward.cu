@@ -95,6 +95,23 @@ int launch_grad_w(const CUtensorMap& gmap, const CUtensorMap& ymap, const float*
                           gmap, ymap, grec, y, part, pbias, p);
 }
 
+// One reading of g for everything, where the sums fit the tensor memory and y is a plane of itself.
+int launch_grad_both(const CUtensorMap& gmap, const CUtensorMap& ymap, const CUtensorMap& omap, const void* w, float* part,
+                     float* pbias, const dcnv4::PredBwdParams& p, cudaStream_t s) {
+    constexpr unsigned smem = dcnv4::GradBothShape::kSmem;
+    static_assert(smem <= kTileSmemLimit, "the stages do not fit");
+    auto kern = dcnv4::pred_grad_both_kernel;
+    if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess) return DCNV4_ERR_LAUNCH;
+    return launch_chained(kern, dim3(static_cast<unsigned>(p.walkers)), dcnv4::kGradYThreads, smem, s, gmap, ymap, omap,
+                          static_cast<const __nv_bfloat16*>(w), part, pbias, p);
+}
+
+int launch_join(const float* part, const float* pbias, float* gw, float* gb, const dcnv4::PredBwdParams& p, cudaStream_t s) {
+    const long long n = (static_cast<long long>(p.NO) * p.C + (gb ? p.NO : 0) + 31) / 32;
+    return launch_chained(dcnv4::pred_grad_w_join_kernel, dim3(static_cast<unsigned>(std::min<long long>(n, 148 * 4))), 512, 0, s,
+                          part, pbias, gw, gb, p);
+}
+
 template <typename T>
 int launch(const void* y, const void* w, const float* grec, float* gy, float* gw, float* gb, unsigned char* ws,
            dcnv4::PredBwdParams p, int dtype, cudaStream_t s) {
@@ -113,6 +130,13 @@ int launch(const void* y, const void* w, const float* grec, float* gy, float* gw
         (raw_w && !tile_map(&ymap, tma_dtype<T>(), E, const_cast<void*>(y), p.C, p.M, 1, 128 / E, 128)) ||
         (p.tma_out && !tile_map(&omap, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, gy, p.C, p.M, 1, 32, 128)))
         return DCNV4_ERR_CUDA;
+    // 200,704 pixels x 64 channels x 108 slots: 46.6 us against 75.8 by the kernels below
+    if constexpr (WP == 1) {
+        if (p.C <= 64 && p.NO <= 128 && raw_w && p.tma_out && aligned(w, 16)) {
+            const int rc = launch_grad_both(gmap, ymap, omap, w, part, pbias, p, s);
+            return rc ? rc : launch_join(part, pbias, gw, gb, p, s);
+        }
+    }
     const long long pairs = static_cast<long long>(p.wrows) * p.wpitch / 2;
     int rc = launch_chained(dcnv4::pred_split_weight_kernel<T>, dim3(static_cast<unsigned>(std::min<long long>((pairs + 255) / 256, 148 * 8))),
                             256, 0, s, static_cast<const T*>(w), planes, p);
@@ -130,9 +154,7 @@ int launch(const void* y, const void* w, const float* grec, float* gy, float* gw
     rc = raw_w ? launch_grad_w<T, true>(gmap, ymap, grec, static_cast<const T*>(y), part, pbias, p, s)
                : launch_grad_w<T, false>(gmap, ymap, grec, static_cast<const T*>(y), part, pbias, p, s);
     if (rc) return rc;
-    const long long n = (static_cast<long long>(p.NO) * p.C + (gb ? p.NO : 0) + 31) / 32;
-    return launch_chained(dcnv4::pred_grad_w_join_kernel, dim3(static_cast<unsigned>(std::min<long long>(n, 148 * 4))), 512, 0, s,
-                          static_cast<const float*>(part), static_cast<const float*>(pbias), gw, gb, p);
+    return launch_join(part, pbias, gw, gb, p, s);
 }
 
 }  // namespace

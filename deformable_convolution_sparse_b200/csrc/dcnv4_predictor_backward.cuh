@@ -18,14 +18,16 @@
 // are added with rounding when they are read; the weight's gradient is read
 // out every kFlushTiles tiles of pixels.
 //
-// Memory bounds the formulas: g is read by two kernels (one would need more
-// tensor memory than there is, dL/dW's sums beside dL/dy's, for more than 128
-// slots). What bounds the kernels: DRAM latency against the 64 to 96 KB of raw
-// tiles a CTA can keep in flight beside its operand planes (such a ring alone,
-// without any work, reads g at 3.0 to 3.5 TB/s), and for three planes of y the
-// products themselves. Measured on B200, everything together: 200,704 pixels x
-// 64 bf16 channels x 108 slots 76 us (grad_y 34, grad_weight 36), 26,047 x 320
-// fp32 x 192 slots 100 us, 196 x 256 fp16 x 432 slots 24 us.
+// Memory bounds the formulas. bf16 with at most 64 channels and 128 slots takes
+// one kernel that reads g once; else g is read by two (dL/dW's sums beside
+// dL/dy's need more tensor memory than there is, the planes of y and W more
+// shared memory). What bounds the kernels: DRAM latency against the 64 to 96 KB
+// of raw tiles a CTA can keep in flight beside its operand planes (such a ring
+// alone, without any work, reads g at 3.0 to 3.5 TB/s), and for three planes of
+// y the products themselves. Measured on B200, everything together: 200,704
+// pixels x 64 channels x 108 slots in bf16 47 us (76 by the two kernels, 34 and
+// 36 of them), 26,047 x 320 fp32 x 192 slots 101 us, 196 x 256 fp16 x 432 slots
+// 24 us.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -743,6 +745,269 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
     tc::fence_after();
     if (warp == 16) tc::dealloc(tmem, 512u);
     asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// All of it in one pass over g, for bf16 y with at most 64 channels and 128
+// slots: the planes of a tile of g serve both as grad_y's left operand (K-major,
+// 64 slots at a time) and as the transposed grad_weight's (MN-major: 128 slots
+// x 64 channels of sums), so that both sets of sums, three accumulators and the
+// small terms' each, fill the tensor memory exactly. W's rows (its own plane)
+// are laid out once per CTA, y's tiles come by TMA as its plane. Warps 0..15
+// write the planes of g and sum it for the bias; a lane of warp 16 loads; warp
+// 17 issues; warps 18..21 read grad_y's sums after every tile and grad_weight's
+// every kFlushTiles.
+struct GradBothShape {
+    static constexpr int kRaws = 2, kYStages = 2;
+    static constexpr unsigned kG = 3u * 16384u, kY = 16384u, kW = 16384u, kOut = 16384u;
+    static constexpr unsigned kSmem = 1024u + 2 * kG + kYStages * kY + kW + kOut + kRaws * kRaw + 256u;
+};
+
+__global__ void __launch_bounds__(kGradYThreads, 1)
+pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CUtensorMap ymap,
+                      const __grid_constant__ CUtensorMap omap, const __nv_bfloat16* __restrict__ w,
+                      float* __restrict__ part, float* __restrict__ pbias, PredBwdParams p) {
+    using S = GradBothShape;
+    extern __shared__ unsigned char pb_smem_raw[];
+    unsigned char* gsm = pb_smem_raw + ((1024u - (smem_addr(pb_smem_raw) & 1023u)) & 1023u);
+    unsigned char* ysm = gsm + 2 * S::kG;
+    unsigned char* wsm = ysm + S::kYStages * S::kY;
+    unsigned char* outs = wsm + S::kW;
+    unsigned char* raws = outs + S::kOut;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(raws + S::kRaws * kRaw);
+    uint64_t *full_g = bars, *empty_g = bars + 2, *full_y = bars + 4, *empty_y = bars + 6, *raw_full = bars + 8,
+             *raw_empty = bars + 12, *full_w = bars + 16, *acc_full = bars + 17, *acc_empty = bars + 18,
+             *sum_full = bars + 19, *sum_empty = bars + 20;  // raw tiles: step n's the (n mod 4)-th
+    uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 21);
+    const int tid = threadIdx.x, warp = static_cast<int>(tc::uniform(threadIdx.x >> 5)), lane = tid & 31;
+    const int walker = static_cast<int>(blockIdx.x), nch = (p.NO + 63) / 64;
+    const int mine = (p.tiles - walker + p.walkers - 1) / p.walkers, steps = mine * nch;
+    auto pixel = [&](int i) { return (walker + i * p.walkers) * 128; };
+
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&full_g[s], kGroup / 32);
+            mbar_init(&empty_g[s], 1);
+            mbar_init(&full_y[s], 1);
+            mbar_init(&empty_y[s], 1);
+        }
+        for (int s = 0; s < 4; ++s) {
+            mbar_init(&raw_full[s], 1);
+            mbar_init(&raw_empty[s], kGroup / 32);
+        }
+        mbar_init(full_w, kConv / 32);
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 128);
+        mbar_init(sum_full, 1);
+        mbar_init(sum_empty, 128);
+        fence_barrier_init();
+    }
+    if (warp == 16) tc::alloc(slot, 512u);
+    tc::fence_before();
+    __syncthreads();  // every CTA holds its tensor memory before the next launch may start
+    tc::fence_after();
+    const uint32_t tmem = tc::uniform(*slot);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    bool ok = true;
+
+    if (warp < 16) {
+        // W's rows in record order, zeros past its end: row = slot, 16-byte chunk j at j ^ (row mod 8)
+        for (int q = tid; q < nch * 512; q += kConv) {
+            const int r = q >> 3, j = q & 7;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (r < p.NO && j * 8 < p.C)
+                v = __ldg(reinterpret_cast<const uint4*>(w + static_cast<size_t>(slot_channel(r, p.G, p.P)) * p.C + j * 8));
+            *reinterpret_cast<uint4*>(wsm + r * 128 + ((j ^ (r & 7)) << 4)) = v;
+        }
+        hand_over(full_w, lane);
+        // this group takes the chunks of its parity: with two a tile always the same one
+        const int s = warp >> 3;
+        const bool last = nch == 1 || s == 1;
+        const ChunkWalk walk(last ? p.NO - (nch - 1) * 64 : 64, tid);
+        float bs[8] = {};
+        for (int n = s; n < steps; n += 2) {
+            ok = mbar_wait_bounded(&raw_full[n & 3], static_cast<unsigned>(n >> 2) & 1u, kCopyWaitLimitNs);
+            if (!ok) break;
+            Piece<float> piece;
+            piece.from_raw(raws + s * kRaw, walk);
+            piece.landed();
+            if (lane == 0) mbar_arrive(&raw_empty[n & 3]);
+            if (n >= 2) ok = mbar_wait_bounded(&empty_g[s], static_cast<unsigned>((n >> 1) - 1) & 1u, kCopyWaitLimitNs);
+            if (!ok) break;
+            piece.template store<3>(gsm + s * S::kG, 16384u, walk);
+            hand_over(&full_g[s], lane);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)  // rows past the tile hold zeros
+                bs[e] += (piece.v[0][e] + piece.v[1][e]) + (piece.v[2][e] + piece.v[3][e]);
+        }
+        if (pbias != nullptr) {
+            // once the last products have read the operand tiles (a commit covers all those before it), the
+            // threads' sums are added there, a slot's in the order of its rows' pieces
+            const int end = (steps - 1) & 1;
+            if (ok) ok = mbar_wait_bounded(&empty_g[end], static_cast<unsigned>((steps - 1) >> 1) & 1u, kCopyWaitLimitNs);
+            float* red = reinterpret_cast<float*>(gsm);  // [thread][8]
+            tc::bar_sync(2, kConv);
+            if (ok)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) red[tid * 8 + k] = bs[k];
+            tc::bar_sync(2, kConv);
+            const int t = tid >> 3, part8 = tid & 7;
+            for (int ch = 0; ch < nch; ++ch) {
+                // eight threads per slot, every eighth of the slot's threads each, then the eight
+                const ChunkWalk of(ch + 1 < nch ? 64 : p.NO - ch * 64, tid);
+                const float* from = red + ch * kGroup * 8;
+                float v = 0.f;
+                if (t < of.ng * 8)
+                    for (int r = part8; r < of.rows; r += 8) {
+                        const float* at = from + (r * of.ng + (t >> 3)) * 8 + (t & 7);
+                        v += nch == 1 ? at[0] + at[kGroup * 8] : at[0];
+                    }
+                v += __shfl_xor_sync(0xffffffffu, v, 1);
+                v += __shfl_xor_sync(0xffffffffu, v, 2);
+                v += __shfl_xor_sync(0xffffffffu, v, 4);
+                if (ok && part8 == 0 && t < of.ng * 8 && ch * 64 + t < p.NO)
+                    pbias[static_cast<size_t>(walker) * p.NO + ch * 64 + t] = v;
+            }
+        }
+    } else if (warp == 16) {
+        if (lane == 0) {
+            for (int i = 0; i < mine && ok; ++i) {
+                for (int ch = 0; ch < nch && ok; ++ch) {
+                    const int n = i * nch + ch, f = n & 3, halves = ch * 64 + 32 < p.NO ? 2 : 1;
+                    if (n >= S::kRaws)
+                        ok = mbar_wait_bounded(&raw_empty[(n - S::kRaws) & 3], static_cast<unsigned>((n - S::kRaws) >> 2) & 1u,
+                                               kCopyWaitLimitNs);
+                    if (!ok) break;
+                    mbar_expect_tx(&raw_full[f], halves * 16384u);
+                    for (int h = 0; h < halves; ++h)
+                        tc::tma_load_3d(raws + (n & 1) * kRaw + h * 16384, &gmap, ch * 64 + h * 32, pixel(i), 0, &raw_full[f]);
+                    mbar_arrive(&raw_full[f]);
+                }
+                const int ys = i & 1;
+                if (ok && i >= 2) ok = mbar_wait_bounded(&empty_y[ys], static_cast<unsigned>((i >> 1) - 1) & 1u, kCopyWaitLimitNs);
+                if (!ok) break;
+                mbar_expect_tx(&full_y[ys], S::kY);
+                tc::tma_load_3d(ysm + ys * S::kY, &ymap, 0, pixel(i), 0, &full_y[ys]);
+                mbar_arrive(&full_y[ys]);
+            }
+        }
+    } else if (warp == 17) {
+        constexpr uint32_t iy = tc::idesc_f16(tc::kFmtBf16, 64, false, true), iw = tc::idesc_f16(tc::kFmtBf16, 64, true, true);
+        const uint32_t lead = tc::lead_lane(), sums = tmem + 256u;
+        ok = tc::warp_wait(full_w, 0u, kCopyWaitLimitNs);
+        for (int i = 0; i < mine && ok; ++i) {
+            const int ys = i & 1, t = i % kFlushTiles;
+            // grad_y, as the chunks come
+            if (i > 0) ok = tc::warp_wait(acc_empty, static_cast<unsigned>(i - 1) & 1u, kCopyWaitLimitNs);
+            for (int ch = 0; ch < nch && ok; ++ch) {
+                const int n = i * nch + ch, s = n & 1;
+                ok = tc::warp_wait(&full_g[s], static_cast<unsigned>(n >> 1) & 1u, kCopyWaitLimitNs);
+                if (!ok) break;
+                tc::fence_after();
+                const uint32_t a = tc::sw128(smem_addr(gsm + s * S::kG)), b = tc::sw128(smem_addr(wsm + ch * 8192));
+                const int ksteps = (min(64, p.NO - ch * 64) + 15) / 16;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k >= ksteps) break;
+                    tc::mma_f16(tmem + (k % 3) * 64u, a + k * 2, b + k * 128, iy, ch > 0 || k >= 3, lead);
+                    tc::mma_f16(tmem + 192u, a + 1024 + k * 2, b + k * 128, iy, ch > 0 || k > 0, lead);
+                    tc::mma_f16(tmem + 192u, a + 2048 + k * 2, b + k * 128, iy, true, lead);
+                }
+            }
+            if (!ok) break;
+            if (lead) tc::commit(acc_full);
+            // grad_weight, both chunks (a single one stands in for the second, whose sums nobody reads)
+            if (t == 0 && i > 0) ok = tc::warp_wait(sum_empty, static_cast<unsigned>(i / kFlushTiles - 1) & 1u, kCopyWaitLimitNs);
+            ok = ok && tc::warp_wait(&full_y[ys], static_cast<unsigned>(i >> 1) & 1u, kCopyWaitLimitNs);
+            if (!ok) break;
+            tc::fence_after();
+            const int s0 = (i * nch) & 1;
+            const uint32_t a = tc::sw128(smem_addr(gsm + s0 * S::kG), nch == 2 ? S::kG : 0u), b = tc::sw128(smem_addr(ysm + ys * S::kY));
+            uint32_t high = sums;
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {
+                tc::mma_f16(high, a + k * 128, b + k * 128, iw, t > 0 || k >= 3, lead);
+                tc::mma_f16(sums + 192u, a + 1024 + k * 128, b + k * 128, iw, t > 0 || k > 0, lead);
+                tc::mma_f16(sums + 192u, a + 2048 + k * 128, b + k * 128, iw, true, lead);
+                high = high == sums + 128 ? sums : high + 64;
+            }
+            if (lead) {
+                for (int ch = 0; ch < nch; ++ch) tc::commit(&empty_g[(s0 + ch) & 1]);
+                tc::commit(&empty_y[ys]);
+                if (t == kFlushTiles - 1 || i == mine - 1) tc::commit(sum_full);
+            }
+        }
+    } else {
+        const int quarter = warp & 3, row = quarter * 32 + lane, et = tid - (kConv + 64);
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const int high = min(3, (min(64, p.NO) + 15) / 16);
+        // three accumulators (as many of them as hold anything) and the small terms', 16 columns
+        auto add4 = [&](uint32_t at, int count, float (&v)[16]) {
+            float x[16];
+            tc::ld16(at + 192u, v);
+            for (int q = 0; q < count; ++q) {
+                tc::ld16(at + q * 64u, x);
+                tc::wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] += x[e];
+            }
+        };
+        for (int i = 0; i < mine; ++i) {
+            ok = tc::bar_and(1, 128, mbar_wait_bounded(acc_full, static_cast<unsigned>(i) & 1u, kCopyWaitLimitNs));
+            if (!ok) break;
+            tc::fence_after();
+            for (int h = 0; h < 2 && h * 32 < p.C; ++h) {
+                // the store that read the staging tile has done so
+                if (et == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                tc::bar_sync(1, 128);
+                for (int cc = 0; cc < 2; ++cc) {
+                    float v[16];
+                    add4(lanes + h * 32 + cc * 16, high, v);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<float4*>(outs + row * 128 + (((cc * 4 + q) ^ (row & 7)) << 4)) =
+                            make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                }
+                fence_proxy_async();
+                tc::bar_sync(1, 128);
+                if (et == 0) {
+                    tc::tma_store_3d(&omap, h * 32, pixel(i), 0, outs);
+                    tc::bulk_commit();
+                }
+            }
+            tc::fence_before();
+            mbar_arrive(acc_empty);
+            if (i % kFlushTiles != kFlushTiles - 1 && i != mine - 1) continue;
+            const int f = i / kFlushTiles;
+            ok = tc::bar_and(1, 128, mbar_wait_bounded(sum_full, static_cast<unsigned>(f) & 1u, kFlushWaitLimitNs));
+            if (!ok) break;
+            tc::fence_after();
+            float* o = part + (static_cast<size_t>(walker) * p.NO + row) * p.C;  // accumulator row = slot
+            for (int q = 0; q < 4; ++q) {
+                float v[16];
+                add4(lanes + 256u + q * 16, 3, v);
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                    if (row < p.NO && q * 16 + e < p.C) {
+                        float4* at = reinterpret_cast<float4*>(o + q * 16 + e);
+                        float4 r = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                        if (f > 0) {
+                            const float4 b = *at;
+                            r = make_float4(r.x + b.x, r.y + b.y, r.z + b.z, r.w + b.w);
+                        }
+                        *at = r;
+                    }
+            }
+            tc::fence_before();
+            mbar_arrive(sum_empty);
+        }
+        if (et == 0) tc::bulk_wait_all();
+    }
+    if (!ok) atomicOr(p.status, kStatusCopyTimeout);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 16) tc::dealloc(tmem, 512u);
 }
 
 // The walkers' partial sums added in a fixed order (sixteen strided runs of

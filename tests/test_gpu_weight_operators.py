@@ -336,6 +336,30 @@ def test_predictor_backward_nan_stays_in_its_rows_and_channels(cuda_device):
     assert torch.isnan(gb).nonzero().flatten().tolist() == [ch]
 
 
+@pytest.mark.parametrize("G", [2, 4], ids=["one_chunk", "two_chunks"])
+def test_predictor_backward_in_one_pass_nan_and_far_apart_magnitudes(G, cuda_device):
+    """The kernel that reads the records' gradients once (bf16, few channels and slots): rows of 1e-30 to 1e30, then
+    NaN and infinities, which stay in their rows, channels and slots."""
+    M, C, K = 20100, 64, 2
+    NO = 3 * G * K * K
+    g = torch.Generator().manual_seed(G)
+    gr = torch.randn(M, G, 3 * K * K, generator=g) * 10.0 ** (torch.rand(M, 1, 1, generator=g) * 60 - 30)
+    y = torch.randn(M, C, generator=g).bfloat16().to(cuda_device)
+    w = torch.randn(NO, C, generator=g).bfloat16().to(cuda_device)
+    gr = gr.to(cuda_device)
+    _check_grads(dcn.predictor_backward(y, w, gr, G=G, K=K), y, w, gr, G, K * K, True)
+    gr = torch.randn(M, G, 3 * K * K, generator=g).to(cuda_device)
+    gr[200, 1, 4] = float("inf")
+    y[19999, 3] = float("nan")
+    gy, gw, gb = dcn.predictor_backward(y, w, gr, G=G, K=K)
+    assert (~torch.isfinite(gy)).any(dim=1).nonzero().flatten().tolist() == [200]
+    ch = ow.slots(G, K * K).tolist().index(3 * K * K + 4)
+    bad = torch.zeros(NO, C, dtype=torch.bool, device=cuda_device)
+    bad[ch] = bad[:, 3] = True
+    assert torch.equal(~torch.isfinite(gw), bad)
+    assert (~torch.isfinite(gb)).nonzero().flatten().tolist() == [ch]
+
+
 def test_predictor_backward_without_pixels_writes_zeros(cuda_device):
     y = torch.zeros(0, 64, device=cuda_device)
     gw = torch.full((27, 64), 5.0, device=cuda_device)
