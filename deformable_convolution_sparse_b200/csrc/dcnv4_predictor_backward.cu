@@ -95,15 +95,16 @@ int launch_grad_w(const CUtensorMap& gmap, const CUtensorMap& ymap, const float*
                           gmap, ymap, grec, y, part, pbias, p);
 }
 
-// One reading of g for everything, where the sums fit the tensor memory and y is a plane of itself.
-int launch_grad_both(const CUtensorMap& gmap, const CUtensorMap& ymap, const CUtensorMap& omap, const void* w, float* part,
-                     float* pbias, const dcnv4::PredBwdParams& p, cudaStream_t s) {
-    constexpr unsigned smem = dcnv4::GradBothShape::kSmem;
+// One reading of g for everything, where the sums fit the tensor memory and the planes the shared memory.
+template <typename T>
+int launch_grad_both(const CUtensorMap& gmap, const CUtensorMap& ymap, const CUtensorMap& omap, const T* y, const T* w,
+                     float* gy, float* part, float* pbias, const dcnv4::PredBwdParams& p, cudaStream_t s) {
+    constexpr unsigned smem = dcnv4::GradBothShape<T>::kSmem;
     static_assert(smem <= kTileSmemLimit, "the stages do not fit");
-    auto kern = dcnv4::pred_grad_both_kernel;
+    auto kern = dcnv4::pred_grad_both_kernel<T>;
     if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess) return DCNV4_ERR_LAUNCH;
-    return launch_chained(kern, dim3(static_cast<unsigned>(p.walkers)), dcnv4::kGradYThreads, smem, s, gmap, ymap, omap,
-                          static_cast<const __nv_bfloat16*>(w), part, pbias, p);
+    return launch_chained(kern, dim3(static_cast<unsigned>(p.walkers)), dcnv4::kGradYThreads, smem, s, gmap, ymap, omap, y, w,
+                          gy, part, pbias, p);
 }
 
 int launch_join(const float* part, const float* pbias, float* gw, float* gb, const dcnv4::PredBwdParams& p, cudaStream_t s) {
@@ -130,10 +131,12 @@ int launch(const void* y, const void* w, const float* grec, float* gy, float* gw
         (raw_w && !tile_map(&ymap, tma_dtype<T>(), E, const_cast<void*>(y), p.C, p.M, 1, 128 / E, 128)) ||
         (p.tma_out && !tile_map(&omap, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, gy, p.C, p.M, 1, 32, 128)))
         return DCNV4_ERR_CUDA;
-    // 200,704 pixels x 64 channels x 108 slots: 46.6 us against 75.8 by the kernels below
-    if constexpr (WP == 1) {
-        if (p.C <= 64 && p.NO <= 128 && raw_w && p.tma_out && aligned(w, 16)) {
-            const int rc = launch_grad_both(gmap, ymap, omap, w, part, pbias, p, s);
+    // 200,704 pixels x 64 channels x 108 slots: bf16 40.9 us against 71.2 by the kernels below, fp16 59.4 against 87.3;
+    // 196 pixels: 8.6 against 12.2, 9.8 against 14.1 (replayed from a graph)
+    if constexpr (WP <= 2) {
+        if (p.C <= 64 && p.NO <= 128 && (WP == 1 || p.NO > 64) && raw_w && p.tma_out && aligned(w, 16)) {
+            const int rc = launch_grad_both<T>(gmap, ymap, omap, static_cast<const T*>(y), static_cast<const T*>(w), gy,
+                                               part, pbias, p, s);
             return rc ? rc : launch_join(part, pbias, gw, gb, p, s);
         }
     }

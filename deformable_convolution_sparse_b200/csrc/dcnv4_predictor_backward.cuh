@@ -18,15 +18,15 @@
 // are added with rounding when they are read; the weight's gradient is read
 // out every kFlushTiles tiles of pixels.
 //
-// Memory bounds the formulas. bf16 with at most 64 channels and 128 slots takes
-// one kernel that reads g once; else g is read by two (dL/dW's sums beside
+// Memory bounds the formulas. 16-bit y with at most 64 channels and 128 slots
+// takes one kernel that reads g once; else g is read by two (dL/dW's sums beside
 // dL/dy's need more tensor memory than there is, the planes of y and W more
 // shared memory). What bounds the kernels: DRAM latency against the 64 to 96 KB
 // of raw tiles a CTA can keep in flight beside its operand planes (such a ring
 // alone, without any work, reads g at 3.0 to 3.5 TB/s), and for three planes of
 // y the products themselves. Measured on B200, everything together: 200,704
-// pixels x 64 channels x 108 slots in bf16 47 us (76 by the two kernels, 34 and
-// 36 of them), 26,047 x 320 fp32 x 192 slots 101 us, 196 x 256 fp16 x 432 slots
+// pixels x 64 channels x 108 slots in bf16 41 us (71 by the two kernels), in
+// fp16 59 (87), replayed from a graph; 26,047 x 320 fp32 x 192 slots 101 us, 196 x 256 fp16 x 432 slots
 // 24 us.
 #pragma once
 
@@ -73,6 +73,18 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&w)[PLANE
             a -= __uint_as_float(w[q] << 16);
             b -= __uint_as_float(w[q] & 0xffff0000u);
         }
+    }
+}
+
+// eight 16-bit values as fp32
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& w, T* t, float (&v)[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 f = unpack2(u[k], t);
+        v[2 * k] = f.x;
+        v[2 * k + 1] = f.y;
     }
 }
 
@@ -747,26 +759,32 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// All of it in one pass over g, for bf16 y with at most 64 channels and 128
+// All of it in one pass over g, for 16-bit y with at most 64 channels and 128
 // slots: the planes of a tile of g serve both as grad_y's left operand (K-major,
 // 64 slots at a time) and as the transposed grad_weight's (MN-major: 128 slots
 // x 64 channels of sums), so that both sets of sums, three accumulators and the
-// small terms' each, fill the tensor memory exactly. W's rows (its own plane)
-// are laid out once per CTA, y's tiles come by TMA as its plane. Warps 0..15
-// write the planes of g and sum it for the bias; a lane of warp 16 loads; warp
-// 17 issues; warps 18..21 read grad_y's sums after every tile and grad_weight's
-// every kFlushTiles.
+// small terms' each, fill the tensor memory exactly. W's planes are laid out
+// once per CTA. Warps 0..15 write the planes of g and sum it for the bias; a
+// lane of warp 16 loads; warp 17 issues; warps 18..21 read grad_y's sums after
+// every tile and grad_weight's every kFlushTiles. bf16 y is its own plane and
+// comes by TMA; fp16's two planes of y and W leave no room for raw tiles of y
+// nor for staging grad_y, so y comes through registers, a tile ahead, and
+// grad_y leaves from them (65 slots or more: both groups of converters then
+// have a chunk of every tile, and see every phase of y's one stage).
+template <typename T>
 struct GradBothShape {
-    static constexpr int kRaws = 2, kYStages = 2;
-    static constexpr unsigned kG = 3u * 16384u, kY = 16384u, kW = 16384u, kOut = 16384u;
+    static constexpr int PL = split_planes<T>(), kRaws = 2, kYStages = PL == 1 ? 2 : 1;
+    static constexpr unsigned kG = 3u * 16384u, kY = PL * 16384u, kW = PL * 16384u, kOut = PL == 1 ? 16384u : 0u;
     static constexpr unsigned kSmem = 1024u + 2 * kG + kYStages * kY + kW + kOut + kRaws * kRaw + 256u;
 };
 
+template <typename T>
 __global__ void __launch_bounds__(kGradYThreads, 1)
 pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CUtensorMap ymap,
-                      const __grid_constant__ CUtensorMap omap, const __nv_bfloat16* __restrict__ w,
-                      float* __restrict__ part, float* __restrict__ pbias, PredBwdParams p) {
-    using S = GradBothShape;
+                      const __grid_constant__ CUtensorMap omap, const T* __restrict__ y, const T* __restrict__ w,
+                      float* __restrict__ gy, float* __restrict__ part, float* __restrict__ pbias, PredBwdParams p) {
+    using S = GradBothShape<T>;
+    constexpr int PL = S::PL;
     extern __shared__ unsigned char pb_smem_raw[];
     unsigned char* gsm = pb_smem_raw + ((1024u - (smem_addr(pb_smem_raw) & 1023u)) & 1023u);
     unsigned char* ysm = gsm + 2 * S::kG;
@@ -787,7 +805,7 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
         for (int s = 0; s < 2; ++s) {
             mbar_init(&full_g[s], kGroup / 32);
             mbar_init(&empty_g[s], 1);
-            mbar_init(&full_y[s], 1);
+            mbar_init(&full_y[s], PL == 1 ? 1 : kConv / 32);
             mbar_init(&empty_y[s], 1);
         }
         for (int s = 0; s < 4; ++s) {
@@ -817,7 +835,13 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
             uint4 v = make_uint4(0, 0, 0, 0);
             if (r < p.NO && j * 8 < p.C)
                 v = __ldg(reinterpret_cast<const uint4*>(w + static_cast<size_t>(slot_channel(r, p.G, p.P)) * p.C + j * 8));
-            *reinterpret_cast<uint4*>(wsm + r * 128 + ((j ^ (r & 7)) << 4)) = v;
+            if constexpr (PL == 1) {
+                *reinterpret_cast<uint4*>(wsm + r * 128 + ((j ^ (r & 7)) << 4)) = v;
+            } else {
+                float f[8];
+                unpack8(v, static_cast<T*>(nullptr), f);
+                store_split8<PL>(wsm, 16384u, r, j, f);
+            }
         }
         hand_over(full_w, lane);
         // this group takes the chunks of its parity: with two a tile always the same one
@@ -825,6 +849,18 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
         const bool last = nch == 1 || s == 1;
         const ChunkWalk walk(last ? p.NO - (nch - 1) * 64 : 64, tid);
         float bs[8] = {};
+        // fp16 (always two chunks): y comes through registers, a tile ahead; this thread's pixel and 16 channels
+        const int yrow = s * 64 + (tid % kGroup >> 2), yc = (tid & 3) * 16;
+        uint4 yv[2];
+        auto load_y = [&](int i) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int m = i < mine ? pixel(i) + yrow : p.M, c = yc + q * 8;
+                yv[q] = m < p.M && c < p.C ? __ldg(reinterpret_cast<const uint4*>(y + static_cast<size_t>(m) * p.C + c))
+                                           : make_uint4(0, 0, 0, 0);
+            }
+        };
+        if constexpr (PL > 1) load_y(0);
         for (int n = s; n < steps; n += 2) {
             ok = mbar_wait_bounded(&raw_full[n & 3], static_cast<unsigned>(n >> 2) & 1u, kCopyWaitLimitNs);
             if (!ok) break;
@@ -836,6 +872,19 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
             if (!ok) break;
             piece.template store<3>(gsm + s * S::kG, 16384u, walk);
             hand_over(&full_g[s], lane);
+            if constexpr (PL > 1) {
+                const int i = n >> 1;
+                if (i > 0) ok = mbar_wait_bounded(&empty_y[0], static_cast<unsigned>(i - 1) & 1u, kCopyWaitLimitNs);
+                if (!ok) break;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float f[8];
+                    unpack8(yv[q], static_cast<T*>(nullptr), f);
+                    store_split8<PL>(ysm, 16384u, yrow, (yc >> 3) + q, f);
+                }
+                hand_over(full_y, lane);
+                load_y(i + 1);
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e)  // rows past the tile hold zeros
                 bs[e] += (piece.v[0][e] + piece.v[1][e]) + (piece.v[2][e] + piece.v[3][e]);
@@ -883,6 +932,7 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
                         tc::tma_load_3d(raws + (n & 1) * kRaw + h * 16384, &gmap, ch * 64 + h * 32, pixel(i), 0, &raw_full[f]);
                     mbar_arrive(&raw_full[f]);
                 }
+                if constexpr (PL > 1) continue;
                 const int ys = i & 1;
                 if (ok && i >= 2) ok = mbar_wait_bounded(&empty_y[ys], static_cast<unsigned>((i >> 1) - 1) & 1u, kCopyWaitLimitNs);
                 if (!ok) break;
@@ -896,7 +946,7 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
         const uint32_t lead = tc::lead_lane(), sums = tmem + 256u;
         ok = tc::warp_wait(full_w, 0u, kCopyWaitLimitNs);
         for (int i = 0; i < mine && ok; ++i) {
-            const int ys = i & 1, t = i % kFlushTiles;
+            const int ys = i % S::kYStages, t = i % kFlushTiles;
             // grad_y, as the chunks come
             if (i > 0) ok = tc::warp_wait(acc_empty, static_cast<unsigned>(i - 1) & 1u, kCopyWaitLimitNs);
             for (int ch = 0; ch < nch && ok; ++ch) {
@@ -910,15 +960,18 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
                 for (int k = 0; k < 4; ++k) {
                     if (k >= ksteps) break;
                     tc::mma_f16(tmem + (k % 3) * 64u, a + k * 2, b + k * 128, iy, ch > 0 || k >= 3, lead);
-                    tc::mma_f16(tmem + 192u, a + 1024 + k * 2, b + k * 128, iy, ch > 0 || k > 0, lead);
-                    tc::mma_f16(tmem + 192u, a + 2048 + k * 2, b + k * 128, iy, true, lead);
+#pragma unroll
+                    for (int q = 1; q < (PL == 1 ? 3 : 5); ++q) {  // (g's plane, W's): 1 0, 2 0, 0 1, 1 1
+                        const int gi = q < 3 ? q : q - 3, wi = q < 3 ? 0 : 1;
+                        tc::mma_f16(tmem + 192u, a + gi * 1024 + k * 2, b + wi * 1024 + k * 128, iy, ch > 0 || k > 0 || q > 1, lead);
+                    }
                 }
             }
             if (!ok) break;
             if (lead) tc::commit(acc_full);
             // grad_weight, both chunks (a single one stands in for the second, whose sums nobody reads)
             if (t == 0 && i > 0) ok = tc::warp_wait(sum_empty, static_cast<unsigned>(i / kFlushTiles - 1) & 1u, kCopyWaitLimitNs);
-            ok = ok && tc::warp_wait(&full_y[ys], static_cast<unsigned>(i >> 1) & 1u, kCopyWaitLimitNs);
+            ok = ok && tc::warp_wait(&full_y[ys], static_cast<unsigned>(i / S::kYStages) & 1u, kCopyWaitLimitNs);
             if (!ok) break;
             tc::fence_after();
             const int s0 = (i * nch) & 1;
@@ -927,8 +980,11 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
 #pragma unroll 1
             for (int k = 0; k < 8; ++k) {
                 tc::mma_f16(high, a + k * 128, b + k * 128, iw, t > 0 || k >= 3, lead);
-                tc::mma_f16(sums + 192u, a + 1024 + k * 128, b + k * 128, iw, t > 0 || k > 0, lead);
-                tc::mma_f16(sums + 192u, a + 2048 + k * 128, b + k * 128, iw, true, lead);
+#pragma unroll
+                for (int q = 1; q < (PL == 1 ? 3 : 5); ++q) {
+                    const int gi = q < 3 ? q : q - 3, yi = q < 3 ? 0 : 1;
+                    tc::mma_f16(sums + 192u, a + gi * 1024 + k * 128, b + yi * 1024 + k * 128, iw, t > 0 || k > 0 || q > 1, lead);
+                }
                 high = high == sums + 128 ? sums : high + 64;
             }
             if (lead) {
@@ -956,23 +1012,37 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
             ok = tc::bar_and(1, 128, mbar_wait_bounded(acc_full, static_cast<unsigned>(i) & 1u, kCopyWaitLimitNs));
             if (!ok) break;
             tc::fence_after();
-            for (int h = 0; h < 2 && h * 32 < p.C; ++h) {
-                // the store that read the staging tile has done so
-                if (et == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                tc::bar_sync(1, 128);
-                for (int cc = 0; cc < 2; ++cc) {
+            if constexpr (PL > 1) {
+                // no room for a staging tile: each lane writes its pixel's row
+                const int m = pixel(i) + row;
+                for (int c = 0; c < 64 && c < p.C; c += 16) {
                     float v[16];
-                    add4(lanes + h * 32 + cc * 16, high, v);
+                    add4(lanes + c, high, v);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        *reinterpret_cast<float4*>(outs + row * 128 + (((cc * 4 + q) ^ (row & 7)) << 4)) =
-                            make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                        if (m < p.M && c + q * 4 < p.C)
+                            *reinterpret_cast<float4*>(gy + static_cast<size_t>(m) * p.C + c + q * 4) =
+                                make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
                 }
-                fence_proxy_async();
-                tc::bar_sync(1, 128);
-                if (et == 0) {
-                    tc::tma_store_3d(&omap, h * 32, pixel(i), 0, outs);
-                    tc::bulk_commit();
+            } else {
+                for (int h = 0; h < 2 && h * 32 < p.C; ++h) {
+                    // the store that read the staging tile has done so
+                    if (et == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    tc::bar_sync(1, 128);
+                    for (int cc = 0; cc < 2; ++cc) {
+                        float v[16];
+                        add4(lanes + h * 32 + cc * 16, high, v);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            *reinterpret_cast<float4*>(outs + row * 128 + (((cc * 4 + q) ^ (row & 7)) << 4)) =
+                                make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                    }
+                    fence_proxy_async();
+                    tc::bar_sync(1, 128);
+                    if (et == 0) {
+                        tc::tma_store_3d(&omap, h * 32, pixel(i), 0, outs);
+                        tc::bulk_commit();
+                    }
                 }
             }
             tc::fence_before();

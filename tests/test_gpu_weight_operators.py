@@ -336,16 +336,17 @@ def test_predictor_backward_nan_stays_in_its_rows_and_channels(cuda_device):
     assert torch.isnan(gb).nonzero().flatten().tolist() == [ch]
 
 
-@pytest.mark.parametrize("G", [2, 4], ids=["one_chunk", "two_chunks"])
-def test_predictor_backward_in_one_pass_nan_and_far_apart_magnitudes(G, cuda_device):
-    """The kernel that reads the records' gradients once (bf16, few channels and slots): rows of 1e-30 to 1e30, then
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("G", [4, 8], ids=["one_chunk", "two_chunks"])
+def test_predictor_backward_in_one_pass_nan_and_far_apart_magnitudes(G, dtype, cuda_device):
+    """The kernel that reads the records' gradients once (few channels and slots): rows of 1e-30 to 1e30, then
     NaN and infinities, which stay in their rows, channels and slots."""
     M, C, K = 20100, 64, 2
     NO = 3 * G * K * K
     g = torch.Generator().manual_seed(G)
     gr = torch.randn(M, G, 3 * K * K, generator=g) * 10.0 ** (torch.rand(M, 1, 1, generator=g) * 60 - 30)
-    y = torch.randn(M, C, generator=g).bfloat16().to(cuda_device)
-    w = torch.randn(NO, C, generator=g).bfloat16().to(cuda_device)
+    y = torch.randn(M, C, generator=g).to(TD[dtype]).to(cuda_device)
+    w = torch.randn(NO, C, generator=g).to(TD[dtype]).to(cuda_device)
     gr = gr.to(cuda_device)
     _check_grads(dcn.predictor_backward(y, w, gr, G=G, K=K), y, w, gr, G, K * K, True)
     gr = torch.randn(M, G, 3 * K * K, generator=g).to(cuda_device)
