@@ -26,8 +26,8 @@
 // alone, without any work, reads g at 3.0 to 3.5 TB/s), and for three planes of
 // y the products themselves. Measured on B200, everything together: 200,704
 // pixels x 64 channels x 108 slots in bf16 41 us (71 by the two kernels), in
-// fp16 59 (87), replayed from a graph; 26,047 x 320 fp32 x 192 slots 101 us, 196 x 256 fp16 x 432 slots
-// 24 us.
+// fp16 59 (87), replayed from a graph; 26,047 x 320 fp32 x 192 slots 101 us,
+// 196 x 256 fp16 x 432 slots 21 us.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -48,6 +48,7 @@ struct PredBwdParams {
     int wrows, wpitch;   // rows and pitch of a plane of W in record order (multiples of 64)
     int groups;          // groups of 128 slots (grad_weight)
     int walkers;         // CTAs that share the pixel tiles of a (slice, group), each with partial sums of its own
+    int direct;          // one walker: its sums are the gradients, in the projection's row order
     int tma_out;         // grad_y by TMA
     int raws;            // grad_weight: raw tiles (0: direct reads)
     unsigned ystep;      // grad_weight: bytes between y's planes, 16 KB per block of 64 channels of a slice
@@ -61,6 +62,11 @@ constexpr uint64_t kFlushWaitLimitNs = 2 * kCopyWaitLimitNs;
 template <typename T>
 constexpr int split_planes() {
     return sizeof(T) == 4 ? 3 : std::is_same<T, __half>::value ? 2 : 1;
+}
+
+// Row of slot s's sums in a walker's part, or in the gradient itself.
+__device__ __forceinline__ size_t sum_row(const PredBwdParams& p, int walker, int s) {
+    return p.direct ? static_cast<size_t>(slot_channel(s, p.G, p.P)) : static_cast<size_t>(walker) * p.NO + s;
 }
 
 // Two fp32 values as bf16 pairs of falling order (a in the low half).
@@ -463,8 +469,8 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
 // that run along channels or slots: MN-major; the same threads sum g for the
 // bias. y in bf16 is its own plane and comes straight by TMA. Of warps 16..19,
 // one issues the products and a lane of another the TMA loads; every kFlushTiles
-// tiles all four read the accumulators out to part [walkers][NO][C], lanes
-// along the channels. A slice of at most 64 channels reads its one block of 64
+// tiles all four read the accumulators out to part [walkers][NO][C] (one walker:
+// to the gradient), lanes along the channels. A slice of at most 64 channels reads its one block of 64
 // for both halves of the M = 128 products.
 template <typename T, bool RAW>
 struct GradWShape {
@@ -638,7 +644,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
                 v += __shfl_xor_sync(0xffffffffu, v, 2);
                 v += __shfl_xor_sync(0xffffffffu, v, 4);
                 if (ok && part8 == 0 && s < ng * 8 && g0 + ch * 64 + s < p.NO)
-                    pbias[static_cast<size_t>(walker) * p.NO + g0 + ch * 64 + s] = v;
+                    pbias[sum_row(p, walker, g0 + ch * 64 + s)] = v;
             }
         }
     } else {
@@ -736,16 +742,25 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
                     for (int e = 0; e < 16; ++e) v[e] += w[e];
                 }
                 const int s = g0 + q * 16;
-                float* o = part + (static_cast<size_t>(walker) * p.NO + s) * p.C + c;
+                // rows in the gradient's order take divisions: one per lane, handed round
+                const int mapped = p.direct ? slot_channel(min(s + (lane & 15), p.NO - 1), p.G, p.P) : 0;
+                const size_t first = static_cast<size_t>(walker) * p.NO + s;
+                size_t at[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int m = __shfl_sync(0xffffffffu, mapped, e);
+                    at[e] = (p.direct ? static_cast<size_t>(m) : first + e) * p.C + c;
+                }
+                auto entry = [&](int e) -> float& { return part[at[e]]; };
                 if (f > 0) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e] = on && s + e < p.NO ? o[static_cast<size_t>(e) * p.C] : 0.f;
+                    for (int e = 0; e < 16; ++e) w[e] = on && s + e < p.NO ? entry(e) : 0.f;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[e] += w[e];
                 }
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    if (on && s + e < p.NO) o[static_cast<size_t>(e) * p.C] = v[e];
+                    if (on && s + e < p.NO) entry(e) = v[e];
             }
             tc::fence_before();
             tc::bar_sync(1, 128);
@@ -915,7 +930,7 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
                 v += __shfl_xor_sync(0xffffffffu, v, 2);
                 v += __shfl_xor_sync(0xffffffffu, v, 4);
                 if (ok && part8 == 0 && t < of.ng * 8 && ch * 64 + t < p.NO)
-                    pbias[static_cast<size_t>(walker) * p.NO + ch * 64 + t] = v;
+                    pbias[sum_row(p, walker, ch * 64 + t)] = v;
             }
         }
     } else if (warp == 16) {
@@ -1052,7 +1067,7 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
             ok = tc::bar_and(1, 128, mbar_wait_bounded(sum_full, static_cast<unsigned>(f) & 1u, kFlushWaitLimitNs));
             if (!ok) break;
             tc::fence_after();
-            float* o = part + (static_cast<size_t>(walker) * p.NO + row) * p.C;  // accumulator row = slot
+            float* o = part + (row < p.NO ? sum_row(p, walker, row) : 0u) * p.C;  // accumulator row = slot
             for (int q = 0; q < 4; ++q) {
                 float v[16];
                 add4(lanes + 256u + q * 16, 3, v);

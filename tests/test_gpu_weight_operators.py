@@ -251,6 +251,8 @@ BWD_CASES = [
     (305000, 16, 5, 2, False, True),
     (304001, 64, 4, 3, False, True),
     (610000, 33, 4, 3, False, True),   # (rows that TMA cannot take)
+    (2200, 1024, 44, 3, False, True),  # one CTA per part of the weight, two runs of tiles
+    (256, 256, 16, 3, False, True),
 ]
 
 
@@ -266,7 +268,8 @@ def test_predictor_backward(case, dtype, cuda_device):
     gr = torch.randn(M, G, 3 * P, generator=g) * torch.exp(3 * torch.randn(M, 1, 1, generator=g))
     gr[::5] = 0.0
     gy, uy = _guarded((M, C), torch.float32, cuda_device)
-    gw, uw = _guarded((NO, C), torch.float32, cuda_device)
+    # (a gradient that is not 16-byte aligned takes the way by partial sums)
+    gw, uw = _guarded((NO, C), torch.float32, cuda_device, shift=int(M in (129, 257)))
     gb, ub = _guarded((NO,), torch.float32, cuda_device)
     args = (y.to(cuda_device), w.to(cuda_device), gr.to(cuda_device))
     grads = dcn.predictor_backward(*args, G=G, K=K, remove_center=rc, with_bias=bias, grad_y=gy, grad_weight=gw,
