@@ -125,7 +125,7 @@ int launch_small(const void* x, void* out, int steps, const int* down, const dcn
     g.nb = (p.n + 63) / 64;
     g.n16 = (p.n + 15) / 16 * 16;
     g.m16 = (p.m + 15) / 16 * 16;
-    const unsigned cols = static_cast<unsigned>(std::max(4 * g.n16, 2 * std::min(256, g.m16)));
+    const unsigned cols = static_cast<unsigned>(4 * std::max(g.n16, std::min(128, g.m16)));
     g.tmem_cols = 32;
     while (g.tmem_cols < cols) g.tmem_cols <<= 1;
     for (int k = 0; k <= steps; ++k) g.down[k] = static_cast<short>(down[k]);

@@ -498,14 +498,14 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
     for (int s = 0; s < g.steps && ok; ++s) {
         const int now = max(0, sc.e - g.down[s]), next = max(0, sc.e - g.down[s + 1]);
         // accumulators of order 0 past the number of k steps hold nothing: left out of the sums
-        auto sums = [&](int cc, int ksteps, float (&v)[16]) {
+        auto sums = [&](int cc, int ksteps, int step, float (&v)[16]) {
             if (ksteps >= 3) {
-                ortho_sum4(lanes + cc * 16, g.n16, v);
+                ortho_sum4(lanes + cc * 16, step, v);
             } else {
                 float w[16];
-                tc::ld16(lanes + 3 * g.n16 + cc * 16, v);
+                tc::ld16(lanes + 3 * step + cc * 16, v);
                 for (int q = 0; q < ksteps; ++q) {
-                    tc::ld16(lanes + q * g.n16 + cc * 16, w);
+                    tc::ld16(lanes + q * step + cc * 16, w);
                     tc::wait_ld();
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[e] += w[e];
@@ -525,7 +525,7 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
         if (!ok) break;
         for (int cc = part; cc < nchunks; cc += 4) {
             float v[16];
-            sums(cc, g.m16 / 16, v);
+            sums(cc, g.m16 / 16, g.n16, v);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 __half hi[8], lo[8];
@@ -540,7 +540,7 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
         const float ub = scalbnf(p.b, -2 * now), uc = scalbnf(p.c, -4 * now) * (kOrthoSP / (kOrthoSA * kOrthoSA));
         for (int cc = part; cc < nchunks; cc += 4) {
             float v[16];
-            sums(cc, nchunks, v);
+            sums(cc, nchunks, g.n16, v);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 __half hi[8], lo[8];
@@ -556,31 +556,32 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
                 put_chunk(as, cc, h, hi, lo);
             }
         }
-        // X = P X, up to 256 columns at a time: hi hi in columns 0.., the cross terms 256 (or the group's width) on
+        // X = P X, up to 128 columns at a time, four accumulators as above `width` apart
         const bool last = s + 1 == g.steps;
-        for (int j0 = 0; j0 < g.m16 && ok; j0 += 256) {
-            const int width = min(256, g.m16 - j0);
+        for (int j0 = 0; j0 < g.m16 && ok; j0 += 128) {
+            const int width = min(128, g.m16 - j0);
             product([&](uint32_t lead) {
                 const uint32_t idesc = tc::idesc_f16(tc::kFmtF16, width, false, true);
                 uint32_t ah = tc::sw128(smem_addr(as)), bh = tc::sw128(smem_addr(xs) + (j0 >> 6) * kOrthoBlock, kOrthoBlock);
+                const uint32_t cross = tmem + 3 * width;
+                uint32_t high = tmem;
 #pragma unroll 1
                 for (int k = 0; k < nchunks; ++k, bh += 128) {
                     const uint32_t al = ah + 1024, bl = bh + 1024;
-                    tc::mma_f16(tmem + width, ah, bl, idesc, k > 0, lead);
-                    tc::mma_f16(tmem + width, al, bh, idesc, true, lead);
-                    tc::mma_f16(tmem, ah, bh, idesc, k > 0, lead);
+                    tc::mma_f16(cross, ah, bl, idesc, k > 0, lead);
+                    tc::mma_f16(cross, al, bh, idesc, true, lead);
+                    tc::mma_f16(high, ah, bh, idesc, k >= 3, lead);
+                    high = high == tmem + 2 * width ? tmem : high + width;
                     ah += (k & 3) == 3 ? kOrthoBlock / 16 - 6 : 2;
                 }
             });
             if (!ok) break;
             const float ux = scalbnf(1.f, (last ? 0 : next) - now) / (last ? kOrthoSP * kOrthoSX : kOrthoSP);
             for (int cc = part; cc < width / 16; cc += 4) {
-                float v[16], w[16];
-                tc::ld16(lanes + cc * 16, v);
-                tc::ld16(lanes + width + cc * 16, w);
-                tc::wait_ld();
+                float v[16];
+                sums(cc, nchunks, width, v);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = (v[e] + w[e]) * ux;
+                for (int e = 0; e < 16; ++e) v[e] *= ux;
                 if (last) {
                     // straight to `out`: a lane's 16 columns are neighbours (R <= C), or the lanes are (R > C)
                     T* o = out + static_cast<size_t>(mat) * count;
