@@ -149,7 +149,9 @@ int product(const CUtensorMap& l, const CUtensorMap& r, const CUtensorMap& o, co
     g.down_next = down[1];
     const unsigned tiles = static_cast<unsigned>(p.B) * g.tiles_i * g.tiles_j;
     const bool deep = tiles <= static_cast<unsigned>(nsm);
-    auto kern = deep ? dcnv4::ortho_product_kernel<MODE, T, 4> : dcnv4::ortho_product_kernel<MODE, T, 2>;
+    const bool runs = g.kblocks > dcnv4::kOrthoRun;
+    auto kern = deep ? (runs ? dcnv4::ortho_product_kernel<MODE, T, 4, true> : dcnv4::ortho_product_kernel<MODE, T, 4, false>)
+                     : (runs ? dcnv4::ortho_product_kernel<MODE, T, 2, true> : dcnv4::ortho_product_kernel<MODE, T, 2, false>);
     const unsigned smem = dcnv4::ortho_smem(deep ? 4 : 2);
     if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess) return DCNV4_ERR_LAUNCH;
     return launch_chained(kern, dim3(tiles), dcnv4::kOrthoThreads, smem, s, l, r, o, a, out, g, p);

@@ -13,8 +13,10 @@
 // plane exceeds 2^14): 22 bits of every entry down to about 2^-22 of the
 // bound. A matrix whose norm is far below eps starts with a small X: it is kept
 // lifted by 2^e (Y = 2^e X, |Y| <= 1), e going down by as many bits per step as
-// the step can grow X. A product is three tensor-core products, hi hi + hi lo + lo hi (lo lo
-// is below 2^-24 of it), each exact, summed in fp32. The tensor cores' fp32
+// the step can grow X. A product is three tensor-core products, hi hi + hi lo +
+// lo hi, each exact, summed in fp32 (lo lo is some 2^-24 of it, but in X X^T and
+// A A it adds up along the diagonal: small matrices, whose other errors are
+// least, take it as well: 1.09e-6 -> 0.86e-6 for 78 x 10). The tensor cores' fp32
 // additions truncate, so a long chain of them drifts one way: the hi hi terms
 // go to three accumulators in turn and the small cross terms to one of their
 // own, and the epilogue adds these with rounding.
@@ -208,9 +210,13 @@ __device__ __forceinline__ uint4 ortho_load(const __half* p) {
 // of tensor memory each) whose latencies overlap. Whole iteration in fp32, 432
 // x 256: 18 matrices (144 and 252 tiles) 120 us, all products with four stages
 // 132, with two 149; 40 matrices 243 with two, 289 with four. 4 of 864 x 512
-// in bf16: 149 us.
+// in bf16: 156 us (149 in one run of k).
 constexpr int kGram = 0, kPoly = 1, kApply = 2, kLast = 3;
 constexpr int kOrthoEpi = 256, kOrthoThreads = 64 + kOrthoEpi;
+// The accumulators are read out, added in registers and begun anew every this
+// many 64 k: without it the truncated additions of one matrix of 809 x 840
+// brought a relative error of 1.03e-5, fp32 matrix products 6.8e-6.
+constexpr int kOrthoRun = 8;
 constexpr unsigned kOrthoStageBytes = 2u * 16384u + 2u * 8192u;
 constexpr unsigned ortho_smem(int stages) { return 1024u + stages * kOrthoStageBytes + 128u; }
 
@@ -220,7 +226,8 @@ struct OrthoTiles {
     int down, down_next;   // bits the lift has gone down before and after this step
 };
 
-template <int MODE, typename T, int STAGES>
+// RUNS: more than one run.
+template <int MODE, typename T, int STAGES, bool RUNS>
 __global__ void __launch_bounds__(kOrthoThreads, STAGES == 2 ? 2 : 1)
 ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ CUtensorMap rmap,
                      const __grid_constant__ CUtensorMap omap, const __half* __restrict__ aplanes, T* __restrict__ out,
@@ -228,8 +235,8 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
     extern __shared__ unsigned char ortho_smem_raw[];
     unsigned char* sm = ortho_smem_raw + ((1024u - (smem_addr(ortho_smem_raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + STAGES * kOrthoStageBytes);
-    uint64_t *full = bars, *empty = bars + STAGES, *done = bars + 2 * STAGES;
-    uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
+    uint64_t *full = bars, *empty = bars + STAGES, *done = bars + 2 * STAGES, *drained = done + 1;
+    uint32_t* slot = reinterpret_cast<uint32_t*>(drained + 1);
     const int tid = threadIdx.x, warp = static_cast<int>(tc::uniform(threadIdx.x >> 5)), lane = tid & 31;
     const unsigned per = static_cast<unsigned>(g.tiles_i) * g.tiles_j;
     const int mat = static_cast<int>(blockIdx.x / per);
@@ -242,6 +249,7 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
             mbar_init(&empty[s], 1);
         }
         mbar_init(done, 1);
+        mbar_init(drained, kOrthoEpi);
         fence_barrier_init();
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&lmap)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&rmap)) : "memory");
@@ -281,7 +289,9 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
         const uint32_t lead = tc::lead_lane();
         for (int kb = 0; kb < g.kblocks; ++kb) {
             const int s = kb % STAGES;
+            const int t = RUNS ? kb % kOrthoRun : kb;
             ok = tc::warp_wait(&full[s], static_cast<unsigned>(kb / STAGES) & 1u, kCopyWaitLimitNs);
+            if (RUNS && t == 0 && kb > 0) ok = ok && tc::warp_wait(drained, static_cast<unsigned>(kb / kOrthoRun - 1) & 1u, kCopyWaitLimitNs);
             if (!ok) break;
             tc::fence_after();
             const unsigned base = smem_addr(sm + s * kOrthoStageBytes);
@@ -289,11 +299,14 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint32_t ah = a + k * 2, al = ah + 1024, bh = b + k * (mn ? 128 : 2), bl = bh + 512;
-                tc::mma_f16(tmem + 192u, ah, bl, idesc, kb > 0 || k > 0, lead);
+                tc::mma_f16(tmem + 192u, ah, bl, idesc, t > 0 || k > 0, lead);
                 tc::mma_f16(tmem + 192u, al, bh, idesc, true, lead);
-                tc::mma_f16(tmem + (k % 3) * 64u, ah, bh, idesc, kb > 0 || k >= 3, lead);
+                tc::mma_f16(tmem + (k % 3) * 64u, ah, bh, idesc, t > 0 || k >= 3, lead);
             }
-            if (lead) tc::commit(&empty[s]);
+            if (lead) {
+                tc::commit(&empty[s]);
+                if (RUNS && t == kOrthoRun - 1 && kb + 1 < g.kblocks) tc::commit(done);
+            }
         }
         if (ok && lead) tc::commit(done);
     } else {
@@ -319,16 +332,42 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
         // powers of two that undo the lift (A carries it twice, A A four times)
         const float ux = scalbnf(1.f, (MODE == kLast ? 0 : next) - now);
         const float ub = MODE == kPoly ? scalbnf(p.b, -2 * now) : 0.f, uc = MODE == kPoly ? scalbnf(p.c, -4 * now) : 0.f;
-        ok = tc::bar_and(1, kOrthoEpi, mbar_wait_bounded(done, 0u, kCopyWaitLimitNs));  // one decision for all the warps
+        const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 32;
+        float sum[2][16];  // the runs before the last
+        unsigned r = 0;
+        if constexpr (RUNS) {
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) sum[cc][e] = 0.f;
+            for (; static_cast<int>(r + 1) * kOrthoRun < g.kblocks; ++r) {
+                ok = tc::bar_and(1, kOrthoEpi, mbar_wait_bounded(done, r & 1u, kCopyWaitLimitNs));
+                if (!ok) break;
+                tc::fence_after();
+#pragma unroll
+                for (int cc = 0; cc < 2; ++cc) {
+                    float v[16];
+                    ortho_sum4(at + cc * 16, 64u, v);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) sum[cc][e] += v[e];
+                }
+                tc::fence_before();
+                mbar_arrive(drained);
+            }
+        }
+        // one decision for all the warps
+        ok = tc::bar_and(1, kOrthoEpi, ok && mbar_wait_bounded(done, r & 1u, kCopyWaitLimitNs));
         if (ok) {
             tc::fence_after();
-            const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 32;
             float* fres = reinterpret_cast<float*>(sm);
             uint4 *hp = reinterpret_cast<uint4*>(sm + row * 128), *lp = reinterpret_cast<uint4*>(sm + 16384 + row * 128);
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) {
                 float v[16];
                 ortho_sum4(at + cc * 16, 64u, v);
+                if constexpr (RUNS)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] += sum[cc][e];
                 if constexpr (MODE == kLast) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
@@ -401,8 +440,8 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
 // overwrites them with P. One warp issues a product's instructions, then all
 // warps turn the accumulators into the next operand. What bounds it is the
 // chain of 3 * steps dependent products, each a few hundred cycles of tensor
-// work between two barriers: 4 matrices of 108 x 64 take 28 us (67 through the
-// kernels above), 18 of 216 x 128 64 us (85), 300 of 108 x 64 83 us (161).
+// work between two barriers: 4 matrices of 108 x 64 take 30 us (67 through the
+// kernels above), 18 of 216 x 128 72 us (85), 300 of 108 x 64 90 us (161).
 constexpr int kOrthoSmallThreads = 512, kOrthoSmallBlocks = 7;
 constexpr unsigned kOrthoBlock = 2u * 16384u;
 constexpr int kOrthoMaxSteps = 64;
@@ -489,6 +528,7 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
             const uint32_t l = h + 1024;
             tc::mma_f16(cross, h, l, idesc, k > 0, lead);
             tc::mma_f16(cross, l, h, idesc, true, lead);
+            tc::mma_f16(cross, l, l, idesc, true, lead);
             tc::mma_f16(high, h, h, idesc, k >= 3, lead);
             high = high == tmem + 2 * g.n16 ? tmem : high + g.n16;
             h += (k & 3) == 3 ? kOrthoBlock / 16 - 6 : 2;  // 16 k further, or the next block of 64
