@@ -309,7 +309,7 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             }
             const ChunkWalk& walk = chunk + 1 < p.chunks ? whole : tail;
             if constexpr (RAW) {
-                ok = mbar_wait_bounded(&raw_full[it & 3], static_cast<unsigned>(it >> 2) & 1u, kCopyWaitLimitNs);
+                ok = tc::warp_wait(&raw_full[it & 3], static_cast<unsigned>(it >> 2) & 1u, kCopyWaitLimitNs);
                 if (!ok) break;
                 piece.from_raw(raws + (it % S::kRaws) * kRaw, walk);
                 piece.landed();
@@ -318,7 +318,7 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 const long long item = blockIdx.x + n * gridDim.x;
                 piece.from_global(grec, walk, item / p.slices * 128, p.M, chunk * 64, p.NO);
             }
-            if (it >= 2) ok = mbar_wait_bounded(&empty[s], static_cast<unsigned>((it >> 1) - 1) & 1u, kCopyWaitLimitNs);
+            if (it >= 2) ok = tc::warp_wait(&empty[s], static_cast<unsigned>((it >> 1) - 1) & 1u, kCopyWaitLimitNs);
             if (!ok) break;
             piece.template store<3>(sm + s * S::kStage, 16384u, walk);
             hand_over(&full_g[s], lane);
@@ -555,7 +555,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
             place = place == raws + (p.raws - 1) * kRaw ? raws : place + kRaw;
         };
         auto take = [&](auto& piece, const ChunkWalk& walk) {
-            ok = mbar_wait_bounded(&raw_full[k & 3], static_cast<unsigned>(k >> 2) & 1u, kCopyWaitLimitNs);
+            ok = tc::warp_wait(&raw_full[k & 3], static_cast<unsigned>(k >> 2) & 1u, kCopyWaitLimitNs);
             if (!ok) return;
             piece.from_raw(place, walk);
             piece.landed();
@@ -568,7 +568,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
             bool freed = i == 0;
             auto y_freed = [&] {
                 if constexpr (!S::kDirectY && S::kYStages == 1) {
-                    if (!freed) ok = ok && mbar_wait_bounded(&empty_y[0], static_cast<unsigned>(i - 1) & 1u, kCopyWaitLimitNs);
+                    if (!freed) ok = ok && tc::warp_wait(&empty_y[0], static_cast<unsigned>(i - 1) & 1u, kCopyWaitLimitNs);
                     freed = true;
                 }
             };
@@ -584,7 +584,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
                         else piece.from_global(y, walk, pixel(i), p.M, c0 + b * 64, p.C);
                         y_freed();
                         if (S::kYStages > 1 && yn > 0)
-                            ok = ok && mbar_wait_bounded(&empty_y[ys], static_cast<unsigned>(yn - 1) & 1u, kCopyWaitLimitNs);
+                            ok = ok && tc::warp_wait(&empty_y[ys], static_cast<unsigned>(yn - 1) & 1u, kCopyWaitLimitNs);
                         if (!ok) break;
                         piece.template store<YP>(sm + ys * ystage + b * 16384, p.ystep, walk);
                         hand_over(&full_y[ys], lane);
@@ -602,7 +602,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
                     if constexpr (RAW) take(piece, walk);
                     else piece.from_global(grec, walk, pixel(i), p.M, g0 + ch * 64, p.NO);
                     y_freed();
-                    if (n >= 2) ok = ok && mbar_wait_bounded(&empty_g[s], static_cast<unsigned>((n >> 1) - 1) & 1u, kCopyWaitLimitNs);
+                    if (n >= 2) ok = ok && tc::warp_wait(&empty_g[s], static_cast<unsigned>((n >> 1) - 1) & 1u, kCopyWaitLimitNs);
                     if (!ok) break;
                     piece.template store<3>(gsm + s * S::kG, 16384u, walk);
                     hand_over(&full_g[s], lane);
@@ -620,7 +620,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
             const int last = mine * nch;
             if (ok && last > 0) {
                 const int s = (last - 1) & 1;
-                ok = mbar_wait_bounded(&empty_g[s], static_cast<unsigned>((last - 1) >> 1) & 1u, kCopyWaitLimitNs);
+                ok = tc::warp_wait(&empty_g[s], static_cast<unsigned>((last - 1) >> 1) & 1u, kCopyWaitLimitNs);
             }
             float* red = reinterpret_cast<float*>(gsm);  // [thread][8], one chunk at a time
 #pragma unroll
@@ -877,19 +877,19 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
         };
         if constexpr (PL > 1) load_y(0);
         for (int n = s; n < steps; n += 2) {
-            ok = mbar_wait_bounded(&raw_full[n & 3], static_cast<unsigned>(n >> 2) & 1u, kCopyWaitLimitNs);
+            ok = tc::warp_wait(&raw_full[n & 3], static_cast<unsigned>(n >> 2) & 1u, kCopyWaitLimitNs);
             if (!ok) break;
             Piece<float> piece;
             piece.from_raw(raws + s * kRaw, walk);
             piece.landed();
             if (lane == 0) mbar_arrive(&raw_empty[n & 3]);
-            if (n >= 2) ok = mbar_wait_bounded(&empty_g[s], static_cast<unsigned>((n >> 1) - 1) & 1u, kCopyWaitLimitNs);
+            if (n >= 2) ok = tc::warp_wait(&empty_g[s], static_cast<unsigned>((n >> 1) - 1) & 1u, kCopyWaitLimitNs);
             if (!ok) break;
             piece.template store<3>(gsm + s * S::kG, 16384u, walk);
             hand_over(&full_g[s], lane);
             if constexpr (PL > 1) {
                 const int i = n >> 1;
-                if (i > 0) ok = mbar_wait_bounded(&empty_y[0], static_cast<unsigned>(i - 1) & 1u, kCopyWaitLimitNs);
+                if (i > 0) ok = tc::warp_wait(&empty_y[0], static_cast<unsigned>(i - 1) & 1u, kCopyWaitLimitNs);
                 if (!ok) break;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -908,7 +908,7 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
             // once the last products have read the operand tiles (a commit covers all those before it), the
             // threads' sums are added there, a slot's in the order of its rows' pieces
             const int end = (steps - 1) & 1;
-            if (ok) ok = mbar_wait_bounded(&empty_g[end], static_cast<unsigned>((steps - 1) >> 1) & 1u, kCopyWaitLimitNs);
+            if (ok) ok = tc::warp_wait(&empty_g[end], static_cast<unsigned>((steps - 1) >> 1) & 1u, kCopyWaitLimitNs);
             float* red = reinterpret_cast<float*>(gsm);  // [thread][8]
             tc::bar_sync(2, kConv);
             if (ok)

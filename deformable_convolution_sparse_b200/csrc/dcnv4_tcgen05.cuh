@@ -65,7 +65,8 @@ __device__ __forceinline__ uint32_t lead_lane() {
     return r;
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
-// a bounded wait of a whole warp, with one answer
+// A bounded wait of a whole warp, with one answer. Where a warp's lanes go on to a vote, a __syncwarp or a
+// barrier, a lane that gave up by itself would leave the others waiting there for it without a limit.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, uint64_t limit_ns) {
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit_ns)) != 0;
 }
