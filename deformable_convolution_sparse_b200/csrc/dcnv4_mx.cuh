@@ -480,7 +480,12 @@ predictor_mx_kernel(const __grid_constant__ CUtensorMap rmap, const T* __restric
         }
         // one warp polls; the others wait at the barrier, where they take no issue slots
         ok = __syncthreads_and(warp != 0 || mbar_wait_bounded(done, static_cast<unsigned>(it) & 1u, kCopyWaitLimitNs)) != 0;
-        if (!ok) break;
+        if (!ok) {
+            // given up: the copies and products in flight are waited for, again with a limit, before the CTA leaves
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            if (warp == 0) mbar_wait_bounded(done, static_cast<unsigned>(it) & 1u, kCopyWaitLimitNs);
+            break;
+        }
         tc::fence_after();
 
         // accumulator row = pixel: lane 32 * (warp % 4) + lane; 16-column chunks shared out among a quarter's warps

@@ -236,7 +236,8 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
     unsigned char* sm = ortho_smem_raw + ((1024u - (smem_addr(ortho_smem_raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + STAGES * kOrthoStageBytes);
     uint64_t *full = bars, *empty = bars + STAGES, *done = bars + 2 * STAGES, *drained = done + 1;
-    uint32_t* slot = reinterpret_cast<uint32_t*>(drained + 1);
+    uint64_t* drain = drained + 1;
+    uint32_t* slot = reinterpret_cast<uint32_t*>(drain + 1);
     const int tid = threadIdx.x, warp = static_cast<int>(tc::uniform(threadIdx.x >> 5)), lane = tid & 31;
     const unsigned per = static_cast<unsigned>(g.tiles_i) * g.tiles_j;
     const int mat = static_cast<int>(blockIdx.x / per);
@@ -250,6 +251,7 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
         }
         mbar_init(done, 1);
         mbar_init(drained, kOrthoEpi);
+        mbar_init(drain, 1);
         fence_barrier_init();
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&lmap)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&rmap)) : "memory");
@@ -263,6 +265,7 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     bool ok = true;
+    int loads = 0;  // the loading lane's steps so far
 
     if (warp == 0) {
         if (lane == 0) {
@@ -281,6 +284,7 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
                         tc::tma_load_3d(st + 32768 + pl * 8192, &rmap, kb * 64, j0, pl * p.B + mat, &full[s]);
                 }
                 mbar_arrive(&full[s]);
+                loads = kb + 1;
             }
         }
     } else if (warp == 1) {
@@ -426,7 +430,11 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
     }
     if (!ok) atomicOr(p.status, kStatusCopyTimeout);
     tc::fence_before();
-    __syncthreads();
+    if (!__syncthreads_and(ok)) {
+        if (warp == 0 && lane == 0) tc::drain_loads<STAGES>(full, loads, STAGES);
+        if (warp == 1) tc::drain_products(drain);
+        __syncthreads();
+    }
     tc::fence_after();
     if (warp == 0) tc::dealloc(tmem, 256u);
 }
@@ -515,6 +523,8 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
             if (lead) tc::commit(&done_bar);
         }
         ok = __syncthreads_and(mbar_wait_bounded(&done_bar, phase & 1u, kCopyWaitLimitNs)) != 0;
+        // given up: the products in flight are waited for once more before the CTA leaves
+        if (!ok) mbar_wait_bounded(&done_bar, phase & 1u, kCopyWaitLimitNs);
         ++phase;
         tc::fence_after();
     };

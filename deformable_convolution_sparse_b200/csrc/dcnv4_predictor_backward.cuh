@@ -266,6 +266,7 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     uint64_t *full_g = bars, *full_w = bars + 2, *empty = bars + 4, *acc_full = bars + 6, *acc_empty = bars + 8,
              *raw_full = bars + 10, *raw_empty = bars + 14;  // of step it: the (it mod 4)-th
     uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 18);
+    uint64_t* drain = bars + 19;
     const int tid = threadIdx.x, warp = static_cast<int>(tc::uniform(threadIdx.x >> 5)), lane = tid & 31;
 
     if (tid == 0) {
@@ -280,6 +281,7 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             mbar_init(&raw_full[s], 1);
             mbar_init(&raw_empty[s], kGroup / 32);
         }
+        mbar_init(drain, 1);
         fence_barrier_init();
     }
     if (warp == 16) tc::alloc(slot, 512u);
@@ -295,6 +297,7 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     const long long mine = blockIdx.x < items ? (items - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
     const long long steps = mine * p.chunks;
     bool ok = true;
+    long long raw_n = 0, w_n = 0;  // the loading lane's steps so far
 
     if (warp < 16) {
         const ChunkWalk whole(64, tid), tail(p.NO - (p.chunks - 1) * 64, tid);
@@ -347,6 +350,7 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 mbar_expect_tx(&raw_full[f], halves * 16384u);
                 for (int h = 0; h < halves; ++h) tc::tma_load_3d(raws + r * kRaw + h * 16384, &gmap, s0 + h * 32, m0, 0, &raw_full[f]);
                 mbar_arrive(&raw_full[f]);
+                raw_n = it + 1;
             };
             for (int k = 0; k < S::kRaws; ++k) load_raw(k);
             for (long long it = 0; it < steps && ok; ++it) {
@@ -361,6 +365,7 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                     for (int b = 0; b < CT / 64; ++b)
                         tc::tma_load_3d(w + (pl * (CT / 64) + b) * 8192, &wmap, c0 + b * 64, s0, pl, &full_w[s]);
                 mbar_arrive(&full_w[s]);
+                w_n = it + 1;
                 load_raw(it + S::kRaws);
             }
         }
@@ -458,7 +463,14 @@ pred_grad_y_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     }
     if (!ok) atomicOr(p.status, kStatusCopyTimeout);
     tc::fence_before();
-    __syncthreads();
+    if (!__syncthreads_and(ok)) {
+        if (warp == 16 && lane == 0) {
+            tc::drain_loads<4>(raw_full, raw_n, S::kRaws);
+            tc::drain_loads<2>(full_w, w_n, 2);
+        }
+        if (warp == 17) tc::drain_products(drain);
+        __syncthreads();
+    }
     tc::fence_after();
     if (warp == 16) tc::dealloc(tmem, 512u);
 }
@@ -503,6 +515,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
     uint64_t *full_y = bars, *empty_y = bars + 2, *full_g = bars + 4, *empty_g = bars + 6, *acc_full = bars + 8,
              *raw_full = bars + 9, *raw_empty = bars + 13;  // of raw tile k: the (k mod 4)-th
     uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 17);
+    uint64_t* drain = bars + 18;
     const int tid = threadIdx.x, warp = static_cast<int>(tc::uniform(threadIdx.x >> 5)), lane = tid & 31;
 
     // CTA -> walker, (slice, group); the slices and groups of one walker side by side
@@ -527,6 +540,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
             mbar_init(&raw_empty[s], kGroup / 32);
         }
         mbar_init(acc_full, 1);
+        mbar_init(drain, 1);
         fence_barrier_init();
     }
     if (warp == 16) tc::alloc(slot, 512u);
@@ -539,6 +553,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
     // its end, so that whatever waits for this kernel has grad_y as well.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     bool ok = true;
+    int raw_n = 0, y_n = 0;  // the loading lane's raw tiles and tiles of y so far
 
     if (warp < 16) {
         const bool sums = c0 == 0 && pbias != nullptr;
@@ -654,7 +669,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
         const unsigned second = wide ? 16384u : 0u;
         const int quarter = warp & 3, row = quarter * 32 + lane, c = c0 + row;
         const bool on = c < p.C && (wide || row < 64);
-        int raw_n = 0, r = 0;
+        int r = 0;
         auto load_raw = [&](const CUtensorMap* map, int col, int step, int blocks, long long m0) {
             const int f = raw_n & 3, before = raw_n - p.raws;
             if (before >= 0)
@@ -680,6 +695,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
                         for (int b = 0; b < ny; ++b)
                             tc::tma_load_3d(sm + ys * ystage + b * 16384, &ymap, c0 + b * 64, static_cast<int>(m0), 0, &full_y[ys]);
                         mbar_arrive(&full_y[ys]);
+                        y_n = i + 1;
                     } else {
                         for (int b = 0; b < ny && ok; ++b) {
                             const int col = c0 + b * 64;
@@ -768,7 +784,14 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
     }
     if (!ok) atomicOr(p.status, kStatusCopyTimeout);
     tc::fence_before();
-    __syncthreads();
+    if (!__syncthreads_and(ok)) {
+        if (warp == 17 && lane == 0) {
+            tc::drain_loads<4>(raw_full, raw_n, p.raws);
+            tc::drain_loads<2>(full_y, y_n, 2);
+        }
+        if (warp == 16) tc::drain_products(drain);
+        __syncthreads();
+    }
     tc::fence_after();
     if (warp == 16) tc::dealloc(tmem, 512u);
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -811,6 +834,7 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
              *raw_empty = bars + 12, *full_w = bars + 16, *acc_full = bars + 17, *acc_empty = bars + 18,
              *sum_full = bars + 19, *sum_empty = bars + 20;  // raw tiles: step n's the (n mod 4)-th
     uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 21);
+    uint64_t* drain = bars + 22;
     const int tid = threadIdx.x, warp = static_cast<int>(tc::uniform(threadIdx.x >> 5)), lane = tid & 31;
     const int walker = static_cast<int>(blockIdx.x), nch = (p.NO + 63) / 64;
     const int mine = (p.tiles - walker + p.walkers - 1) / p.walkers, steps = mine * nch;
@@ -832,6 +856,7 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
         mbar_init(acc_empty, 128);
         mbar_init(sum_full, 1);
         mbar_init(sum_empty, 128);
+        mbar_init(drain, 1);
         fence_barrier_init();
     }
     if (warp == 16) tc::alloc(slot, 512u);
@@ -842,6 +867,7 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     bool ok = true;
+    int raw_n = 0, y_n = 0;  // the loading lane's raw tiles and tiles of y so far
 
     if (warp < 16) {
         // W's rows in record order, zeros past its end: row = slot, 16-byte chunk j at j ^ (row mod 8)
@@ -946,6 +972,7 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
                     for (int h = 0; h < halves; ++h)
                         tc::tma_load_3d(raws + (n & 1) * kRaw + h * 16384, &gmap, ch * 64 + h * 32, pixel(i), 0, &raw_full[f]);
                     mbar_arrive(&raw_full[f]);
+                    raw_n = n + 1;
                 }
                 if constexpr (PL > 1) continue;
                 const int ys = i & 1;
@@ -954,6 +981,7 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
                 mbar_expect_tx(&full_y[ys], S::kY);
                 tc::tma_load_3d(ysm + ys * S::kY, &ymap, 0, pixel(i), 0, &full_y[ys]);
                 mbar_arrive(&full_y[ys]);
+                y_n = i + 1;
             }
         }
     } else if (warp == 17) {
@@ -1090,7 +1118,14 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
     }
     if (!ok) atomicOr(p.status, kStatusCopyTimeout);
     tc::fence_before();
-    __syncthreads();
+    if (!__syncthreads_and(ok)) {
+        if (warp == 16 && lane == 0) {
+            tc::drain_loads<4>(raw_full, raw_n, S::kRaws);
+            tc::drain_loads<2>(full_y, y_n, 2);
+        }
+        if (warp == 17) tc::drain_products(drain);
+        __syncthreads();
+    }
     tc::fence_after();
     if (warp == 16) tc::dealloc(tmem, 512u);
 }

@@ -88,6 +88,21 @@ __device__ __forceinline__ void dealloc(uint32_t base, uint32_t cols) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
 }
 
+// After a wait has given up, before the kernel leaves: what is still in flight is waited for, again with a limit,
+// so that nothing lands in shared or tensor memory that is no longer this CTA's. The lane that loads: the last
+// `depth` of `issued` steps, step k announced on full[k mod N]. The warp that issues products: all of them (the
+// same lane is elected every time); `bar` is a barrier of one arrival for this alone.
+template <int N>
+__device__ __forceinline__ void drain_loads(uint64_t* full, long long issued, int depth) {
+    for (long long k = issued > depth ? issued - depth : 0; k < issued; ++k)
+        mbar_wait_bounded(&full[k % N], static_cast<unsigned>(k / N) & 1u, kCopyWaitLimitNs);
+}
+__device__ __forceinline__ void drain_products(uint64_t* bar) {
+    if (lead_lane()) commit(bar);
+    __syncwarp();
+    warp_wait(bar, 0u, kCopyWaitLimitNs);
+}
+
 // 16 consecutive fp32 columns of this thread's lane; valid after wait_ld()
 __device__ __forceinline__ void ld16(uint32_t taddr, float (&v)[16]) {
     asm volatile(

@@ -50,3 +50,30 @@ def test_converting_warps_give_up_as_a_whole():
         assert "mbar_wait_bounded" not in branch, name
         assert "tc::warp_wait(" in branch and "hand_over(" in branch, name
     assert seen == 3
+
+
+@pytest.mark.parametrize("file", FILES)
+def test_a_kernel_that_gives_up_leaves_nothing_in_flight(file):
+    """A kernel whose wait gave up waits once more, again with a limit, for the loads and products it has in flight
+    before it frees its tensor memory and leaves: they would land in memory that is no longer its own."""
+    seen = 0
+    for name, body in _kernels(file):
+        if "tc::alloc(" not in body:
+            continue
+        seen += 1
+        if "tc::tma_load_3d(" in body:
+            gave_up = _block(body, body.index("if (!__syncthreads_and(ok)) {"))
+            assert "tc::drain_loads<" in gave_up and "tc::drain_products(drain)" in gave_up, name
+            assert body.index("mbar_init(drain, 1)") < body.index("griddepcontrol"), name
+            # every ring of loads is among them
+            for bar in set(re.findall(r"tc::tma_load_3d\([^;]*&(\w+)\[", body)):
+                assert f"({bar}, " in gave_up, (name, bar)
+        else:
+            # products only, one batch at a time: the same barrier is waited for again
+            done = re.search(r"mbar_wait_bounded\(&?(done\w*)", body).group(1)
+            gave_up = body[body.index("if (!ok)"):]
+            assert len(re.findall(rf"mbar_wait_bounded\(&?{done}\b", body)) == 2, name
+            assert re.search(rf"mbar_wait_bounded\(&?{done}\b", gave_up), name
+            if "cp.async.cg" in body:
+                assert "cp.async.wait_all" in _block(body, body.index("if (!ok)")), name
+    assert seen > 0
