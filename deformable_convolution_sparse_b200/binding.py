@@ -568,8 +568,9 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients: tuple = (3.4445
     the transpose when R > C): the update the Muon optimiser forms from a
     weight's momentum. Returns the same shape and dtype; the iterates carry
     fp32 precision whatever the dtype. Coefficients whose iteration could
-    leave its bounds are refused. Asynchronous on ``stream`` (default: the
-    current stream).
+    leave its bounds, or lets small singular values fall far behind the
+    others, are refused. Asynchronous on ``stream`` (default: the current
+    stream).
     """
     _check_tensor(x, "x")
     if x.dim() < 2:

@@ -263,7 +263,7 @@ const char* dcnv4_strerror(int status) {
         case DCNV4_ERR_STAGING: return "one image does not fit half of the static staging area";
         case DCNV4_ERR_FLAGS: return "unknown variant flag";
         case DCNV4_ERR_WORKSPACE: return "the workspace is too small";
-        case DCNV4_ERR_COEFFICIENTS: return "coefficients or eps not finite, eps not positive, or an unbounded iteration";
+        case DCNV4_ERR_COEFFICIENTS: return "coefficients or eps not finite, eps not positive, or an iteration that leaves its range";
         default: return "unknown status";
     }
 }

@@ -50,24 +50,37 @@ double poly_bound(double a, double b, double c, double r) {
     return best;
 }
 
-// The iteration stays bounded: singular values start in [0, 1]; no step may
-// lift one above 4, nor the factor |a + b s^2 + c s^4| above 64. down[k]: bits
-// by which the steps before k can have grown a matrix (the factor's bound,
-// rounded up to a power of two).
-bool coefficients_bounded(double a, double b, double c, int steps, int* down) {
-    double r = 1.0;
-    down[0] = 0;
-    for (int k = 0; k < steps; ++k) {
+// Bounds of the iteration, and the powers of two that keep its planes in range
+// (dcnv4::OrthoStep). Singular values start in [0, 1]; r bounds them before
+// step k, grown the product of the steps' largest factors |a + b s^2 + c s^4|
+// (what a matrix far smaller than 1 can have grown by). False: a step may lift
+// a singular value above 4 or its factor above 64; or small singular values,
+// whose factor is a, may fall to less than 1/16 of either bound, out of the
+// range in which the planes hold them.
+bool iteration_bounds(double a, double b, double c, int steps, dcnv4::OrthoStep* step) {
+    // held to what ldexp and the kernels' exponents take; a matrix of 2^-700 is 0 in fp32 whatever its planes hold
+    auto log2_floor = [](double v) { return v > 0.0 ? std::clamp(std::ilogb(v), -700, 700) : -700; };
+    auto log2_ceil = [&](double v) { return log2_floor(v) + (v > std::ldexp(1.0, log2_floor(v)) ? 1 : 0); };
+    double r = 1.0, grown = 1.0, linear = 1.0;
+    for (int k = 0;; ++k) {
+        step[k].low = log2_floor(4.0 / std::max(r, 1e-300));
+        step[k].down = log2_ceil(grown);
+        step[k].up = 0;
+        if (k > 0) {
+            // the change of a step is a float's factor; a lift below the largest is as safe
+            step[k].low = std::min(step[k].low, step[k - 1].low + 120);
+            step[k].down = std::max(step[k].down, step[k - 1].down - 120);
+        }
+        if (k == steps) return true;
         double q = std::max(std::fabs(a), std::fabs(a + b * r * r + c * r * r * r * r));
         if (c != 0.0 && -b / (2.0 * c) > 0.0 && -b / (2.0 * c) < r * r) q = std::max(q, std::fabs(a - b * b / (4.0 * c)));
         if (!(q <= 64.0)) return false;
-        int bits = 0;
-        while ((1 << bits) < q) ++bits;
-        down[k + 1] = down[k] + bits;
+        if (q > 0.0) step[k].up = log2_floor(64.0 / q);  // (0: P is zero)
         r = poly_bound(a, b, c, r);
-        if (!(r <= 4.0)) return false;
+        grown *= q;
+        linear *= std::fabs(a);
+        if (!(r <= 4.0) || !(std::max(r, grown) <= 16.0 * linear)) return false;
     }
-    return true;
 }
 
 dcnv4::OrthoParams make_params(int B, int R, int C) {
@@ -118,7 +131,7 @@ bool fits_one_cta(const dcnv4::OrthoParams& p) {
 }
 
 template <typename T>
-int launch_small(const void* x, void* out, int steps, const int* down, const dcnv4::OrthoParams& p, cudaStream_t s) {
+int launch_small(const void* x, void* out, int steps, const dcnv4::OrthoStep* step, const dcnv4::OrthoParams& p, cudaStream_t s) {
     dcnv4::OrthoSmall g{};
     g.steps = steps;
     g.xb = (p.m + 63) / 64;
@@ -128,7 +141,7 @@ int launch_small(const void* x, void* out, int steps, const int* down, const dcn
     const unsigned cols = static_cast<unsigned>(4 * std::max(g.n16, std::min(128, g.m16)));
     g.tmem_cols = 32;
     while (g.tmem_cols < cols) g.tmem_cols <<= 1;
-    for (int k = 0; k <= steps; ++k) g.down[k] = static_cast<short>(down[k]);
+    std::copy(step, step + steps + 1, g.step);
     const unsigned smem = 1024u + static_cast<unsigned>(g.xb + g.nb) * dcnv4::kOrthoBlock;
     auto kern = dcnv4::ortho_small_kernel<T>;
     constexpr unsigned most = 1024u + dcnv4::kOrthoSmallBlocks * dcnv4::kOrthoBlock;
@@ -140,13 +153,13 @@ int launch_small(const void* x, void* out, int steps, const int* down, const dcn
 
 template <int MODE, typename T>
 int product(const CUtensorMap& l, const CUtensorMap& r, const CUtensorMap& o, const __half* a, T* out, int cols, int k,
-            const int* down, int nsm, const dcnv4::OrthoParams& p, cudaStream_t s) {
+            const dcnv4::OrthoStep* step, int nsm, const dcnv4::OrthoParams& p, cudaStream_t s) {
     dcnv4::OrthoTiles g{};
     g.tiles_i = (p.n + 127) / 128;
     g.tiles_j = (cols + 63) / 64;
     g.kblocks = (k + 63) / 64;
-    g.down = down[0];
-    g.down_next = down[1];
+    g.now = step[0];
+    g.next = step[1];
     const unsigned tiles = static_cast<unsigned>(p.B) * g.tiles_i * g.tiles_j;
     const bool deep = tiles <= static_cast<unsigned>(nsm);
     const bool runs = g.kblocks > dcnv4::kOrthoRun;
@@ -158,9 +171,9 @@ int product(const CUtensorMap& l, const CUtensorMap& r, const CUtensorMap& o, co
 }
 
 template <typename T>
-int launch(const void* x, void* out, unsigned char* ws, int steps, const int* down, dcnv4::OrthoParams p,
+int launch(const void* x, void* out, unsigned char* ws, int steps, const dcnv4::OrthoStep* step, dcnv4::OrthoParams p,
            cudaStream_t s) {
-    if (steps > 0 && fits_one_cta(p)) return launch_small<T>(x, out, steps, down, p, s);
+    if (steps > 0 && fits_one_cta(p)) return launch_small<T>(x, out, steps, step, p, s);
     const Layout l = layout(p);
     p.lift = reinterpret_cast<int*>(ws + l.lift);
     double* part = reinterpret_cast<double*>(ws);
@@ -186,11 +199,11 @@ int launch(const void* x, void* out, unsigned char* ws, int steps, const int* do
     rc = launch_chained(dcnv4::ortho_start_kernel<T>, dim3(st), 256, 0, s, static_cast<const T*>(x),
                         static_cast<const double*>(part), x0, steps == 0 ? o : static_cast<T*>(nullptr), p);
     for (int k = 0, cur = 0; k < steps && !rc; ++k, cur ^= 1) {
-        rc = product<dcnv4::kGram, float>(xm[cur], xr[cur], am, a, static_cast<float*>(nullptr), p.n, p.m, down + k, nsm, p, s);
-        if (!rc) rc = product<dcnv4::kPoly, float>(am, ar, qm, a, static_cast<float*>(nullptr), p.n, p.n, down + k, nsm, p, s);
+        rc = product<dcnv4::kGram, float>(xm[cur], xr[cur], am, a, static_cast<float*>(nullptr), p.n, p.m, step + k, nsm, p, s);
+        if (!rc) rc = product<dcnv4::kPoly, float>(am, ar, qm, a, static_cast<float*>(nullptr), p.n, p.n, step + k, nsm, p, s);
         if (rc) break;
-        if (k + 1 < steps) rc = product<dcnv4::kApply, float>(qm, xr[cur], xm[cur ^ 1], a, static_cast<float*>(nullptr), p.m, p.n, down + k, nsm, p, s);
-        else rc = product<dcnv4::kLast, T>(qm, xr[cur], xm[cur ^ 1], a, o, p.m, p.n, down + k, nsm, p, s);
+        if (k + 1 < steps) rc = product<dcnv4::kApply, float>(qm, xr[cur], xm[cur ^ 1], a, static_cast<float*>(nullptr), p.m, p.n, step + k, nsm, p, s);
+        else rc = product<dcnv4::kLast, T>(qm, xr[cur], xm[cur ^ 1], a, o, p.m, p.n, step + k, nsm, p, s);
     }
     return rc;
 }
@@ -212,9 +225,9 @@ int dcnv4_orthogonalize(const void* x, void* out, void* workspace, size_t worksp
     const int rc = check_stack(B, R, C, dtype);
     if (rc) return rc;
     if (steps < 0 || steps > kMaxSteps) return DCNV4_ERR_SHAPE;
-    int down[kMaxSteps + 1];
+    dcnv4::OrthoStep step[kMaxSteps + 1];
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c) || !std::isfinite(eps) || !(eps > 0.f) ||
-        !coefficients_bounded(a, b, c, steps, down))
+        !iteration_bounds(a, b, c, steps, step))
         return DCNV4_ERR_COEFFICIENTS;
     if (B == 0) return DCNV4_OK;
     if (!x || !out || !workspace) return DCNV4_ERR_NULL;
@@ -233,9 +246,9 @@ int dcnv4_orthogonalize(const void* x, void* out, void* workspace, size_t worksp
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (dtype) {
-        case DCNV4_F32: return launch<float>(x, out, ws, steps, down, p, s);
-        case DCNV4_F16: return launch<__half>(x, out, ws, steps, down, p, s);
-        default: return launch<__nv_bfloat16>(x, out, ws, steps, down, p, s);
+        case DCNV4_F32: return launch<float>(x, out, ws, steps, step, p, s);
+        case DCNV4_F16: return launch<__half>(x, out, ws, steps, step, p, s);
+        default: return launch<__nv_bfloat16>(x, out, ws, steps, step, p, s);
     }
 }
 

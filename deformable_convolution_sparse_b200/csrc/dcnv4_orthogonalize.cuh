@@ -8,12 +8,14 @@
 // transposed when R > C.
 //
 // Precision on the tensor cores. X, A and P are kept as two fp16 planes, hi =
-// fp16(v s) and lo = fp16(v s - hi), with power-of-two scales s that the
-// iteration's bounds make safe (|X| <= 4, |A| <= 16, |P| <= 64, so that no
-// plane exceeds 2^14): 22 bits of every entry down to about 2^-22 of the
-// bound. A matrix whose norm is far below eps starts with a small X: it is kept
-// lifted by 2^e (Y = 2^e X, |Y| <= 1), e going down by as many bits per step as
-// the step can grow X. A product is three tensor-core products, hi hi + hi lo +
+// fp16(v s) and lo = fp16(v s - hi): an entry is off by at most 2^-23 of itself
+// (one unit of fp32's last place; half of all entries are exact) down to 2^-16
+// of the largest that the planes take, 2^14, and by 2^-39 of that below (lo is
+// subnormal there). X is kept lifted, Y = 2^l X with l the largest for which
+// the iteration's bounds promise |Y| <= 4 (and so |A| <= 16): l follows the
+// singular values' bound down to zero as well as up, and a matrix whose norm
+// is far below eps starts with as large a Y as any. P is lifted likewise, to
+// at most 64. A product is three tensor-core products, hi hi + hi lo +
 // lo hi, each exact, summed in fp32 (lo lo is some 2^-24 of it, but in X X^T and
 // A A it adds up along the diagonal: small matrices, whose other errors are
 // least, take it as well: 1.09e-6 -> 0.86e-6 for 78 x 10). The tensor cores' fp32
@@ -38,11 +40,19 @@ struct OrthoParams {
     int chunks;        // partial sums of squares per matrix (one kernel per product)
     int np, mp;        // row pitches of the n x n and n x m planes, multiples of 8 elements
     float a, b, c, eps;
-    int* lift;         // [B] the exponents e of the first step (one kernel per product)
+    int* lift;         // [B] the lifts before the first step (one kernel per product)
     unsigned* status;
 };
 
-// scales of the planes of X, A, P
+// Powers of two before step k, from the coefficients alone: X of every matrix
+// can be lifted by 2^low, and X that started lifted by 2^l by 2^(l - down);
+// P of the step by 2^up. The larger lift is taken.
+struct OrthoStep {
+    int low, down, up;
+};
+__device__ __forceinline__ int ortho_lift(const OrthoStep& s, int start) { return max(s.low, start - s.down); }
+
+// scales of the planes of Y, A, P
 constexpr float kOrthoSX = 4096.f, kOrthoSA = 1024.f, kOrthoSP = 256.f;
 
 template <typename T>
@@ -82,17 +92,18 @@ __device__ __forceinline__ double ortho_sumsq(const T* __restrict__ x, long long
 
 // The division by den = norm + eps and the lift, from the sum of squares:
 // v / den = (v 2^-k) / (den 2^-k) with den 2^-k in [1/2, 1), so nothing
-// overflows whatever the norm; norm / den lies in [2^(-1-e), 2^-e).
+// overflows whatever the norm; norm / den 2^lift lies in [2, 4], or lift is
+// as large as fp32's exponents need.
 struct OrthoScale {
     float mant;
-    int k, e;
+    int k, lift;
 };
 __device__ __forceinline__ OrthoScale ortho_scale(double sum, float eps) {
     OrthoScale s;
     const double norm = sqrt(sum), den = norm + eps;
     s.k = 0;
     s.mant = isfinite(den) ? static_cast<float>(frexp(den, &s.k)) : __uint_as_float(0x7fc00000u);
-    s.e = norm > 0.0 && isfinite(den) ? min(120, max(0, -ilogb(norm / den) - 1)) : 0;
+    s.lift = norm > 0.0 && isfinite(den) ? min(122, max(2, 1 - ilogb(norm / den))) : 2;
     return s;
 }
 
@@ -105,7 +116,7 @@ __device__ __forceinline__ void ortho_start_tile(const T* __restrict__ x, __half
                                                  const OrthoParams& p) {
     const size_t base = static_cast<size_t>(mat) * p.R * p.C;
     // scale, then divide: exact powers of two around one rounding
-    const int shift = out ? -sc.k : sc.e - sc.k;
+    const int shift = out ? -sc.k : sc.lift - sc.k;
     for (int q = threadIdx.x; q < 4096; q += blockDim.x) {
         const int r = r0 + (q >> 6), c = c0 + (q & 63);
         if (r < p.R && c < p.C) {
@@ -166,7 +177,7 @@ ortho_start_kernel(const T* __restrict__ x, const double* __restrict__ part, __h
     double sum = (lane < p.chunks ? pm[lane] : 0.0) + (lane + 32 < p.chunks ? pm[lane + 32] : 0.0);
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const OrthoScale sc = ortho_scale(sum, p.eps);
-    if (t == 0 && threadIdx.x == 0) p.lift[mat] = sc.e;
+    if (t == 0 && threadIdx.x == 0) p.lift[mat] = sc.lift;
     ortho_start_tile(x, planes, out, mat, static_cast<int>(t / tcn) * 64, static_cast<int>(t % tcn) * 64, sc, tile, p);
 }
 
@@ -223,7 +234,7 @@ constexpr unsigned ortho_smem(int stages) { return 1024u + stages * kOrthoStageB
 struct OrthoTiles {
     int tiles_i, tiles_j;  // tiles of the result
     int kblocks;           // 64 k each
-    int down, down_next;   // bits the lift has gone down before and after this step
+    OrthoStep now, next;   // before and after this step
 };
 
 // RUNS: more than one run.
@@ -316,7 +327,7 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
     } else {
         const int quarter = warp & 3, row = quarter * 32 + lane, et = tid - 64, half = (warp - 2) >> 2;
         const int i = i0 + row, lift = p.lift[mat];
-        const int now = max(0, lift - g.down), next = max(0, lift - g.down_next);
+        const int now = ortho_lift(g.now, lift), next = ortho_lift(g.next, lift);
         // kPoly: this thread's 32 entries of A, read while the products run
         uint4 ah[4], al[4];
         if constexpr (MODE == kPoly) {
@@ -333,9 +344,12 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
                 }
             }
         }
-        // powers of two that undo the lift (A carries it twice, A A four times)
-        const float ux = scalbnf(1.f, (MODE == kLast ? 0 : next) - now);
-        const float ub = MODE == kPoly ? scalbnf(p.b, -2 * now) : 0.f, uc = MODE == kPoly ? scalbnf(p.c, -4 * now) : 0.f;
+        // powers of two that undo the lifts (A carries X's twice, A A four times) and give P and the next X theirs
+        const int up = g.now.up;
+        // (the last ones in two factors: together they can be too small for a float)
+        const int undo = MODE == kLast ? -now - up : next - now - up;
+        const float ux = scalbnf(1.f, MODE == kLast ? undo / 2 : undo), uy = scalbnf(1.f, undo - undo / 2), ua = scalbnf(p.a, up);
+        const float ub = MODE == kPoly ? scalbnf(p.b, up - 2 * now) : 0.f, uc = MODE == kPoly ? scalbnf(p.c, up - 4 * now) : 0.f;
         const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 32;
         float sum[2][16];  // the runs before the last
         unsigned r = 0;
@@ -375,7 +389,7 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
                 if constexpr (MODE == kLast) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        fres[row * 64 + ((half * 32 + cc * 16 + e) ^ (row & 31))] = v[e] * (1.f / (kOrthoSP * kOrthoSX)) * ux;
+                        fres[row * 64 + ((half * 32 + cc * 16 + e) ^ (row & 31))] = v[e] * (1.f / (kOrthoSP * kOrthoSX)) * ux * uy;
                 } else {
                     float scale;  // accumulator to plane units
                     if constexpr (MODE == kGram) scale = kOrthoSA / (kOrthoSX * kOrthoSX);
@@ -394,7 +408,7 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
                             if constexpr (MODE == kPoly) {
                                 const float av = (__half2float(hi[e]) + __half2float(lo[e])) * (kOrthoSP / kOrthoSA);
                                 const int j = j0 + half * 32 + cc * 16 + h * 8 + e;
-                                r = fmaf(uc, r, fmaf(ub, av, i == j ? p.a * kOrthoSP : 0.f));
+                                r = fmaf(uc, r, fmaf(ub, av, i == j ? ua * kOrthoSP : 0.f));
                             }
                             ortho_split(r, hi[e], lo[e]);
                         }
@@ -457,7 +471,7 @@ struct OrthoSmall {
     int steps, xb, nb;       // blocks of X, of A
     int n16, m16;            // n, m rounded up to 16
     unsigned tmem_cols;
-    short down[kOrthoMaxSteps + 1];
+    OrthoStep step[kOrthoMaxSteps + 1];
 };
 
 // hi and lo of entry (i, j), scaled, in a row of blocks
@@ -503,7 +517,7 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
     const OrthoScale sc = ortho_scale(total, p.eps);
     for (int e = tid; e < count; e += kOrthoSmallThreads) {
         const int r = e / p.C, c = e - r * p.C;
-        const float v = scalbnf(ElemTraits<T>::to_float(__ldg(xm + e)), sc.e - sc.k) / sc.mant;
+        const float v = scalbnf(ElemTraits<T>::to_float(__ldg(xm + e)), sc.lift - sc.k) / sc.mant;
         ortho_put(xs, p.transposed ? c : r, p.transposed ? r : c, v * kOrthoSX);
     }
     fence_proxy_async();
@@ -546,7 +560,7 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
     };
     const int nchunks = g.n16 / 16;
     for (int s = 0; s < g.steps && ok; ++s) {
-        const int now = max(0, sc.e - g.down[s]), next = max(0, sc.e - g.down[s + 1]);
+        const int now = ortho_lift(g.step[s], sc.lift), next = ortho_lift(g.step[s + 1], sc.lift), up = g.step[s].up;
         // accumulators of order 0 past the number of k steps hold nothing: left out of the sums
         auto sums = [&](int cc, int ksteps, int step, float (&v)[16]) {
             if (ksteps >= 3) {
@@ -587,7 +601,8 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
         // P = a I + b A + c A A, over A
         product([&](uint32_t lead) { square(smem_addr(as), nchunks, lead); });
         if (!ok) break;
-        const float ub = scalbnf(p.b, -2 * now), uc = scalbnf(p.c, -4 * now) * (kOrthoSP / (kOrthoSA * kOrthoSA));
+        const float ua = scalbnf(p.a, up) * kOrthoSP, ub = scalbnf(p.b, up - 2 * now);
+        const float uc = scalbnf(p.c, up - 4 * now) * (kOrthoSP / (kOrthoSA * kOrthoSA));
         for (int cc = part; cc < nchunks; cc += 4) {
             float v[16];
             sums(cc, nchunks, g.n16, v);
@@ -601,7 +616,7 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
                 for (int e = 0; e < 8; ++e) {
                     const float av = (__half2float(hi[e]) + __half2float(lo[e])) * (kOrthoSP / kOrthoSA);
                     const bool diagonal = row == cc * 16 + h * 8 + e && row < p.n;
-                    ortho_split(fmaf(uc, v[h * 8 + e], fmaf(ub, av, diagonal ? p.a * kOrthoSP : 0.f)), hi[e], lo[e]);
+                    ortho_split(fmaf(uc, v[h * 8 + e], fmaf(ub, av, diagonal ? ua : 0.f)), hi[e], lo[e]);
                 }
                 put_chunk(as, cc, h, hi, lo);
             }
@@ -626,12 +641,14 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
                 }
             });
             if (!ok) break;
-            const float ux = scalbnf(1.f, (last ? 0 : next) - now) / (last ? kOrthoSP * kOrthoSX : kOrthoSP);
+            // (the last powers of two as two factors: together they can be too small for a float)
+            const int undo = last ? -now - up : next - now - up, part_of = last ? undo / 2 : 0;
+            const float ux = scalbnf(1.f, undo - part_of) / (last ? kOrthoSP * kOrthoSX : kOrthoSP), uy = scalbnf(1.f, part_of);
             for (int cc = part; cc < width / 16; cc += 4) {
                 float v[16];
                 sums(cc, nchunks, width, v);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] *= ux;
+                for (int e = 0; e < 16; ++e) v[e] = v[e] * ux * uy;
                 if (last) {
                     // straight to `out`: a lane's 16 columns are neighbours (R <= C), or the lanes are (R > C)
                     T* o = out + static_cast<size_t>(mat) * count;

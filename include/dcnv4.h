@@ -106,7 +106,8 @@ typedef enum {
     DCNV4_ERR_FLAGS = 12,    /* dcnv4_forward_ex: a flag bit that is not defined        */
     DCNV4_ERR_WORKSPACE = 13, /* the workspace is smaller than its _workspace call says  */
     DCNV4_ERR_COEFFICIENTS = 14 /* dcnv4_orthogonalize: coefficients or eps not finite,  */
-                             /* eps <= 0, or an iteration that leaves its bounds         */
+                             /* eps <= 0, or an iteration that leaves its bounds or lets */
+                             /* small singular values fall behind them                   */
 } dcnv4_status_t;
 
 /* Variant switches of dcnv4_forward_ex / dcnv4_validate_ex (bitwise or).
@@ -330,7 +331,11 @@ DCNV4_API int dcnv4_predictor_mx(const void *y, const uint8_t *weight_codes, con
  * only the division). Refused with DCNV4_ERR_COEFFICIENTS: coefficients or
  * eps that are not finite, eps <= 0, and coefficients that within `steps`
  * steps could lift a singular value of [0, 1] above 4 or the factor
- * |a + b s^2 + c s^4| above 64. workspace: device, 256-byte aligned, at least
+ * |a + b s^2 + c s^4| above 64, or by which small singular values, whose
+ * factor is a, would fall behind: |a|^k below 1/16 of the largest singular
+ * value that k <= steps steps can give, or of the product of their largest
+ * factors (a matrix may shrink as a whole: a = 0.5, b = c = 0 is taken).
+ * workspace: device, 256-byte aligned, at least
  * dcnv4_orthogonalize_workspace's bytes; its contents before and after do not
  * matter, and calls whose work overlaps on the GPU need one each. Other
  * errors: DCNV4_ERR_SHAPE (B < 0, R or C <= 0, steps out of range),
