@@ -72,10 +72,13 @@ bool iteration_bounds(double a, double b, double c, int steps, dcnv4::OrthoStep*
             step[k].down = std::max(step[k].down, step[k - 1].down - 120);
         }
         if (k == steps) return true;
-        double q = std::max(std::fabs(a), std::fabs(a + b * r * r + c * r * r * r * r));
-        if (c != 0.0 && -b / (2.0 * c) > 0.0 && -b / (2.0 * c) < r * r) q = std::max(q, std::fabs(a - b * b / (4.0 * c)));
+        // extremes of the factor a + b u + c u^2 over u = s^2 in [0, r^2], and of Q's singular values, less a
+        const double end = b * r * r + c * r * r * r * r, at = c != 0.0 ? -b / (2.0 * c) : 0.0;
+        const double inside = at > 0.0 && at < r * r ? b * at + c * at * at : 0.0;
+        const double q = std::max({std::fabs(a), std::fabs(a + end), std::fabs(a + inside)});
+        const double only = std::max(std::fabs(end), std::fabs(inside));
         if (!(q <= 64.0)) return false;
-        if (q > 0.0) step[k].up = log2_floor(64.0 / q);  // (0: P is zero)
+        if (only > 0.0) step[k].up = std::min(120, log2_floor(64.0 / only));  // (0: Q is zero)
         r = poly_bound(a, b, c, r);
         grown *= q;
         linear *= std::fabs(a);
@@ -94,7 +97,7 @@ dcnv4::OrthoParams make_params(int B, int R, int C) {
     return p;
 }
 
-// Workspace: the sums of squares, the lifts, then the fp16 plane pairs of X (two, in turn), A and P.
+// Workspace: the sums of squares, the lifts, then the fp16 plane pairs of X (two, in turn), A and Q.
 struct Layout {
     size_t lift, x0, x1, a, p, bytes;
 };
@@ -152,7 +155,7 @@ int launch_small(const void* x, void* out, int steps, const dcnv4::OrthoStep* st
 }
 
 template <int MODE, typename T>
-int product(const CUtensorMap& l, const CUtensorMap& r, const CUtensorMap& o, const __half* a, T* out, int cols, int k,
+int product(const CUtensorMap& l, const CUtensorMap& r, const CUtensorMap& o, T* out, int cols, int k,
             const dcnv4::OrthoStep* step, int nsm, const dcnv4::OrthoParams& p, cudaStream_t s) {
     dcnv4::OrthoTiles g{};
     g.tiles_i = (p.n + 127) / 128;
@@ -167,7 +170,7 @@ int product(const CUtensorMap& l, const CUtensorMap& r, const CUtensorMap& o, co
                      : (runs ? dcnv4::ortho_product_kernel<MODE, T, 2, true> : dcnv4::ortho_product_kernel<MODE, T, 2, false>);
     const unsigned smem = dcnv4::ortho_smem(deep ? 4 : 2);
     if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess) return DCNV4_ERR_LAUNCH;
-    return launch_chained(kern, dim3(tiles), dcnv4::kOrthoThreads, smem, s, l, r, o, a, out, g, p);
+    return launch_chained(kern, dim3(tiles), dcnv4::kOrthoThreads, smem, s, l, r, o, out, g, p);
 }
 
 template <typename T>
@@ -199,11 +202,11 @@ int launch(const void* x, void* out, unsigned char* ws, int steps, const dcnv4::
     rc = launch_chained(dcnv4::ortho_start_kernel<T>, dim3(st), 256, 0, s, static_cast<const T*>(x),
                         static_cast<const double*>(part), x0, steps == 0 ? o : static_cast<T*>(nullptr), p);
     for (int k = 0, cur = 0; k < steps && !rc; ++k, cur ^= 1) {
-        rc = product<dcnv4::kGram, float>(xm[cur], xr[cur], am, a, static_cast<float*>(nullptr), p.n, p.m, step + k, nsm, p, s);
-        if (!rc) rc = product<dcnv4::kPoly, float>(am, ar, qm, a, static_cast<float*>(nullptr), p.n, p.n, step + k, nsm, p, s);
+        rc = product<dcnv4::kGram, float>(xm[cur], xr[cur], am, static_cast<float*>(nullptr), p.n, p.m, step + k, nsm, p, s);
+        if (!rc) rc = product<dcnv4::kPoly, float>(am, ar, qm, static_cast<float*>(nullptr), p.n, p.n, step + k, nsm, p, s);
         if (rc) break;
-        if (k + 1 < steps) rc = product<dcnv4::kApply, float>(qm, xr[cur], xm[cur ^ 1], a, static_cast<float*>(nullptr), p.m, p.n, step + k, nsm, p, s);
-        else rc = product<dcnv4::kLast, T>(qm, xr[cur], xm[cur ^ 1], a, o, p.m, p.n, step + k, nsm, p, s);
+        if (k + 1 < steps) rc = product<dcnv4::kApply, float>(qm, xr[cur], xm[cur ^ 1], static_cast<float*>(nullptr), p.m, p.n, step + k, nsm, p, s);
+        else rc = product<dcnv4::kLast, T>(qm, xr[cur], xm[cur ^ 1], o, p.m, p.n, step + k, nsm, p, s);
     }
     return rc;
 }

@@ -1,27 +1,31 @@
 // sm_100a kernels of the Newton-Schulz orthogonalisation of a stack of weight
 // updates. Each matrix X (R x C) is divided by its Frobenius norm (plus eps),
 // which puts its singular values in [0, 1], and then
-//   A = X X^T,  X <- P X,  P = a I + b A + c A A
+//   A = X X^T,  X <- a X + Q X,  Q = b A + c A A
 // is repeated `steps` times: every singular value s goes through the odd
 // polynomial a s + b s^3 + c s^5 while the singular vectors stay. The products
 // are formed on the smaller side, n = min(R, C), m = max(R, C): X is taken
 // transposed when R > C.
 //
-// Precision on the tensor cores. X, A and P are kept as two fp16 planes, hi =
+// Precision on the tensor cores. X, A and Q are kept as two fp16 planes, hi =
 // fp16(v s) and lo = fp16(v s - hi): an entry is off by at most 2^-23 of itself
 // (one unit of fp32's last place; half of all entries are exact) down to 2^-16
 // of the largest that the planes take, 2^14, and by 2^-39 of that below (lo is
 // subnormal there). X is kept lifted, Y = 2^l X with l the largest for which
 // the iteration's bounds promise |Y| <= 4 (and so |A| <= 16): l follows the
 // singular values' bound down to zero as well as up, and a matrix whose norm
-// is far below eps starts with as large a Y as any. P is lifted likewise, to
+// is far below eps starts with as large a Y as any. Q is lifted likewise, to
 // at most 64. A product is three tensor-core products, hi hi + hi lo +
 // lo hi, each exact, summed in fp32 (lo lo is some 2^-24 of it, but in X X^T and
 // A A it adds up along the diagonal: small matrices, whose other errors are
 // least, take it as well: 1.09e-6 -> 0.86e-6 for 78 x 10). The tensor cores' fp32
 // additions truncate, so a long chain of them drifts one way: the hi hi terms
 // go to three accumulators in turn and the small cross terms to one of their
-// own, and the epilogue adds these with rounding.
+// own, and the epilogue adds these with rounding. The step's a X is added there
+// too, and not multiplied as the diagonal of P = a I + Q: next to it every
+// further addition would truncate the sum by up to a unit of its last place,
+// all downwards, step after step. (12 steps of 0.9, 0.05, 0 on 129 x 257: error
+// 1.8e-6 that way, 2e-7 this way; fp32 products 4e-7.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -46,14 +50,17 @@ struct OrthoParams {
 
 // Powers of two before step k, from the coefficients alone: X of every matrix
 // can be lifted by 2^low, and X that started lifted by 2^l by 2^(l - down);
-// P of the step by 2^up. The larger lift is taken.
+// Q of the step by 2^up. The larger lift is taken.
 struct OrthoStep {
     int low, down, up;
 };
 __device__ __forceinline__ int ortho_lift(const OrthoStep& s, int start) { return max(s.low, start - s.down); }
 
-// scales of the planes of Y, A, P
-constexpr float kOrthoSX = 4096.f, kOrthoSA = 1024.f, kOrthoSP = 256.f;
+// 2^e for e <= 127; 0 below fp32's normal numbers (b, c <= 192 and what they scale is as negligible there)
+__device__ __forceinline__ float ortho_pow2(int e) { return e < -126 ? 0.f : __uint_as_float(static_cast<unsigned>(e + 127) << 23); }
+
+// scales of the planes of Y, A, Q
+constexpr float kOrthoSX = 4096.f, kOrthoSA = 1024.f, kOrthoSQ = 256.f;
 
 template <typename T>
 __device__ __forceinline__ T ortho_from_float(float v) {
@@ -197,18 +204,11 @@ __device__ __forceinline__ void ortho_sum4(uint32_t at, uint32_t step, float (&v
     for (int e = 0; e < 16; ++e) v[e] += w[0][e];
 }
 
-// 16 bytes, loaded where it is written (not moved behind a later wait)
-__device__ __forceinline__ uint4 ortho_load(const __half* p) {
-    uint4 v;
-    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
-
 // One product of the iteration, a 128 x 64 tile of the result per CTA:
 //   kGram:  A = X X^T          (k over m; both operands K-major rows of X)
-//   kPoly:  P = aI + bA + cAA  (k over n; A is symmetric: both K-major)
-//   kApply: X' = P X           (k over n; X's rows run along the result's
-//                               columns: an MN-major operand)
+//   kPoly:  Q = bA + cAA   (k over n; A is symmetric: both K-major)
+//   kApply: X' = aX + QX   (k over n; X's rows run along the result's
+//                           columns: an MN-major operand)
 //   kLast:  kApply with the result rounded to T and written to `out`
 // Warp 0 (one lane) loads 64 k at a time by TMA: 128 rows x 64 k of the left
 // planes, 64 x 64 of the right ones, in a ring of STAGES; warp 1 issues the
@@ -241,8 +241,7 @@ struct OrthoTiles {
 template <int MODE, typename T, int STAGES, bool RUNS>
 __global__ void __launch_bounds__(kOrthoThreads, STAGES == 2 ? 2 : 1)
 ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_constant__ CUtensorMap rmap,
-                     const __grid_constant__ CUtensorMap omap, const __half* __restrict__ aplanes, T* __restrict__ out,
-                     OrthoTiles g, OrthoParams p) {
+                     const __grid_constant__ CUtensorMap omap, T* __restrict__ out, OrthoTiles g, OrthoParams p) {
     extern __shared__ unsigned char ortho_smem_raw[];
     unsigned char* sm = ortho_smem_raw + ((1024u - (smem_addr(ortho_smem_raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + STAGES * kOrthoStageBytes);
@@ -275,6 +274,12 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
     const uint32_t tmem = tc::uniform(*slot);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // The epilogue needs the tile's own entries of A (kPoly) or X (kApply, kLast), and finds them in the ring: the
+    // order of k goes round so that the block of the left operand with this tile's columns, or the two of the right
+    // one with its rows, come last.
+    int k0 = 0;
+    if constexpr (MODE == kPoly) k0 = (j0 / 64 + 1) % g.kblocks;
+    else if constexpr (MODE >= kApply) k0 = (i0 / 64 + 2) % g.kblocks;
     bool ok = true;
     int loads = 0;  // the loading lane's steps so far
 
@@ -286,13 +291,14 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
                     ok = mbar_wait_bounded(&empty[s], static_cast<unsigned>(kb / STAGES - 1) & 1u, kCopyWaitLimitNs);
                 if (!ok) break;
                 unsigned char* st = sm + s * kOrthoStageBytes;
+                const int k = (kb + k0 < g.kblocks ? kb + k0 : kb + k0 - g.kblocks) * 64;
                 mbar_expect_tx(&full[s], kOrthoStageBytes);
                 for (int pl = 0; pl < 2; ++pl) {
-                    tc::tma_load_3d(st + pl * 16384, &lmap, kb * 64, i0, pl * p.B + mat, &full[s]);
+                    tc::tma_load_3d(st + pl * 16384, &lmap, k, i0, pl * p.B + mat, &full[s]);
                     if (MODE >= kApply)
-                        tc::tma_load_3d(st + 32768 + pl * 8192, &rmap, j0, kb * 64, pl * p.B + mat, &full[s]);
+                        tc::tma_load_3d(st + 32768 + pl * 8192, &rmap, j0, k, pl * p.B + mat, &full[s]);
                     else
-                        tc::tma_load_3d(st + 32768 + pl * 8192, &rmap, kb * 64, j0, pl * p.B + mat, &full[s]);
+                        tc::tma_load_3d(st + 32768 + pl * 8192, &rmap, k, j0, pl * p.B + mat, &full[s]);
                 }
                 mbar_arrive(&full[s]);
                 loads = kb + 1;
@@ -326,30 +332,19 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
         if (ok && lead) tc::commit(done);
     } else {
         const int quarter = warp & 3, row = quarter * 32 + lane, et = tid - 64, half = (warp - 2) >> 2;
-        const int i = i0 + row, lift = p.lift[mat];
+        const int lift = p.lift[mat];
         const int now = ortho_lift(g.now, lift), next = ortho_lift(g.next, lift);
-        // kPoly: this thread's 32 entries of A, read while the products run
-        uint4 ah[4], al[4];
-        if constexpr (MODE == kPoly) {
-            const size_t plane = static_cast<size_t>(p.B) * p.n * p.np;
-            const __half* ar = aplanes + (static_cast<size_t>(mat) * p.n + i) * p.np + j0 + half * 32;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                // the pitch is a multiple of 8: a chunk of 8 that starts before it lies inside the row
-                const bool on = i < p.n && j0 + half * 32 + q * 8 < p.np;
-                ah[q] = al[q] = make_uint4(0, 0, 0, 0);
-                if (on) {
-                    ah[q] = ortho_load(ar + q * 8);
-                    al[q] = ortho_load(ar + plane + q * 8);
-                }
-            }
-        }
-        // powers of two that undo the lifts (A carries X's twice, A A four times) and give P and the next X theirs
-        const int up = g.now.up;
+        // where this thread's own row lies: hi and, a plane further on, lo (kApply and kLast: rows past the blocks of
+        // 64 that there are lie past the matrix)
+        const int own_kb = MODE == kPoly ? g.kblocks - 1 : max(0, g.kblocks - 2 + (row >> 6)), own_s = own_kb % STAGES;
+        const unsigned char* own_row = sm + own_s * kOrthoStageBytes + (MODE == kPoly ? row * 128 : 32768 + (row & 63) * 128);
+        constexpr unsigned own_plane = MODE == kPoly ? 16384u : 8192u;
+        // powers of two that undo the lifts (A carries X's twice, A A four times) and give Q and the next X theirs
         // (the last ones in two factors: together they can be too small for a float)
-        const int undo = MODE == kLast ? -now - up : next - now - up;
-        const float ux = scalbnf(1.f, MODE == kLast ? undo / 2 : undo), uy = scalbnf(1.f, undo - undo / 2), ua = scalbnf(p.a, up);
-        const float ub = MODE == kPoly ? scalbnf(p.b, up - 2 * now) : 0.f, uc = MODE == kPoly ? scalbnf(p.c, up - 4 * now) : 0.f;
+        const int up = g.now.up, undo = MODE == kLast ? -now : next - now;
+        const float ux = ortho_pow2(MODE == kLast ? undo / 2 : undo), uy = ortho_pow2(undo - undo / 2) * (1.f / kOrthoSX);
+        const float uq = ortho_pow2(-up) * (1.f / kOrthoSQ);
+        const float ub = p.b * ortho_pow2(up - 2 * now), uc = p.c * ortho_pow2(up - 4 * now) * (kOrthoSQ / (kOrthoSA * kOrthoSA));
         const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 32;
         float sum[2][16];  // the runs before the last
         unsigned r = 0;
@@ -374,7 +369,10 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
             }
         }
         // one decision for all the warps
-        ok = tc::bar_and(1, kOrthoEpi, ok && mbar_wait_bounded(done, r & 1u, kCopyWaitLimitNs));
+        ok = ok && mbar_wait_bounded(done, r & 1u, kCopyWaitLimitNs);
+        // (long complete: what makes the loads' bytes this thread's to read)
+        if (MODE != kGram) ok = ok && mbar_wait_bounded(&full[own_s], static_cast<unsigned>(own_kb / STAGES) & 1u, kCopyWaitLimitNs);
+        ok = tc::bar_and(1, kOrthoEpi, ok);
         if (ok) {
             tc::fence_after();
             float* fres = reinterpret_cast<float*>(sm);
@@ -386,33 +384,31 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
                 if constexpr (RUNS)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[e] += sum[cc][e];
-                if constexpr (MODE == kLast) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        fres[row * 64 + ((half * 32 + cc * 16 + e) ^ (row & 31))] = v[e] * (1.f / (kOrthoSP * kOrthoSX)) * ux * uy;
-                } else {
-                    float scale;  // accumulator to plane units
-                    if constexpr (MODE == kGram) scale = kOrthoSA / (kOrthoSX * kOrthoSX);
-                    else if constexpr (MODE == kPoly) scale = kOrthoSP / (kOrthoSA * kOrthoSA);
-                    else scale = ux / kOrthoSP;
+                for (int h = 0; h < 2; ++h) {
+                    __half hi[8], lo[8];
+                    const int ch = (half * 4 + cc * 2 + h) ^ (row & 7);
+                    if constexpr (MODE != kGram) {
+                        // (kPoly: possibly the very chunk that the result takes below)
+                        *reinterpret_cast<uint4*>(hi) = reinterpret_cast<const uint4*>(own_row)[ch];
+                        *reinterpret_cast<uint4*>(lo) = reinterpret_cast<const uint4*>(own_row + own_plane)[ch];
+                    }
+                    // accumulators to plane units, with A's or X's own term added in fp32
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        __half hi[8], lo[8];
-                        if constexpr (MODE == kPoly) {
-                            *reinterpret_cast<uint4*>(hi) = ah[cc * 2 + h];
-                            *reinterpret_cast<uint4*>(lo) = al[cc * 2 + h];
+                    for (int e = 0; e < 8; ++e) {
+                        float r = v[h * 8 + e];
+                        if constexpr (MODE == kGram) {
+                            r *= kOrthoSA / (kOrthoSX * kOrthoSX);
+                        } else {
+                            const float own = __half2float(hi[e]) + __half2float(lo[e]);
+                            if constexpr (MODE == kPoly)
+                                r = fmaf(uc, r, ub * (own * (kOrthoSQ / kOrthoSA)));
+                            else r = fmaf(uq, r, p.a * own) * ux;
                         }
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float r = v[h * 8 + e] * scale;
-                            if constexpr (MODE == kPoly) {
-                                const float av = (__half2float(hi[e]) + __half2float(lo[e])) * (kOrthoSP / kOrthoSA);
-                                const int j = j0 + half * 32 + cc * 16 + h * 8 + e;
-                                r = fmaf(uc, r, fmaf(ub, av, i == j ? ua * kOrthoSP : 0.f));
-                            }
-                            ortho_split(r, hi[e], lo[e]);
-                        }
-                        const int ch = (half * 4 + cc * 2 + h) ^ (row & 7);
+                        if constexpr (MODE == kLast) fres[row * 64 + ((half * 32 + cc * 16 + h * 8 + e) ^ (row & 31))] = r * uy;
+                        else ortho_split(r, hi[e], lo[e]);
+                    }
+                    if constexpr (MODE != kLast) {
                         hp[ch] = *reinterpret_cast<uint4*>(hi);
                         lp[ch] = *reinterpret_cast<uint4*>(lo);
                     }
@@ -459,7 +455,7 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
 // bytes each, 128-byte swizzle; rows and columns past the matrix are zero. X's
 // blocks serve as both operands of the Gram product (K-major) and as the right
 // one of the application (MN-major), A's as both of the polynomial, which
-// overwrites them with P. One warp issues a product's instructions, then all
+// overwrites them with Q. One warp issues a product's instructions, then all
 // warps turn the accumulators into the next operand. What bounds it is the
 // chain of 3 * steps dependent products, each a few hundred cycles of tensor
 // work between two barriers: 4 matrices of 108 x 64 take 30 us (67 through the
@@ -598,11 +594,11 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
                 put_chunk(as, cc, h, hi, lo);
             }
         }
-        // P = a I + b A + c A A, over A
+        // Q = b A + c A A, over A
         product([&](uint32_t lead) { square(smem_addr(as), nchunks, lead); });
         if (!ok) break;
-        const float ua = scalbnf(p.a, up) * kOrthoSP, ub = scalbnf(p.b, up - 2 * now);
-        const float uc = scalbnf(p.c, up - 4 * now) * (kOrthoSP / (kOrthoSA * kOrthoSA));
+        const float ub = p.b * ortho_pow2(up - 2 * now);
+        const float uc = p.c * ortho_pow2(up - 4 * now) * (kOrthoSQ / (kOrthoSA * kOrthoSA));
         for (int cc = part; cc < nchunks; cc += 4) {
             float v[16];
             sums(cc, nchunks, g.n16, v);
@@ -614,14 +610,13 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
                 *reinterpret_cast<uint4*>(lo) = at[1024];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float av = (__half2float(hi[e]) + __half2float(lo[e])) * (kOrthoSP / kOrthoSA);
-                    const bool diagonal = row == cc * 16 + h * 8 + e && row < p.n;
-                    ortho_split(fmaf(uc, v[h * 8 + e], fmaf(ub, av, diagonal ? ua : 0.f)), hi[e], lo[e]);
+                    const float av = (__half2float(hi[e]) + __half2float(lo[e])) * (kOrthoSQ / kOrthoSA);
+                    ortho_split(fmaf(uc, v[h * 8 + e], ub * av), hi[e], lo[e]);
                 }
                 put_chunk(as, cc, h, hi, lo);
             }
         }
-        // X = P X, up to 128 columns at a time, four accumulators as above `width` apart
+        // X = a X + Q X, up to 128 columns at a time, four accumulators as above `width` apart
         const bool last = s + 1 == g.steps;
         for (int j0 = 0; j0 < g.m16 && ok; j0 += 128) {
             const int width = min(128, g.m16 - j0);
@@ -642,13 +637,22 @@ ortho_small_kernel(const T* __restrict__ x, T* __restrict__ out, const __grid_co
             });
             if (!ok) break;
             // (the last powers of two as two factors: together they can be too small for a float)
-            const int undo = last ? -now - up : next - now - up, part_of = last ? undo / 2 : 0;
-            const float ux = scalbnf(1.f, undo - part_of) / (last ? kOrthoSP * kOrthoSX : kOrthoSP), uy = scalbnf(1.f, part_of);
+            const int undo = last ? -now : next - now;
+            const float ux = ortho_pow2(last ? undo / 2 : undo), uq = ortho_pow2(-up) * (1.f / kOrthoSQ);
+            const float uy = last ? ortho_pow2(undo - undo / 2) * (1.f / kOrthoSX) : 1.f;
             for (int cc = part; cc < width / 16; cc += 4) {
                 float v[16];
                 sums(cc, nchunks, width, v);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = v[e] * ux * uy;
+                for (int h = 0; h < 2; ++h) {
+                    __half hi[8], lo[8];
+                    const uint4* at = chunk_of(xs, (j0 >> 4) + cc, h);
+                    *reinterpret_cast<uint4*>(hi) = *at;
+                    *reinterpret_cast<uint4*>(lo) = at[1024];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[h * 8 + e] = fmaf(uq, v[h * 8 + e], p.a * (__half2float(hi[e]) + __half2float(lo[e]))) * ux * uy;
+                }
                 if (last) {
                     // straight to `out`: a lane's 16 columns are neighbours (R <= C), or the lanes are (R > C)
                     T* o = out + static_cast<size_t>(mat) * count;

@@ -325,8 +325,11 @@ DCNV4_API int dcnv4_predictor_mx(const void *y, const uint8_t *weight_codes, con
  *   X <- a X + (b A + c A A) X,  A = X X^T
  * (on X^T when R > C), which keeps its singular vectors and moves every
  * singular value s to a s + b s^3 + c s^5. x: device, dtype, read only; out:
- * device, dtype, [B, R, C], fully overwritten. Sums and the iterates carry
- * fp32 precision whatever dtype is; the result is rounded once. A matrix of zeros
+ * device, dtype, [B, R, C], fully overwritten. Whatever dtype is, sums are
+ * fp32, the step's a X is added in fp32, and between steps an entry of X, A
+ * and b A + c A A is held as two fp16 values: to one unit of fp32's last
+ * place, or to 2^-38 of its matrix's norm where that is more. The result is
+ * rounded once. A matrix of zeros
  * gives zeros; a NaN or an infinity makes its matrix NaN. steps: 0..64 (0:
  * only the division). Refused with DCNV4_ERR_COEFFICIENTS: coefficients or
  * eps that are not finite, eps <= 0, and coefficients that within `steps`

@@ -1,5 +1,6 @@
 """dcnv4_orthogonalize over the whole range of coefficients it takes: iterations that shrink a matrix as well as
-ones that let it grow, in both of its forms (a matrix per CTA, a kernel per product).
+ones that let it grow, at the published coefficients and at others, in both of its forms (a matrix per CTA,
+a kernel per product), from matrices of any size.
 
 Tolerance of an iteration with b = c = 0, entry by entry: the quotient by the norm is rounded once and the norm is
 off by less than that, 2 * 2^-24; in each step P = a I has one entry a row, held to 2^-23, X is held to 2^-23 of
@@ -11,6 +12,7 @@ import pytest
 import torch
 
 import deformable_convolution_sparse_b200 as dcn
+from oracle import weight as ow
 
 pytestmark = pytest.mark.gpu
 
@@ -40,6 +42,55 @@ def test_coefficients_that_scale_the_matrix(a, steps, form, cuda_device, monkeyp
         err = np.abs(_np(out) - want)
         floor = steps * 2.0 ** -38 * np.linalg.norm(want, axis=(1, 2), keepdims=True) + 2.0 ** -149   # (fp32's last)
         assert np.all(err <= (2 + 12 * steps) * 2.0 ** -24 * np.abs(want) + floor), (shape, (err / np.abs(want)).max())
+
+
+@pytest.mark.parametrize("form", ["", "products"])
+@pytest.mark.parametrize("co,steps", [((0.5, 0.0, 0.0), 8), ((0.9, 0.05, 0.0), 12), ((0.6, 0.1, -0.02), 5),
+                                      ((1.5, -0.5, 0.0), 12), ((1.875, -1.25, 0.375), 9), ((3.4445, -4.775, 2.0315), 7)],
+                         ids=str)
+def test_coefficients_of_all_kinds(co, steps, form, cuda_device, monkeypatch):
+    """Against the same iteration by fp32 matrix products, both measured against 64 bits: no more than three
+    times its error (operands off by 2^-23 where those are off by 2^-24, and truncated additions), plus 2^-22."""
+    monkeypatch.setenv("DCNV4_ORTHO_FORM", form)
+    for shape in SMALL[1:] + LARGE:
+        x = torch.randn(*shape, generator=torch.Generator().manual_seed(sum(shape))).to(cuda_device)
+        x[0, 0] *= 1e-3
+
+        def plain(v):
+            t = v.shape[1] > v.shape[2]
+            v = v.transpose(1, 2) if t else v
+            v = v / (torch.linalg.matrix_norm(v, keepdim=True) + 1e-7)
+            for _ in range(steps):
+                g = v @ v.transpose(1, 2)
+                v = co[0] * v + (co[1] * g + co[2] * (g @ g)) @ v
+            return v.transpose(1, 2) if t else v
+        ref = plain(x.double())
+        err = [float((t.double() - ref).norm() / ref.norm())
+               for t in (dcn.orthogonalize(x, steps=steps, coefficients=co), plain(x))]
+        assert err[0] <= 3 * err[1] + 2.0 ** -22, (shape, err)
+    assert dcn.device_status() == 0
+
+
+@pytest.mark.parametrize("form", ["", "products"])
+@pytest.mark.parametrize("scale,eps", [(1e-9, 1.0), (1e-20, 1e-3), (1e-3, 1.0), (1e30, 1e-7), (1e-30, 1e-38)], ids=str)
+def test_matrices_of_any_size_keep_their_bits(scale, eps, form, cuda_device, monkeypatch):
+    """Norms far below eps, and far from 1, with coefficients that converge (so that a lost plane shows): against
+    64 bits, no more than three times the error of fp32 products of the matrix brought to size first."""
+    monkeypatch.setenv("DCNV4_ORTHO_FORM", form)
+    co, steps = (1.5, -0.5, 0.0), 10
+    for shape in ((2, 5, 8), (3, 108, 64), (1, 300, 128)):
+        g = torch.Generator().manual_seed(sum(shape))
+        x = (torch.randn(*shape, generator=g).double() * scale).float()
+        ref = ow.orthogonalize(_np(x), steps, co, float(np.float32(eps)))
+        v = torch.tensor(_np(x) / (np.linalg.norm(_np(x), axis=(1, 2), keepdims=True) + float(np.float32(eps))))
+        lift = 2.0 ** -np.floor(np.log2(float(v.norm())))
+        w, s2 = (v * lift).float().to(cuda_device), lift ** -2.0
+        for _ in range(steps):
+            w = co[0] * w + s2 * co[1] * (w @ w.transpose(1, 2)) @ w
+        out = dcn.orthogonalize(x.to(cuda_device), steps=steps, coefficients=co, eps=eps)
+        err = [np.linalg.norm(t - ref) / np.linalg.norm(ref) for t in (_np(out), _np(w) / lift)]
+        assert err[0] <= 3 * err[1] + 2.0 ** -22, (shape, err)
+    assert dcn.device_status() == 0
 
 
 def test_coefficients_that_let_small_singular_values_fall_behind_are_refused(cuda_device):
