@@ -223,6 +223,33 @@ struct Piece {
         }
     }
 };
+// A converting thread's sums of g for the bias, eight slots: fp32 over runs of
+// at most kBiasRun chunks, fp64 from there on, so that the error does not grow
+// with the number of pixels (9,000,001 equal values in one fp32 sum per thread:
+// 4e-6 of the sum). The fp64 sums are kept in memory (volatile: registers are
+// what these threads have least of) and touched once a run: some 2 % of the
+// time; fp64 in the sums over the threads and in the join too cost 10 %.
+constexpr int kBiasRun = 16;
+struct BiasSums {
+    float run[8] = {};
+    volatile double total[8];
+    __device__ __forceinline__ void add(const float (&v)[kPieces][8]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)  // rows past the tile hold zeros
+            run[e] += (v[0][e] + v[1][e]) + (v[2][e] + v[3][e]);
+    }
+    __device__ __forceinline__ void flush(bool first) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            total[e] = first ? static_cast<double>(run[e]) : total[e] + static_cast<double>(run[e]);
+            run[e] = 0.f;
+        }
+    }
+    __device__ __forceinline__ void finish() {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) run[e] = static_cast<float>(total[e] + static_cast<double>(run[e]));
+    }
+};
 // the operand tiles this warp's threads wrote, handed over (one arrival per warp)
 __device__ __forceinline__ void hand_over(uint64_t* bar, int lane) {
     fence_proxy_async();
@@ -557,7 +584,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
 
     if (warp < 16) {
         const bool sums = c0 == 0 && pbias != nullptr;
-        float bs[2][8] = {};              // [chunk][slot of this thread's group]
+        BiasSums bs[2];                   // of each chunk
         const ChunkWalk walk0(p.NO - g0, tid), walk1(nch == 2 ? p.NO - g0 - 64 : 64, tid);
         const ChunkWalk ywalk0(p.C - c0, tid), ywalk1(wide ? p.C - c0 - 64 : 64, tid);
         const int group = warp >> 3;
@@ -576,57 +603,60 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
             piece.landed();
             if (lane == 0) mbar_arrive(&raw_empty[k & 3]);
         };
-        for (int i = 0; i < mine && ok; ++i) {
-            // With one stage of y, both groups wait for its release once a tile, before their first store. A group
-            // that writes y (or a stage of g) in every other tile only would otherwise miss a phase of the barrier
-            // and take the one before for the one it needs.
-            bool freed = i == 0;
-            auto y_freed = [&] {
-                if constexpr (!S::kDirectY && S::kYStages == 1) {
-                    if (!freed) ok = ok && tc::warp_wait(&empty_y[0], static_cast<unsigned>(i - 1) & 1u, kCopyWaitLimitNs);
-                    freed = true;
-                }
-            };
-            if constexpr (!S::kDirectY) {
-                const int ys = i % S::kYStages, yn = i / S::kYStages;
+        for (int begin = 0; begin < mine && ok; begin += kBiasRun) {
+            for (int i = begin, end = min(mine, begin + kBiasRun); i < end && ok; ++i) {
+                // With one stage of y, both groups wait for its release once a tile, before their first store. A group
+                // that writes y (or a stage of g) in every other tile only would otherwise miss a phase of the barrier
+                // and take the one before for the one it needs.
+                bool freed = i == 0;
+                auto y_freed = [&] {
+                    if constexpr (!S::kDirectY && S::kYStages == 1) {
+                        if (!freed) ok = ok && tc::warp_wait(&empty_y[0], static_cast<unsigned>(i - 1) & 1u, kCopyWaitLimitNs);
+                        freed = true;
+                    }
+                };
+                if constexpr (!S::kDirectY) {
+                    const int ys = i % S::kYStages, yn = i / S::kYStages;
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    if (b >= ny || !ok) break;
+                    for (int b = 0; b < 2; ++b) {
+                        if (b >= ny || !ok) break;
+                        if ((k & 1) == group) {
+                            const ChunkWalk& walk = b ? ywalk1 : ywalk0;
+                            Piece<T> piece;
+                            if constexpr (RAW) take(piece, walk);
+                            else piece.from_global(y, walk, pixel(i), p.M, c0 + b * 64, p.C);
+                            y_freed();
+                            if (S::kYStages > 1 && yn > 0)
+                                ok = ok && tc::warp_wait(&empty_y[ys], static_cast<unsigned>(yn - 1) & 1u, kCopyWaitLimitNs);
+                            if (!ok) break;
+                            piece.template store<YP>(sm + ys * ystage + b * 16384, p.ystep, walk);
+                            hand_over(&full_y[ys], lane);
+                        }
+                        next();
+                    }
+                }
+#pragma unroll
+                for (int ch = 0; ch < 2; ++ch) {
+                    if (ch >= nch || !ok) break;
                     if ((k & 1) == group) {
-                        const ChunkWalk& walk = b ? ywalk1 : ywalk0;
-                        Piece<T> piece;
+                        const ChunkWalk& walk = ch ? walk1 : walk0;
+                        const int n = i * nch + ch, s = n & 1;
+                        Piece<float> piece;
                         if constexpr (RAW) take(piece, walk);
-                        else piece.from_global(y, walk, pixel(i), p.M, c0 + b * 64, p.C);
+                        else piece.from_global(grec, walk, pixel(i), p.M, g0 + ch * 64, p.NO);
                         y_freed();
-                        if (S::kYStages > 1 && yn > 0)
-                            ok = ok && tc::warp_wait(&empty_y[ys], static_cast<unsigned>(yn - 1) & 1u, kCopyWaitLimitNs);
+                        if (n >= 2) ok = ok && tc::warp_wait(&empty_g[s], static_cast<unsigned>((n >> 1) - 1) & 1u, kCopyWaitLimitNs);
                         if (!ok) break;
-                        piece.template store<YP>(sm + ys * ystage + b * 16384, p.ystep, walk);
-                        hand_over(&full_y[ys], lane);
+                        piece.template store<3>(gsm + s * S::kG, 16384u, walk);
+                        hand_over(&full_g[s], lane);
+                        if (sums) bs[ch].add(piece.v);
                     }
                     next();
                 }
             }
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-                if (ch >= nch || !ok) break;
-                if ((k & 1) == group) {
-                    const ChunkWalk& walk = ch ? walk1 : walk0;
-                    const int n = i * nch + ch, s = n & 1;
-                    Piece<float> piece;
-                    if constexpr (RAW) take(piece, walk);
-                    else piece.from_global(grec, walk, pixel(i), p.M, g0 + ch * 64, p.NO);
-                    y_freed();
-                    if (n >= 2) ok = ok && tc::warp_wait(&empty_g[s], static_cast<unsigned>((n >> 1) - 1) & 1u, kCopyWaitLimitNs);
-                    if (!ok) break;
-                    piece.template store<3>(gsm + s * S::kG, 16384u, walk);
-                    hand_over(&full_g[s], lane);
-                    if (sums)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)  // rows past the tile hold zeros
-                            bs[ch][e] += (piece.v[0][e] + piece.v[1][e]) + (piece.v[2][e] + piece.v[3][e]);
-                }
-                next();
+            if (sums && begin + kBiasRun < mine) {
+                bs[0].flush(begin == 0);
+                bs[1].flush(begin == 0);
             }
         }
         if (sums) {
@@ -643,9 +673,11 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
                 if (ch >= nch) break;
                 const int ng = ch ? walk1.ng : walk0.ng, rows = ch ? walk1.rows : walk0.rows;
                 tc::bar_sync(2, kConv);
-                if (ok)
+                if (ok) {
+                    if (mine > kBiasRun) bs[ch].finish();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) red[tid * 8 + k] = bs[ch][k];
+                    for (int k = 0; k < 8; ++k) red[tid * 8 + k] = bs[ch].run[k];
+                }
                 tc::bar_sync(2, kConv);
                 // eight threads per slot, every eighth of the slot's threads of both groups each, then the eight
                 const int s = tid >> 3, part8 = tid & 7;
@@ -889,7 +921,7 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
         const int s = warp >> 3;
         const bool last = nch == 1 || s == 1;
         const ChunkWalk walk(last ? p.NO - (nch - 1) * 64 : 64, tid);
-        float bs[8] = {};
+        BiasSums bs;
         // fp16 (always two chunks): y comes through registers, a tile ahead; this thread's pixel and 16 channels
         const int yrow = s * 64 + (tid % kGroup >> 2), yc = (tid & 3) * 16;
         uint4 yv[2];
@@ -902,33 +934,34 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
             }
         };
         if constexpr (PL > 1) load_y(0);
-        for (int n = s; n < steps; n += 2) {
-            ok = tc::warp_wait(&raw_full[n & 3], static_cast<unsigned>(n >> 2) & 1u, kCopyWaitLimitNs);
-            if (!ok) break;
-            Piece<float> piece;
-            piece.from_raw(raws + s * kRaw, walk);
-            piece.landed();
-            if (lane == 0) mbar_arrive(&raw_empty[n & 3]);
-            if (n >= 2) ok = tc::warp_wait(&empty_g[s], static_cast<unsigned>((n >> 1) - 1) & 1u, kCopyWaitLimitNs);
-            if (!ok) break;
-            piece.template store<3>(gsm + s * S::kG, 16384u, walk);
-            hand_over(&full_g[s], lane);
-            if constexpr (PL > 1) {
-                const int i = n >> 1;
-                if (i > 0) ok = tc::warp_wait(&empty_y[0], static_cast<unsigned>(i - 1) & 1u, kCopyWaitLimitNs);
+        for (int begin = s; begin < steps && ok; begin += 2 * kBiasRun) {
+            for (int n = begin, end = min(steps, begin + 2 * kBiasRun); n < end; n += 2) {
+                ok = tc::warp_wait(&raw_full[n & 3], static_cast<unsigned>(n >> 2) & 1u, kCopyWaitLimitNs);
                 if (!ok) break;
+                Piece<float> piece;
+                piece.from_raw(raws + s * kRaw, walk);
+                piece.landed();
+                if (lane == 0) mbar_arrive(&raw_empty[n & 3]);
+                if (n >= 2) ok = tc::warp_wait(&empty_g[s], static_cast<unsigned>((n >> 1) - 1) & 1u, kCopyWaitLimitNs);
+                if (!ok) break;
+                piece.template store<3>(gsm + s * S::kG, 16384u, walk);
+                hand_over(&full_g[s], lane);
+                if constexpr (PL > 1) {
+                    const int i = n >> 1;
+                    if (i > 0) ok = tc::warp_wait(&empty_y[0], static_cast<unsigned>(i - 1) & 1u, kCopyWaitLimitNs);
+                    if (!ok) break;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float f[8];
-                    unpack8(yv[q], static_cast<T*>(nullptr), f);
-                    store_split8<PL>(ysm, 16384u, yrow, (yc >> 3) + q, f);
+                    for (int q = 0; q < 2; ++q) {
+                        float f[8];
+                        unpack8(yv[q], static_cast<T*>(nullptr), f);
+                        store_split8<PL>(ysm, 16384u, yrow, (yc >> 3) + q, f);
+                    }
+                    hand_over(full_y, lane);
+                    load_y(i + 1);
                 }
-                hand_over(full_y, lane);
-                load_y(i + 1);
+                bs.add(piece.v);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e)  // rows past the tile hold zeros
-                bs[e] += (piece.v[0][e] + piece.v[1][e]) + (piece.v[2][e] + piece.v[3][e]);
+            if (begin + 2 * kBiasRun < steps) bs.flush(begin == s);
         }
         if (pbias != nullptr) {
             // once the last products have read the operand tiles (a commit covers all those before it), the
@@ -937,9 +970,11 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
             if (ok) ok = tc::warp_wait(&empty_g[end], static_cast<unsigned>((steps - 1) >> 1) & 1u, kCopyWaitLimitNs);
             float* red = reinterpret_cast<float*>(gsm);  // [thread][8]
             tc::bar_sync(2, kConv);
-            if (ok)
+            if (ok) {
+                if (s + 2 * kBiasRun < steps) bs.finish();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) red[tid * 8 + k] = bs[k];
+                for (int k = 0; k < 8; ++k) red[tid * 8 + k] = bs.run[k];
+            }
             tc::bar_sync(2, kConv);
             const int t = tid >> 3, part8 = tid & 7;
             for (int ch = 0; ch < nch; ++ch) {

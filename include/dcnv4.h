@@ -257,8 +257,10 @@ DCNV4_API int dcnv4_predictor(const void *y, const void *weight, const float *bi
  * grad_y: device fp32 [M, C]; grad_weight: device fp32 [NO, C]; grad_bias:
  * device fp32 [NO], or NULL when it is not wanted. All three are fully
  * overwritten (M == 0: the weight's and the bias's with zeros). flags as
- * dcnv4_predictor. Sums are fp32 and their order is fixed by the sizes: the
- * same bits in every run. A NaN or an infinity in y, weight or
+ * dcnv4_predictor. Sums are fp32 (grad_bias: fp64 between runs of at most 16
+ * tiles of 128 pixels, off by at most 2^-18 of sum_m |gp[m, o]| however many
+ * pixels there are) and their order is fixed by the sizes: the same bits in
+ * every run. A NaN or an infinity in y, weight or
  * grad_offset_mask (or an fp32 magnitude above 3.38e38) makes the sums it
  * enters NaN or infinite, no others. workspace: device, 256-byte aligned, at least
  * dcnv4_predictor_backward_workspace's bytes; its contents before and after
