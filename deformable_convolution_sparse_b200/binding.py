@@ -435,8 +435,9 @@ def predictor_backward(y: torch.Tensor, weight: torch.Tensor, grad_offset_mask: 
     y: [..., C]; weight: [3*G*P, C] in y's dtype; grad_offset_mask: fp32
     [..., G, 3*P], as ``backward`` returns it. Returns (grad_y [..., C],
     grad_weight [3*G*P, C], grad_bias [3*G*P]), all fp32; grad_bias is None
-    with ``with_bias=False``. The sums' order is fixed: equal calls give equal
-    bits. Asynchronous on ``stream`` (default: the current stream).
+    with ``with_bias=False``. The sums' order is fixed by the sizes, the dtype
+    and the buffers' 16-byte alignment: equal calls on equally aligned buffers
+    give equal bits. Asynchronous on ``stream`` (default: the current stream).
     """
     for t, name in ((y, "y"), (weight, "weight"), (grad_offset_mask, "grad_offset_mask")):
         _check_tensor(t, name)

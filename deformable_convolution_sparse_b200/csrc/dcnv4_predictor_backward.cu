@@ -22,8 +22,9 @@ namespace {
 
 #include "dcnv4_unit_common.inl"
 
-// Tiles, slices and walkers, from the sizes alone (and a nominal 148 SMs), so
-// that the sums' order, and with it the result's bits, are the same everywhere.
+// Tiles, slices and walkers, from the sizes alone (and a nominal 148 SMs): what
+// is left to choose the sums' order, and with it the result's bits, is dtype and
+// which buffers TMA can take (launch()).
 dcnv4::PredBwdParams make_params(int M, int C, int G, long long P, long long NO) {
     dcnv4::PredBwdParams p{};
     p.M = M; p.C = C; p.G = G; p.P = static_cast<int>(P); p.NO = static_cast<int>(NO);

@@ -259,7 +259,10 @@ DCNV4_API int dcnv4_predictor(const void *y, const void *weight, const float *bi
  * overwritten (M == 0: the weight's and the bias's with zeros). flags as
  * dcnv4_predictor. Sums are fp32 (grad_bias: fp64 between runs of at most 16
  * tiles of 128 pixels, off by at most 2^-18 of sum_m |gp[m, o]| however many
- * pixels there are) and their order is fixed by the sizes: the same bits in
+ * pixels there are) and their order is fixed by the sizes, dtype and which
+ * of the pointers lie on 16-byte boundaries (rows that TMA cannot take are read
+ * another way, and 16-bit y of few channels and slots all at once where it can
+ * take them): equal calls on equally aligned buffers give the same bits in
  * every run. A NaN or an infinity in y, weight or
  * grad_offset_mask (or an fp32 magnitude above 3.38e38) makes the sums it
  * enters NaN or infinite, no others. workspace: device, 256-byte aligned, at least
