@@ -208,11 +208,15 @@ def validate(x_ptr: int, om_ptr: int, out_ptr: int, N: int, H: int, W: int, C: i
                                          float(offset_scale), int(dtype))
 
 
+# The current stream's handle without a Stream object made for it (0.5 us against 3.3). Not among torch's documented
+# names: where it is missing, the documented ones do.
+_CURRENT_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_handle(stream) -> int:
     if stream is None:
-        if torch.cuda.is_initialized():
-            # the current stream of the current device, without making a Stream object of it
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        if _CURRENT_RAW_STREAM is not None and torch.cuda.is_initialized():
+            return _CURRENT_RAW_STREAM(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream)
 
@@ -404,7 +408,7 @@ def _launching_on(device, stream):
     """Makes ``device`` current, and ``stream`` too when one is given: outputs and workspaces then come from
     the memory pool of the stream whose kernels use them, which is what orders their reuse."""
     if stream is None:
-        return _HERE if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
+        return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     return torch.cuda.stream(stream)
