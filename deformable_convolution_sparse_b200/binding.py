@@ -213,10 +213,11 @@ def validate(x_ptr: int, om_ptr: int, out_ptr: int, N: int, H: int, W: int, C: i
 _CURRENT_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream_handle(stream) -> int:
+def _stream_handle(stream, device: int | None = None) -> int:
+    """Handle of ``stream``, or of the current stream of the current device (``device``, where the caller knows it)."""
     if stream is None:
         if _CURRENT_RAW_STREAM is not None and torch.cuda.is_initialized():
-            return _CURRENT_RAW_STREAM(torch.cuda.current_device())
+            return _CURRENT_RAW_STREAM(torch.cuda.current_device() if device is None else device)
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream)
 
@@ -466,7 +467,8 @@ def predictor_backward(y: torch.Tensor, weight: torch.Tensor, grad_offset_mask: 
         ws = torch.empty(size, dtype=torch.uint8, device=dev)
         rc = load_library().dcnv4_predictor_backward(y.data_ptr(), weight.data_ptr(), grad_offset_mask.data_ptr(),
                                           gy.data_ptr(), gw.data_ptr(), 0 if gb is None else gb.data_ptr(),
-                                          ws.data_ptr(), size, M, C, G, K, flags, dt, _stream_handle(stream))
+                                          ws.data_ptr(), size, M, C, G, K, flags, dt,
+                                          _stream_handle(stream, dev.index))
     if rc != DCNV4_OK:
         raise DCNv4Error(rc, "dcnv4_predictor_backward")
     return gy, gw, gb
@@ -503,7 +505,7 @@ def mx_quantize(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torc
         codes = _output(codes, "codes", lead + (nb * 16,), torch.uint8, x.device)
         scales = _output(scales, "scales", lead + (nb,), torch.uint8, x.device)
         rc = load_library().dcnv4_mx_quantize(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), _pixels(lead), C,
-                                              TORCH_DTYPE[x.dtype], _stream_handle(stream))
+                                              TORCH_DTYPE[x.dtype], _stream_handle(stream, x.device.index))
     if rc != DCNV4_OK:
         raise DCNv4Error(rc, "dcnv4_mx_quantize")
     return codes, scales
@@ -524,7 +526,7 @@ def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, C: int, dtype: torc
     with _launching_on(codes.device, stream):
         out = _output(out, "out", lead + (C,), dtype, codes.device)
         rc = load_library().dcnv4_mx_dequantize(codes.data_ptr(), scales.data_ptr(), out.data_ptr(), _pixels(lead), C,
-                                                TORCH_DTYPE[dtype], _stream_handle(stream))
+                                                TORCH_DTYPE[dtype], _stream_handle(stream, codes.device.index))
     if rc != DCNV4_OK:
         raise DCNv4Error(rc, "dcnv4_mx_dequantize")
     return out
@@ -558,7 +560,7 @@ def predictor_mx(y: torch.Tensor, weight_codes: torch.Tensor, weight_scales: tor
         rc = load_library().dcnv4_predictor_mx(y.data_ptr(), weight_codes.data_ptr(), weight_scales.data_ptr(), bp,
                                                out.data_ptr(), _pixels(lead), C, G, K,
                                                FLAG_REMOVE_CENTER if remove_center else 0, TORCH_DTYPE[y.dtype],
-                                               _stream_handle(stream))
+                                               _stream_handle(stream, y.device.index))
     if rc != DCNV4_OK:
         raise DCNv4Error(rc, "dcnv4_predictor_mx")
     return out
@@ -590,7 +592,7 @@ def orthogonalize(x: torch.Tensor, steps: int = 5, coefficients: tuple = (3.4445
         out = _output(out, "out", tuple(x.shape), x.dtype, x.device)
         ws = torch.empty(size, dtype=torch.uint8, device=x.device)
         rc = load_library().dcnv4_orthogonalize(x.data_ptr(), out.data_ptr(), ws.data_ptr(), size, B, R, C, int(steps),
-                                     a, b, c, float(eps), dt, _stream_handle(stream))
+                                     a, b, c, float(eps), dt, _stream_handle(stream, x.device.index))
     if rc != DCNV4_OK:
         raise DCNv4Error(rc, "dcnv4_orthogonalize")
     return out

@@ -219,14 +219,14 @@ __device__ __forceinline__ void ortho_sum4(uint32_t at, uint32_t step, float (&v
 // ring is deep, four stages, while the tiles fit the SMs once; when there are
 // more tiles than SMs, two stages leave room for two CTAs per SM (256 columns
 // of tensor memory each) whose latencies overlap. Whole iteration in fp32, 432
-// x 256: 18 matrices (144 and 252 tiles) 120 us, all products with four stages
-// 132, with two 149; 40 matrices 243 with two, 289 with four. 4 of 864 x 512
-// in bf16: 156 us (149 in one run of k).
+// x 256: 18 matrices (144 and 252 tiles) 119 us, all products with four stages
+// 134, with two 145; 40 matrices 237 with two, 295 with four. 4 of 864 x 512
+// in bf16: 154 us (147 in one run of k).
 constexpr int kGram = 0, kPoly = 1, kApply = 2, kLast = 3;
 constexpr int kOrthoEpi = 256, kOrthoThreads = 64 + kOrthoEpi;
 // The accumulators are read out, added in registers and begun anew every this
-// many 64 k: without it the truncated additions of one matrix of 809 x 840
-// brought a relative error of 1.03e-5, fp32 matrix products 6.8e-6.
+// many 64 k, so that truncation does not grow with k: one matrix of 809 x 840
+// has an error of 1.1e-6 so, 1.9e-6 without (fp32 matrix products: 2.8e-6).
 constexpr int kOrthoRun = 8;
 constexpr unsigned kOrthoStageBytes = 2u * 16384u + 2u * 8192u;
 constexpr unsigned ortho_smem(int stages) { return 1024u + stages * kOrthoStageBytes + 128u; }
@@ -457,9 +457,10 @@ ortho_product_kernel(const __grid_constant__ CUtensorMap lmap, const __grid_cons
 // one of the application (MN-major), A's as both of the polynomial, which
 // overwrites them with Q. One warp issues a product's instructions, then all
 // warps turn the accumulators into the next operand. What bounds it is the
-// chain of 3 * steps dependent products, each a few hundred cycles of tensor
-// work between two barriers: 4 matrices of 108 x 64 take 30 us (67 through the
-// kernels above), 18 of 216 x 128 72 us (85), 300 of 108 x 64 90 us (161).
+// chain of 3 * steps dependent products between two barriers each: for 108 x 64
+// 28, 16 and 12 instructions of 49 to 58 cycles, some 2,900 cycles a step of the
+// 11,000 that it takes. 4 matrices of 108 x 64 take 31 us (61 through the
+// kernels above), 18 of 216 x 128 75 us (84), 300 of 108 x 64 94 us (163).
 constexpr int kOrthoSmallThreads = 512, kOrthoSmallBlocks = 7;
 constexpr unsigned kOrthoBlock = 2u * 16384u;
 constexpr int kOrthoMaxSteps = 64;

@@ -34,9 +34,10 @@ dcnv4::PredBwdParams make_params(int M, int C, int G, long long P, long long NO)
     p.wpitch = (C + 63) / 64 * 64;
     p.groups = (p.NO + 127) / 128;
     const long long per = static_cast<long long>(p.groups) * ((C + 127) / 128);
-    // one walker, and so no launch to join partial sums, for one or two tiles: 196 pixels x 256 fp16 channels x 432
-    // slots 21.0 us against 22.2 (22.1 against 25.1 with the calls' cost on the host), x 512 x 864 22.6 against 43.2,
-    // x 64 bf16 x 108 9.5 against 8.8 (17.2 against 20.4)
+    // one walker, and so no launch to join partial sums, for one or two tiles. Measured from a graph, one walker
+    // against several: 196 pixels x 256 fp16 channels x 432 slots 21.8 us against 23.7, x 512 x 864 23.6 against 43.9;
+    // x 64 bf16 x 108 10.1 against 9.1, x 320 fp32 x 192 22.2 against 21.0 (less than the launch that the host is
+    // spared). 257 pixels of the four: 26.9 against 24.1, 28.5 against 45.0, 12.6 against 9.3, 28.0 against 21.2.
     p.walkers = p.tiles <= 2 ? 1 : static_cast<int>(std::max<long long>(1, std::min<long long>(p.tiles, 148 / per)));
     return p;
 }
@@ -129,7 +130,8 @@ int launch(const void* y, const void* w, const float* grec, float* gy, float* gw
     p.direct = p.walkers == 1 && aligned(gw, 16) ? 1 : 0;
     float *part = p.direct ? gw : reinterpret_cast<float*>(ws + l.part);
     float *pbias = !gb || p.direct ? gb : reinterpret_cast<float*>(ws + l.pbias);
-    // TMA wants rows of whole 16-byte units on 16-byte boundaries
+    // TMA wants rows of whole 16-byte units on 16-byte boundaries (200,704 pixels x 64 bf16 channels with 81 slots, read
+    // directly, take 95 us, with 108 by TMA 42 in one pass or 71 in two)
     const bool raw_g = p.NO % 4 == 0 && aligned(grec, 16), raw_w = raw_g && p.C * E % 16 == 0 && aligned(y, 16);
     p.tma_out = p.C % 4 == 0 && aligned(gy, 16) ? 1 : 0;
     CUtensorMap wmap{}, gmap{}, ymap{}, omap{};

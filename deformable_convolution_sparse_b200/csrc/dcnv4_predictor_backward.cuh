@@ -9,7 +9,8 @@
 //
 // Precision on the tensor cores. An fp32 value is the exact sum of three bf16
 // values, h = bf16(v), m = bf16(v - h), l = v - h - m (24 bits in three times
-// 8, whatever the magnitude); fp16 takes two and bf16 one. A product of two
+// 8; below 2^-110 l falls under bf16's smallest number, and the sum is off by at
+// most 2^-134); fp16 takes two and bf16 one. A product of two
 // such sums keeps the pairs whose orders add to at most 2 (the others are
 // below 2^-26 of it): 3 tensor-core products for bf16 operands, 5 for fp16, 6
 // for fp32, each exact, summed in fp32. The tensor cores' additions truncate,
@@ -25,9 +26,10 @@
 // of raw tiles a CTA can keep in flight beside its operand planes (such a ring
 // alone, without any work, reads g at 3.0 to 3.5 TB/s), and for three planes of
 // y the products themselves. Measured on B200, everything together: 200,704
-// pixels x 64 channels x 108 slots in bf16 41 us (71 by the two kernels), in
-// fp16 59 (87), replayed from a graph; 26,047 x 320 fp32 x 192 slots 101 us,
-// 196 x 256 fp16 x 432 slots 21 us.
+// pixels x 64 channels x 108 slots in bf16 42 us (71 by the two kernels), in
+// fp16 59 (87), 129,032 x 128 x 216 slots in bf16 94, 26,047 x 320 fp32 x 192
+// slots 100, 196 x 256 fp16 x 432 slots 22, all replayed from a graph. Rows that
+// TMA cannot take, 200,704 x 64 in bf16 with 27 slots 78, with 54 87, with 81 95.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -2,9 +2,11 @@
 // each (dcnv4_mx.cu, dcnv4_predictor_backward.cu, dcnv4_orthogonalize.cu).
 // Included inside their anonymous namespace, after dcnv4_host_common.inl.
 
-// Launches with programmatic stream serialisation: every thread of `kern`
-// executes griddepcontrol.wait before its first global access (DCNV4_PDL=0:
-// plain serialisation).
+// Launches with programmatic stream serialisation (DCNV4_PDL=0: plain): every
+// thread of `kern` executes griddepcontrol.wait before its first global access.
+// The one exception is pred_grad_w_kernel, which waits at its end: the launch
+// directly before it has to be pred_grad_y_kernel, which writes nothing that it
+// touches, and whose CTAs let it start only after a wait of their own.
 template <typename... KA, typename... A>
 int launch_chained(void (*kern)(KA...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
     cudaLaunchConfig_t cfg{};
