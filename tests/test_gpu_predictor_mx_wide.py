@@ -64,3 +64,26 @@ def test_predictor_mx_over_many_tiles(case, dtype, cuda_device):
                              torch.tensor(wq[1]).to(cuda_device), None if b is None else b.to(cuda_device), G=G, K=K,
                              remove_center=rc)
     assert torch.equal(again, out[part])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("ly,lw", [(-126, 0), (-126, -3), (-60, -66), (-126, 120), (120, -126), (126, 0), (-100, -40)])
+def test_predictor_mx_at_the_ends_of_the_scales(ly, lw, dtype, cuda_device):
+    """Activations of 2^ly and weights of 2^lw: sums down to fp32's subnormals and up to its largest number. (Each sum
+    is off by up to a unit of the subnormals, 2^-149, too.)"""
+    M, C, G = 300, 96, 2
+    gen = torch.Generator().manual_seed(ly + lw)
+    y = (torch.randn(M, C, generator=gen) * 0.3 * 2.0 ** ly).to(TD[dtype])
+    w = torch.randn(54, C, generator=gen) * 0.3 * 2.0 ** lw
+    codes, scales = dcn.mx_quantize(w.to(cuda_device))
+    out = dcn.predictor_mx(y.to(cuda_device), codes, scales, None, G=G, K=3)
+    q = ow.mx_values(*ow.mx_quantize(y.double().numpy()), C)
+    wv = ow.mx_values(ow.mx_unpack(codes.cpu().numpy()), scales.cpu().numpy(), C)
+    ref = oracle.dcnv4_predictor(q, wv, None, G=G, P=9).reshape(M, -1)
+    mag = oracle.dcnv4_predictor(np.abs(q), np.abs(wv), None, G=G, P=9).reshape(M, -1)
+    got = out.double().cpu().numpy().reshape(M, -1)
+    assert not np.isnan(got).any()
+    tol = torch.finfo(TD[dtype]).eps / 2 * np.abs(ref) * (1 + 2.0 ** -10) + TINY[dtype] + (C + 2) * 2.0 ** -23 * mag + 2.0 ** -149
+    inside = np.abs(ref) + tol < torch.finfo(TD[dtype]).max
+    assert np.all((np.abs(got - ref) <= tol)[inside])
+    assert np.all(np.abs(got[np.abs(ref) > 3.5e38]) > 3.3e38)   # past the end: infinite, or the largest number
