@@ -83,6 +83,9 @@ int launch_grad_y(const CUtensorMap& wmap, const CUtensorMap& gmap, const CUtens
                           wmap, gmap, omap, grec, gy, p);
 }
 
+// More tiles of pixels per walker than the bias's sums take in fp32 (the first walker has the most).
+bool long_sums(const dcnv4::PredBwdParams& p) { return (p.tiles + p.walkers - 1) / p.walkers > dcnv4::kBiasRun; }
+
 template <typename T, bool RAW>
 int launch_grad_w(const CUtensorMap& gmap, const CUtensorMap& ymap, const float* grec, const T* y, float* part,
                   float* pbias, dcnv4::PredBwdParams p, cudaStream_t s) {
@@ -91,7 +94,7 @@ int launch_grad_w(const CUtensorMap& gmap, const CUtensorMap& ymap, const float*
     p.ystep = p.C > 64 ? 32768u : 16384u;
     p.raws = S::raws(p.ystep);
     const unsigned smem = S::smem(p.ystep);
-    auto kern = dcnv4::pred_grad_w_kernel<T, RAW>;
+    auto kern = long_sums(p) ? dcnv4::pred_grad_w_kernel<T, RAW, true> : dcnv4::pred_grad_w_kernel<T, RAW, false>;
     if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(std::max(S::smem(16384u), S::smem(32768u)))) !=
         cudaSuccess)
         return DCNV4_ERR_LAUNCH;
@@ -106,7 +109,7 @@ int launch_grad_both(const CUtensorMap& gmap, const CUtensorMap& ymap, const CUt
                      float* gy, float* part, float* pbias, const dcnv4::PredBwdParams& p, cudaStream_t s) {
     constexpr unsigned smem = dcnv4::GradBothShape<T>::kSmem;
     static_assert(smem <= kTileSmemLimit, "the stages do not fit");
-    auto kern = dcnv4::pred_grad_both_kernel<T>;
+    auto kern = long_sums(p) ? dcnv4::pred_grad_both_kernel<T, true> : dcnv4::pred_grad_both_kernel<T, false>;
     if (smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess) return DCNV4_ERR_LAUNCH;
     return launch_chained(kern, dim3(static_cast<unsigned>(p.walkers)), dcnv4::kGradYThreads, smem, s, gmap, ymap, omap, y, w,
                           gy, part, pbias, p);
@@ -131,7 +134,7 @@ int launch(const void* y, const void* w, const float* grec, float* gy, float* gw
     float *part = p.direct ? gw : reinterpret_cast<float*>(ws + l.part);
     float *pbias = !gb || p.direct ? gb : reinterpret_cast<float*>(ws + l.pbias);
     // TMA wants rows of whole 16-byte units on 16-byte boundaries (200,704 pixels x 64 bf16 channels with 81 slots, read
-    // directly, take 95 us, with 108 by TMA 42 in one pass or 71 in two)
+    // directly, take 93 us, with 108 by TMA 41 in one pass or 71 in two)
     const bool raw_g = p.NO % 4 == 0 && aligned(grec, 16), raw_w = raw_g && p.C * E % 16 == 0 && aligned(y, 16);
     p.tma_out = p.C % 4 == 0 && aligned(gy, 16) ? 1 : 0;
     CUtensorMap wmap{}, gmap{}, ymap{}, omap{};

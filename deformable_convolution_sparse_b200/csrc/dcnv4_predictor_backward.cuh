@@ -26,10 +26,10 @@
 // of raw tiles a CTA can keep in flight beside its operand planes (such a ring
 // alone, without any work, reads g at 3.0 to 3.5 TB/s), and for three planes of
 // y the products themselves. Measured on B200, everything together: 200,704
-// pixels x 64 channels x 108 slots in bf16 42 us (71 by the two kernels), in
-// fp16 59 (87), 129,032 x 128 x 216 slots in bf16 94, 26,047 x 320 fp32 x 192
-// slots 100, 196 x 256 fp16 x 432 slots 22, all replayed from a graph. Rows that
-// TMA cannot take, 200,704 x 64 in bf16 with 27 slots 78, with 54 87, with 81 95.
+// pixels x 64 channels x 108 slots in bf16 41 us (71 by the two kernels), in
+// fp16 59 (87), 129,032 x 128 x 216 slots in bf16 93, 26,047 x 320 fp32 x 192
+// slots 100, 196 x 256 fp16 x 432 slots 21, all replayed from a graph. Rows that
+// TMA cannot take, 200,704 x 64 in bf16 with 27 slots 71, with 54 83, with 81 93.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -226,30 +226,38 @@ struct Piece {
     }
 };
 // A converting thread's sums of g for the bias, eight slots: fp32 over runs of
-// at most kBiasRun chunks, fp64 from there on, so that the error does not grow
+// at most kBiasRun tiles, fp64 from there on, so that the error does not grow
 // with the number of pixels (9,000,001 equal values in one fp32 sum per thread:
 // 4e-6 of the sum). The fp64 sums are kept in memory (volatile: registers are
-// what these threads have least of) and touched once a run: some 2 % of the
-// time; fp64 in the sums over the threads and in the join too cost 10 %.
+// what these threads have least of) and touched once a run. Even unused they
+// cost 0.4 to 2.5 us, so calls whose CTAs have one run at most (303,104 pixels
+// in the one-pass kernel) take builds without them (not LONG); fp64 in the sums
+// over the threads and in the join too cost 3 to 6 us.
 constexpr int kBiasRun = 16;
+template <bool LONG>
 struct BiasSums {
+    static constexpr int kRun = LONG ? kBiasRun : 1 << 29;  // tiles
     float run[8] = {};
-    volatile double total[8];
+    volatile double total[LONG ? 8 : 1];
     __device__ __forceinline__ void add(const float (&v)[kPieces][8]) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)  // rows past the tile hold zeros
             run[e] += (v[0][e] + v[1][e]) + (v[2][e] + v[3][e]);
     }
     __device__ __forceinline__ void flush(bool first) {
+        if constexpr (LONG) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            total[e] = first ? static_cast<double>(run[e]) : total[e] + static_cast<double>(run[e]);
-            run[e] = 0.f;
+            for (int e = 0; e < 8; ++e) {
+                total[e] = first ? static_cast<double>(run[e]) : total[e] + static_cast<double>(run[e]);
+                run[e] = 0.f;
+            }
         }
     }
     __device__ __forceinline__ void finish() {
+        if constexpr (LONG) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) run[e] = static_cast<float>(total[e] + static_cast<double>(run[e]));
+            for (int e = 0; e < 8; ++e) run[e] = static_cast<float>(total[e] + static_cast<double>(run[e]));
+        }
     }
 };
 // the operand tiles this warp's threads wrote, handed over (one arrival per warp)
@@ -528,7 +536,7 @@ struct GradWShape {
 };
 constexpr int kGradWThreads = kConv + 128;
 
-template <typename T, bool RAW>
+template <typename T, bool RAW, bool LONG>
 __global__ void __launch_bounds__(kGradWThreads, 1)
 pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CUtensorMap ymap,
                    const float* __restrict__ grec, const T* __restrict__ y, float* __restrict__ part,
@@ -586,7 +594,8 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
 
     if (warp < 16) {
         const bool sums = c0 == 0 && pbias != nullptr;
-        BiasSums bs[2];                   // of each chunk
+        using Sums = BiasSums<LONG>;
+        Sums bs[2];                       // of each chunk
         const ChunkWalk walk0(p.NO - g0, tid), walk1(nch == 2 ? p.NO - g0 - 64 : 64, tid);
         const ChunkWalk ywalk0(p.C - c0, tid), ywalk1(wide ? p.C - c0 - 64 : 64, tid);
         const int group = warp >> 3;
@@ -605,8 +614,8 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
             piece.landed();
             if (lane == 0) mbar_arrive(&raw_empty[k & 3]);
         };
-        for (int begin = 0; begin < mine && ok; begin += kBiasRun) {
-            for (int i = begin, end = min(mine, begin + kBiasRun); i < end && ok; ++i) {
+        for (int begin = 0; begin < mine && ok; begin += Sums::kRun) {
+            for (int i = begin, end = min(mine, begin + Sums::kRun); i < end && ok; ++i) {
                 // With one stage of y, both groups wait for its release once a tile, before their first store. A group
                 // that writes y (or a stage of g) in every other tile only would otherwise miss a phase of the barrier
                 // and take the one before for the one it needs.
@@ -656,7 +665,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
                     next();
                 }
             }
-            if (sums && begin + kBiasRun < mine) {
+            if (sums && begin + Sums::kRun < mine) {
                 bs[0].flush(begin == 0);
                 bs[1].flush(begin == 0);
             }
@@ -676,7 +685,7 @@ pred_grad_w_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_consta
                 const int ng = ch ? walk1.ng : walk0.ng, rows = ch ? walk1.rows : walk0.rows;
                 tc::bar_sync(2, kConv);
                 if (ok) {
-                    if (mine > kBiasRun) bs[ch].finish();
+                    if (mine > Sums::kRun) bs[ch].finish();
 #pragma unroll
                     for (int k = 0; k < 8; ++k) red[tid * 8 + k] = bs[ch].run[k];
                 }
@@ -850,7 +859,7 @@ struct GradBothShape {
     static constexpr unsigned kSmem = 1024u + 2 * kG + kYStages * kY + kW + kOut + kRaws * kRaw + 256u;
 };
 
-template <typename T>
+template <typename T, bool LONG>
 __global__ void __launch_bounds__(kGradYThreads, 1)
 pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CUtensorMap ymap,
                       const __grid_constant__ CUtensorMap omap, const T* __restrict__ y, const T* __restrict__ w,
@@ -923,7 +932,8 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
         const int s = warp >> 3;
         const bool last = nch == 1 || s == 1;
         const ChunkWalk walk(last ? p.NO - (nch - 1) * 64 : 64, tid);
-        BiasSums bs;
+        using Sums = BiasSums<LONG>;
+        Sums bs;
         // fp16 (always two chunks): y comes through registers, a tile ahead; this thread's pixel and 16 channels
         const int yrow = s * 64 + (tid % kGroup >> 2), yc = (tid & 3) * 16;
         uint4 yv[2];
@@ -936,8 +946,8 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
             }
         };
         if constexpr (PL > 1) load_y(0);
-        for (int begin = s; begin < steps && ok; begin += 2 * kBiasRun) {
-            for (int n = begin, end = min(steps, begin + 2 * kBiasRun); n < end; n += 2) {
+        for (int begin = s; begin < steps && ok; begin += 2 * Sums::kRun) {
+            for (int n = begin, end = min(steps, begin + 2 * Sums::kRun); n < end; n += 2) {
                 ok = tc::warp_wait(&raw_full[n & 3], static_cast<unsigned>(n >> 2) & 1u, kCopyWaitLimitNs);
                 if (!ok) break;
                 Piece<float> piece;
@@ -963,7 +973,7 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
                 }
                 bs.add(piece.v);
             }
-            if (begin + 2 * kBiasRun < steps) bs.flush(begin == s);
+            if (begin + 2 * Sums::kRun < steps) bs.flush(begin == s);
         }
         if (pbias != nullptr) {
             // once the last products have read the operand tiles (a commit covers all those before it), the
@@ -973,7 +983,7 @@ pred_grad_both_kernel(const __grid_constant__ CUtensorMap gmap, const __grid_con
             float* red = reinterpret_cast<float*>(gsm);  // [thread][8]
             tc::bar_sync(2, kConv);
             if (ok) {
-                if (s + 2 * kBiasRun < steps) bs.finish();
+                if (s + 2 * Sums::kRun < steps) bs.finish();
 #pragma unroll
                 for (int k = 0; k < 8; ++k) red[tid * 8 + k] = bs.run[k];
             }
