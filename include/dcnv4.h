@@ -333,8 +333,8 @@ DCNV4_API int dcnv4_predictor_mx(const void *y, const uint8_t *weight_codes, con
  * device, dtype, [B, R, C], fully overwritten. Whatever dtype is, sums are
  * fp32, the step's a X is added in fp32, and between steps an entry of X, A
  * and b A + c A A is held as two fp16 values: to one unit of fp32's last
- * place, or to 2^-38 of its matrix's norm where that is more. The result is
- * rounded once. A matrix of zeros
+ * place, or, below 2^-16 of the largest entry that the iteration's bounds
+ * allow, to 2^-39 of that. The result is rounded once. A matrix of zeros
  * gives zeros; a NaN or an infinity makes its matrix NaN. steps: 0..64 (0:
  * only the division). Refused with DCNV4_ERR_COEFFICIENTS: coefficients or
  * eps that are not finite, eps <= 0, and coefficients that within `steps`
